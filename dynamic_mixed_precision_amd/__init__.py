@@ -29,6 +29,7 @@ FP4_BF16_DEQUANT = 0
 FP4_SCALED_MFMA = 1
 OP_GAMMA, OP_QUANT_NVFP4, OP_TDC, OP_PREP_WEIGHT, OP_OUTLIER, OP_GEMM_AMAX, OP_GEMM = 0, 1, 2, 3, 4, 5, 6
 OP_GEMM_W4 = 7
+OP_GRAD_NORM = 8
 
 EXPORTS = ("dmpq_last_error", "dmpq_version", "dmpq_workspace_bytes", "dmpq_gamma_sums",
            "dmpq_gate_and_route", "dmpq_hadamard_quant_int8", "dmpq_hadamard_quant_nvfp4",
@@ -37,7 +38,10 @@ EXPORTS = ("dmpq_last_error", "dmpq_version", "dmpq_workspace_bytes", "dmpq_gamm
            "dmpq_outlier_count", "dmpq_pdr_decide", "dmpq_gemm_bf16", "dmpq_qgemm_int8_ex",
            "dmpq_qgemm_nvfp4_ex", "dmpq_gemm_bf16_ex", "dmpq_selftest_codec",
            "dmpq_hadamard_quant_nvfp4_noalloc", "dmpq_qgemm_int8_from_nvfp4",
-           "dmpq_hadamard_quant_int8_w8")
+           "dmpq_hadamard_quant_int8_w8", "dmpq_lora_shrink", "dmpq_lora_forward",
+           "dmpq_gemm_bf16_lora", "dmpq_qgemm_int8_lora", "dmpq_qgemm_nvfp4_lora",
+           "dmpq_lora_backward_bytes", "dmpq_lora_backward", "dmpq_adamw_table_bytes",
+           "dmpq_adamw_table", "dmpq_grad_norm", "dmpq_adamw_step")
 
 
 class DmpqError(RuntimeError):
@@ -50,6 +54,12 @@ class TdcState(C.Structure):
     """Mirror of dmpq_tdc_state."""
     _fields_ = [("n_refresh", C.c_int64), ("d", C.c_double), ("acc", C.c_double),
                 ("delta_valid", C.c_int32), ("gamma_valid", C.c_int32), ("gamma", C.c_double)]
+
+
+class AdamwTensor(C.Structure):
+    """Mirror of dmpq_adamw_tensor."""
+    _fields_ = [("p", C.c_void_p), ("g", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
+                ("ms", C.c_void_p), ("vs", C.c_void_p), ("copy", C.c_void_p), ("n", C.c_int64)]
 
 
 class TdcParams(C.Structure):
@@ -102,6 +112,18 @@ def _declare(L):
         "dmpq_hadamard_quant_nvfp4_noalloc": (i32, [vp, vp, i64, i64, i32, vp, vp, vp]),
         "dmpq_qgemm_int8_from_nvfp4": (i32, [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, i32, vp,
                                              C.c_size_t]),
+        "dmpq_lora_shrink": (i32, [vp] * 6 + [i64] * 5 + [vp]),
+        "dmpq_lora_forward": (i32, [vp] * 9 + [i64] * 6 + [i32, vp, vp]),
+        "dmpq_gemm_bf16_lora": (i32, [vp] * 9 + [i64] * 6 + [i32, vp, i32, vp, C.c_size_t]),
+        "dmpq_qgemm_int8_lora": (i32, [vp] * 11 + [i64] * 6 + [i32, vp, i32, vp, C.c_size_t]),
+        "dmpq_qgemm_nvfp4_lora": (i32, [vp] * 13 + [i64] * 6 + [i32, vp, i32, vp, C.c_size_t]),
+        "dmpq_lora_backward_bytes": (C.c_size_t, [i64] * 6),
+        "dmpq_lora_backward": (i32, [vp] * 11 + [i64] * 6 + [vp, vp, vp, vp, C.c_size_t]),
+        "dmpq_adamw_table_bytes": (C.c_size_t, [C.POINTER(AdamwTensor), i64]),
+        "dmpq_adamw_table": (i32, [C.POINTER(AdamwTensor), i64, i32, i32, i32, vp, C.c_size_t,
+                                   C.POINTER(C.c_int64)]),
+        "dmpq_grad_norm": (i32, [vp, vp, i64, i64, i32, vp, vp, C.c_size_t]),
+        "dmpq_adamw_step": (i32, [vp, vp, i64, i64, i32, i32, i32, f64, f64, f64, f64, f64, i64, vp, f64]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -434,3 +456,193 @@ def selftest_codec(codec: int, lo: int, hi: int, stats, stream=None) -> None:
         _need(stats, "stats", 12 * (128 if codec == CODEC_E4M3 else 16), 4)
     _check(lib().dmpq_selftest_codec(_stream(stream), codec, lo, hi, _ptr(stats)),
            "dmpq_selftest_codec")
+
+
+# ---- low-rank adapters beside a linear ----------------------------------------
+
+def _need_lora(x_rows: int, a, b, rank, scale, seg_start, seg_adapter, t, K=None, N=None):
+    """The pool and batch that every adapter call shares; returns (R, S, n)."""
+    pool = a if a is not None else b
+    if len(pool.shape) != 3:
+        raise ValueError(f"the adapter pool has shape {tuple(pool.shape)}, needs 3 dimensions")
+    n = pool.shape[0]
+    R = a.shape[1] if a is not None else b.shape[2]
+    if a is not None:
+        _need(a, "a", 2 * n * R * K, 2)
+        if tuple(a.shape) != (n, R, K):
+            raise ValueError(f"a has shape {tuple(a.shape)}, needs {(n, R, K)}")
+    if b is not None:
+        _need(b, "b", 2 * n * N * R, 2)
+        if tuple(b.shape) != (n, N, R):
+            raise ValueError(f"b has shape {tuple(b.shape)}, needs {(n, N, R)}")
+    _need(rank, "rank", 4 * n, 4)
+    if scale is not None:
+        _need(scale, "scale", 4 * n, 4)
+    S = seg_start.numel() - 1
+    if S < 0:
+        raise ValueError("seg_start needs at least one entry")
+    _need(seg_start, "seg_start", 4 * (S + 1), 4)
+    _need(seg_adapter, "seg_adapter", 4 * S, 4)
+    _need(t, "t", 4 * x_rows * R, 4)
+    return R, S, n
+
+
+def new_lora_workspace(M: int, N: int, K: int, R: int, S: int, n_adapters: int, device="cuda"):
+    """Workspace tensor for lora_backward."""
+    import torch
+    return torch.empty(int(lib().dmpq_lora_backward_bytes(M, N, K, R, S, n_adapters)), dtype=torch.uint8,
+                       device=device)
+
+
+def lora_shrink(x, a, rank, seg_start, seg_adapter, t, stream=None) -> None:
+    """t [M, R] fp32 = x a^T, each row through the adapter of its request."""
+    M, K = x.shape
+    _need(x, "x", 2 * M * K, 2)
+    R, S, n = _need_lora(M, a, None, rank, None, seg_start, seg_adapter, t, K=K)
+    _check(lib().dmpq_lora_shrink(_stream(stream), _ptr(x), _ptr(a), _ptr(rank), _ptr(seg_start),
+                                  _ptr(seg_adapter), M, K, R, S, n, _ptr(t)), "dmpq_lora_shrink")
+
+
+def lora_forward(x, base, a, b, rank, scale, seg_start, seg_adapter, t, y, out_dtype: int = OUT_BF16,
+                 stream=None) -> None:
+    """t as lora_shrink, and y = base + scale * t b^T (base may be y, or None for zeros)."""
+    M, K = x.shape
+    N = b.shape[1]
+    _need(x, "x", 2 * M * K, 2)
+    R, S, n = _need_lora(M, a, b, rank, scale, seg_start, seg_adapter, t, K=K, N=N)
+    _need_out(y, M, N, out_dtype)
+    if base is not None:
+        _need_out(base, M, N, out_dtype)
+    _check(lib().dmpq_lora_forward(_stream(stream), _ptr(x), _ptr(base), _ptr(a), _ptr(b), _ptr(rank),
+                                   _ptr(scale), _ptr(seg_start), _ptr(seg_adapter), M, N, K, R, S, n,
+                                   out_dtype, _ptr(t), _ptr(y)), "dmpq_lora_forward")
+
+
+def gemm_bf16_lora(x, w, t, b, rank, scale, seg_start, seg_adapter, y, epilogue: int = 0, ws=None,
+                   out_dtype: int = OUT_BF16, stream=None) -> None:
+    """gemm_bf16_ex with the adapters' scale * t b^T added in its epilogue."""
+    M, N, K = _need_bf16_gemm(x, w, y, out_dtype)
+    R, S, n = _need_lora(M, None, b, rank, scale, seg_start, seg_adapter, t, N=N)
+    _check(lib().dmpq_gemm_bf16_lora(_stream(stream), _ptr(x), _ptr(w), _ptr(t), _ptr(b), _ptr(rank),
+                                     _ptr(scale), _ptr(seg_start), _ptr(seg_adapter), M, N, K, R, S, n,
+                                     out_dtype, _ptr(y), epilogue, *_ws(ws)), "dmpq_gemm_bf16_lora")
+
+
+def qgemm_int8_lora(qa, sa, qw, sw, t, b, rank, scale, seg_start, seg_adapter, y, epilogue: int = 0,
+                    ws=None, out_dtype: int = OUT_BF16, stream=None) -> None:
+    """qgemm_int8_ex with the adapters' scale * t b^T added in its epilogue."""
+    M, N, K = _need_int8_gemm(qa, sa, qw, sw, y, out_dtype)
+    R, S, n = _need_lora(M, None, b, rank, scale, seg_start, seg_adapter, t, N=N)
+    _check(lib().dmpq_qgemm_int8_lora(_stream(stream), _ptr(qa), _ptr(sa), _ptr(qw), _ptr(sw), _ptr(t),
+                                      _ptr(b), _ptr(rank), _ptr(scale), _ptr(seg_start), _ptr(seg_adapter),
+                                      M, N, K, R, S, n, out_dtype, _ptr(y), epilogue, *_ws(ws)),
+           "dmpq_qgemm_int8_lora")
+
+
+def qgemm_nvfp4_lora(ca, sa, ga, cw, sw, gw, t, b, rank, scale, seg_start, seg_adapter, y,
+                     epilogue: int = 0, ws=None, out_dtype: int = OUT_BF16, stream=None) -> None:
+    """qgemm_nvfp4_ex with the adapters' scale * t b^T added in its epilogue."""
+    M, N, K = _need_nvfp4_gemm(ca, sa, ga, cw, sw, gw, y, out_dtype)
+    R, S, n = _need_lora(M, None, b, rank, scale, seg_start, seg_adapter, t, N=N)
+    _check(lib().dmpq_qgemm_nvfp4_lora(_stream(stream), _ptr(ca), _ptr(sa), _ptr(ga), _ptr(cw), _ptr(sw),
+                                       _ptr(gw), _ptr(t), _ptr(b), _ptr(rank), _ptr(scale),
+                                       _ptr(seg_start), _ptr(seg_adapter), M, N, K, R, S, n, out_dtype,
+                                       _ptr(y), epilogue, *_ws(ws)), "dmpq_qgemm_nvfp4_lora")
+
+
+def lora_backward(dy, x, t, a, b, rank, scale, seg_start, seg_adapter, dx_base, dx, da, db, ws,
+                  stream=None) -> None:
+    """dx = dx_base + scale dy b a, da [n, R, K] and db [n, N, R] fp32 (dx_base
+    may be dx, or None for zeros; dx None: not computed)."""
+    M, K = x.shape
+    N = b.shape[1]
+    _need(x, "x", 2 * M * K, 2)
+    _need(dy, "dy", 2 * M * N, 2)
+    R, S, n = _need_lora(M, a, b, rank, scale, seg_start, seg_adapter, t, K=K, N=N)
+    for g, name in ((dx_base, "dx_base"), (dx, "dx")):
+        if g is not None:
+            _need(g, name, 2 * M * K, 2)
+    _need(da, "da", 4 * n * R * K, 4)
+    _need(db, "db", 4 * n * N * R, 4)
+    _check(lib().dmpq_lora_backward(_stream(stream), _ptr(dy), _ptr(x), _ptr(t), _ptr(a), _ptr(b),
+                                    _ptr(rank), _ptr(scale), _ptr(seg_start), _ptr(seg_adapter),
+                                    _ptr(dx_base), M, N, K, R, S, n, _ptr(dx), _ptr(da), _ptr(db),
+                                    *_ws(ws)), "dmpq_lora_backward")
+
+
+# ---- AdamW over many tensors ----------------------------------------------------
+
+class AdamwTable:
+    """The places of the tensors that one adamw_step call updates.  Holds
+    references to them: their memory must not move while the table is used."""
+
+    def __init__(self, table, n: int, chunks: int, p_dtype: int, g_dtype: int, bits: int, keep):
+        self.table, self.n, self.chunks = table, n, chunks
+        self.p_dtype, self.g_dtype, self.bits = p_dtype, g_dtype, bits
+        self._keep = keep
+
+
+def adamw_table(params, grads, m, v, m_scales=None, v_scales=None, copies=None) -> AdamwTable:
+    """Table of the given lists of tensors, one entry each: params and grads
+    fp32 or bf16 (one type per list), states m and v fp32, or 8-bit codes with
+    m_scales and v_scales (fp32, one per 256 values); copies: bf16 copies of
+    the new params, or None."""
+    import torch
+    k = len(params)
+    eight = m_scales is not None
+    lists = [params, grads, m, v, m_scales if eight else [None] * k, v_scales if eight else [None] * k,
+             copies if copies is not None else [None] * k]
+    if any(x is None or len(x) != k for x in lists):
+        raise ValueError("adamw_table needs lists of the same length")
+    p_dtype = OUT_BF16 if _one_size(params, "params") == 2 else OUT_F32
+    g_dtype = OUT_BF16 if _one_size(grads, "grads") == 2 else OUT_F32
+    rows = (AdamwTensor * max(1, k))()
+    for i, (p, g, mi, vi, ms, vs, c) in enumerate(zip(*lists)):
+        n = p.numel()
+        blocks = (n + 255) // 256
+        _need(g, "grad", n * g.element_size())
+        for s, name in ((mi, "m"), (vi, "v")):
+            _need(s, name, n * (1 if eight else 4), 1 if eight else 4)
+        if eight:
+            _need(ms, "m_scales", 4 * blocks, 4)
+            _need(vs, "v_scales", 4 * blocks, 4)
+        if c is not None:
+            _need(c, "copy", 2 * n, 2)
+        for f, q in (("p", p), ("g", g), ("m", mi), ("v", vi), ("ms", ms), ("vs", vs), ("copy", c)):
+            setattr(rows[i], f, _ptr(q))
+        rows[i].n = n
+    nbytes = int(lib().dmpq_adamw_table_bytes(rows, k))
+    host = torch.empty(max(nbytes, 16), dtype=torch.uint8)
+    chunks = C.c_int64(0)
+    bits = 8 if eight else 32
+    _check(lib().dmpq_adamw_table(rows, k, p_dtype, g_dtype, bits, host.data_ptr(), nbytes,
+                                  C.byref(chunks)), "dmpq_adamw_table")
+    device = params[0].device if k else "cuda"
+    return AdamwTable(host.to(device), k, chunks.value, p_dtype, g_dtype, bits, lists)
+
+
+def _one_size(ts, name: str) -> int:
+    sizes = {t.element_size() for t in ts} or {4}
+    if len(sizes) != 1 or not sizes <= {2, 4}:
+        raise ValueError(f"{name} must all be fp32 or all bf16")
+    return sizes.pop()
+
+
+def grad_norm(table: AdamwTable, norm, ws, stream=None) -> None:
+    """norm (fp64[1]) = the L2 norm of all gradients of the table."""
+    _need(norm, "norm", 8, 8)
+    _check(lib().dmpq_grad_norm(_stream(stream), _ptr(table.table), table.n, table.chunks, table.g_dtype,
+                                _ptr(norm), *_ws(ws)), "dmpq_grad_norm")
+
+
+def adamw_step(table: AdamwTable, lr: float, beta1: float = 0.9, beta2: float = 0.999,
+               eps: float = 1e-8, weight_decay: float = 0.01, step: int = 1, norm=None,
+               max_norm: float = 0.0, stream=None) -> None:
+    """One AdamW step of every tensor of the table, in place.  norm: the
+    gradients' norm from grad_norm, for clipping to max_norm (> 0) and for
+    leaving out a step whose norm is not finite."""
+    if norm is not None:
+        _need(norm, "norm", 8, 8)
+    _check(lib().dmpq_adamw_step(_stream(stream), _ptr(table.table), table.n, table.chunks, table.p_dtype,
+                                 table.g_dtype, table.bits, lr, beta1, beta2, eps, weight_decay, int(step),
+                                 _ptr(norm), max_norm), "dmpq_adamw_step")

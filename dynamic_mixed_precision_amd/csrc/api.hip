@@ -164,7 +164,8 @@ size_t dmpq_workspace_bytes(int op, int64_t M, int64_t K) {
         case DMPQ_OP_QUANT_NVFP4:
         case DMPQ_OP_TDC:
         case DMPQ_OP_PREP_WEIGHT:
-        case DMPQ_OP_OUTLIER: return kWsBytes;
+        case DMPQ_OP_OUTLIER:
+        case DMPQ_OP_GRAD_NORM: return kWsBytes;
     }
     return 0;
 }
@@ -519,6 +520,295 @@ dmpq_status dmpq_selftest_codec(hipStream_t stream, int codec, uint32_t lo, uint
                     __func__, lo, hi);
     REQUIRE_PTR(d_stats);
     return hip_status(launch_codec_stats(stream, codec, lo, hi, d_stats), __func__);
+}
+
+// ---- low-rank adapters ------------------------------------------------------
+
+// The shapes and pointers that every adapter call shares; fills `out`.
+// scaled: the call reads the adapters' scales.
+static dmpq_status check_lora(const char *fn, int64_t M, int64_t N, int64_t K, int64_t R, int64_t S,
+                              int64_t n_adapters, const int32_t *rank, const float *scale, bool scaled,
+                              const int32_t *seg_start, const int32_t *seg_adapter, LoraBatch *out) {
+    if (M < 0 || N < 0 || S < 0 || n_adapters < 0)
+        return fail(DMPQ_ERR_BAD_SHAPE, "%s: M = %lld, N = %lld, S = %lld, n_adapters = %lld must be >= 0", fn,
+                    (long long)M, (long long)N, (long long)S, (long long)n_adapters);
+    if (R <= 0 || R % 16 != 0)
+        return fail(DMPQ_ERR_BAD_SHAPE, "%s: R = %lld must be a positive multiple of 16", fn, (long long)R);
+    if (dmpq_status s = check_k(fn, K)) return s;
+    if (R > kMaxLoraRank)
+        return fail(DMPQ_ERR_UNSUPPORTED, "%s: R = %lld exceeds %d", fn, (long long)R, kMaxLoraRank);
+    if (M > INT32_MAX / 2 || N > INT32_MAX / 2 || K > INT32_MAX / 2 || S > INT32_MAX / 4 || n_adapters > INT32_MAX / 2)
+        return fail(DMPQ_ERR_UNSUPPORTED, "%s: M, N, K, S or n_adapters too large", fn);
+    REQUIRE_PTR_NF(fn, rank, n_adapters);
+    REQUIRE_PTR_NF(fn, scale, scaled ? n_adapters : 0);
+    REQUIRE_PTR_NF(fn, seg_start, 1);
+    REQUIRE_PTR_NF(fn, seg_adapter, S);
+    *out = LoraBatch{rank, scale, seg_start, seg_adapter, (int)M, (int)R, (int)S, (int)n_adapters};
+    return DMPQ_OK;
+}
+
+dmpq_status dmpq_lora_shrink(hipStream_t stream, const uint16_t *x, const uint16_t *a,
+                             const int32_t *rank, const int32_t *seg_start,
+                             const int32_t *seg_adapter, int64_t M, int64_t K, int64_t R, int64_t S,
+                             int64_t n_adapters, float *t) {
+    LoraBatch B;
+    if (dmpq_status s = check_lora(__func__, M, 0, K, R, S, n_adapters, rank, nullptr, false, seg_start, seg_adapter,
+                                   &B))
+        return s;
+    REQUIRE_PTR_N(x, M);
+    REQUIRE_PTR_N(a, n_adapters);
+    REQUIRE_PTR_N(t, M);
+    return hip_status(launch_lora_shrink(stream, x, a, B, K, t), __func__);
+}
+
+dmpq_status dmpq_lora_forward(hipStream_t stream, const uint16_t *x, const void *base,
+                              const uint16_t *a, const uint16_t *b, const int32_t *rank,
+                              const float *scale, const int32_t *seg_start,
+                              const int32_t *seg_adapter, int64_t M, int64_t N, int64_t K, int64_t R,
+                              int64_t S, int64_t n_adapters, int out_dtype, float *t, void *y) {
+    LoraBatch B;
+    if (dmpq_status s = check_lora(__func__, M, N, K, R, S, n_adapters, rank, scale, true, seg_start, seg_adapter, &B))
+        return s;
+    REQUIRE_PTR_N(x, M);
+    REQUIRE_PTR_N(base, 0);
+    REQUIRE_PTR_N(a, n_adapters);
+    REQUIRE_PTR_N(b, n_adapters * N);
+    REQUIRE_PTR_N(t, M);
+    REQUIRE_PTR_N(y, M * N);
+    if (out_dtype != DMPQ_OUT_F32 && out_dtype != DMPQ_OUT_BF16)
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: out_dtype %d is not F32 or BF16", __func__, out_dtype);
+    hipError_t e = launch_lora_shrink(stream, x, a, B, K, t);
+    if (e == hipSuccess) e = launch_lora_expand(stream, t, base, b, B, N, out_dtype, y);
+    return hip_status(e, __func__);
+}
+
+// The adapter term of a GEMM epilogue, and the checks that the *_lora GEMMs
+// add to those of the *_ex ones.
+static dmpq_status check_lora_gemm(const char *fn, int64_t M, int64_t N, int64_t K, int64_t R, int64_t S,
+                                   int64_t n_adapters, const float *t, const uint16_t *b,
+                                   const int32_t *rank, const float *scale, const int32_t *seg_start,
+                                   const int32_t *seg_adapter, const void *y, int out_dtype, int epilogue,
+                                   const void *ws, size_t ws_bytes, LoraEpi *out) {
+    if (dmpq_status s = check_gemm(fn, M, N, K)) return s;
+    if (dmpq_status s = check_lora(fn, M, N, K, R, S, n_adapters, rank, scale, true, seg_start, seg_adapter,
+                                   &out->batch))
+        return s;
+    REQUIRE_PTR_NF(fn, t, M);
+    REQUIRE_PTR_NF(fn, b, n_adapters * N);
+    REQUIRE_PTR_NF(fn, y, M * N);
+    out->t = t;
+    out->b = b;
+    return check_epilogue(fn, M, N, out_dtype, 3, epilogue, ws, ws_bytes);
+}
+
+dmpq_status dmpq_gemm_bf16_lora(hipStream_t stream, const uint16_t *x, const uint16_t *w,
+                                const float *t, const uint16_t *b, const int32_t *rank,
+                                const float *scale, const int32_t *seg_start,
+                                const int32_t *seg_adapter, int64_t M, int64_t N, int64_t K,
+                                int64_t R, int64_t S, int64_t n_adapters, int out_dtype, void *y,
+                                int epilogue, void *ws, size_t ws_bytes) {
+    LoraEpi lora;
+    if (dmpq_status s = check_lora_gemm(__func__, M, N, K, R, S, n_adapters, t, b, rank, scale, seg_start,
+                                        seg_adapter, y, out_dtype, epilogue, ws, ws_bytes, &lora))
+        return s;
+    REQUIRE_PTR_N(x, M);
+    REQUIRE_PTR_N(w, N);
+    return hip_status(launch_gemm_bf16(stream, x, w, M, N, K, out_dtype, y, epilogue, static_cast<float *>(ws),
+                                       split_area(ws, ws_bytes, M, N), &lora),
+                      __func__);
+}
+
+dmpq_status dmpq_qgemm_int8_lora(hipStream_t stream, const int8_t *qa, const float *sa,
+                                 const int8_t *qw, const float *sw, const float *t,
+                                 const uint16_t *b, const int32_t *rank, const float *scale,
+                                 const int32_t *seg_start, const int32_t *seg_adapter, int64_t M,
+                                 int64_t N, int64_t K, int64_t R, int64_t S, int64_t n_adapters,
+                                 int out_dtype, void *y, int epilogue, void *ws, size_t ws_bytes) {
+    LoraEpi lora;
+    if (dmpq_status s = check_lora_gemm(__func__, M, N, K, R, S, n_adapters, t, b, rank, scale, seg_start,
+                                        seg_adapter, y, out_dtype, epilogue, ws, ws_bytes, &lora))
+        return s;
+    REQUIRE_PTR_N(qa, M);
+    REQUIRE_PTR_N(sa, M);
+    REQUIRE_PTR_N(qw, N);
+    REQUIRE_PTR_N(sw, N);
+    return hip_status(launch_gemm_int8(stream, qa, sa, qw, sw, M, N, K, out_dtype, y, epilogue,
+                                       static_cast<float *>(ws), split_area(ws, ws_bytes, M, N), &lora),
+                      __func__);
+}
+
+dmpq_status dmpq_qgemm_nvfp4_lora(hipStream_t stream, const uint8_t *ca, const uint8_t *sa,
+                                  const float *d_ga, const uint8_t *cw, const uint8_t *sw,
+                                  const float *d_gw, const float *t, const uint16_t *b,
+                                  const int32_t *rank, const float *scale, const int32_t *seg_start,
+                                  const int32_t *seg_adapter, int64_t M, int64_t N, int64_t K,
+                                  int64_t R, int64_t S, int64_t n_adapters, int out_dtype, void *y,
+                                  int epilogue, void *ws, size_t ws_bytes) {
+    LoraEpi lora;
+    if (dmpq_status s = check_lora_gemm(__func__, M, N, K, R, S, n_adapters, t, b, rank, scale, seg_start,
+                                        seg_adapter, y, out_dtype, epilogue, ws, ws_bytes, &lora))
+        return s;
+    REQUIRE_PTR_N(ca, M);
+    REQUIRE_PTR_N(sa, M);
+    REQUIRE_PTR_N(d_ga, M * N);
+    REQUIRE_PTR_N(cw, N);
+    REQUIRE_PTR_N(sw, N);
+    REQUIRE_PTR_N(d_gw, M * N);
+    return hip_status(launch_gemm_nvfp4(stream, ca, sa, d_ga, cw, sw, d_gw, M, N, K, out_dtype, y,
+                                        DMPQ_FP4_BF16_DEQUANT, epilogue, static_cast<float *>(ws),
+                                        split_area(ws, ws_bytes, M, N), &lora),
+                      __func__);
+}
+
+size_t dmpq_lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t S,
+                                int64_t n_adapters) {
+    const int64_t most = INT32_MAX / 2;
+    if (M < 0 || N < 0 || K < 0 || R < 0 || S < 0 || n_adapters < 0 || M > most || N > most || K > most ||
+        R > kMaxLoraRank || S > most / 2 || n_adapters > most)
+        return 0;
+    return lora_backward_bytes(M, N, K, R, S, n_adapters);
+}
+
+dmpq_status dmpq_lora_backward(hipStream_t stream, const uint16_t *dy, const uint16_t *x,
+                               const float *t, const uint16_t *a, const uint16_t *b,
+                               const int32_t *rank, const float *scale, const int32_t *seg_start,
+                               const int32_t *seg_adapter, const uint16_t *dx_base, int64_t M,
+                               int64_t N, int64_t K, int64_t R, int64_t S, int64_t n_adapters,
+                               uint16_t *dx, float *da, float *db, void *ws, size_t ws_bytes) {
+    LoraBatch B;
+    if (dmpq_status s = check_lora(__func__, M, N, K, R, S, n_adapters, rank, scale, true, seg_start, seg_adapter, &B))
+        return s;
+    if (N % 16 != 0 || N == 0)
+        return fail(DMPQ_ERR_BAD_SHAPE, "%s: N = %lld must be a positive multiple of 16", __func__, (long long)N);
+    REQUIRE_PTR_N(dy, M);
+    REQUIRE_PTR_N(x, M);
+    REQUIRE_PTR_N(t, M);
+    REQUIRE_PTR_N(a, n_adapters);
+    REQUIRE_PTR_N(b, n_adapters);
+    REQUIRE_PTR_N(dx_base, 0);
+    REQUIRE_PTR_N(dx, 0);
+    REQUIRE_PTR_N(da, n_adapters);
+    REQUIRE_PTR_N(db, n_adapters);
+    const size_t need = dmpq_lora_backward_bytes(M, N, K, R, S, n_adapters);
+    if (need > 0 && !ws) return fail(DMPQ_ERR_WORKSPACE, "%s: workspace is NULL", __func__);
+    if (ws && !aligned16(ws)) return fail(DMPQ_ERR_MISALIGNED, "%s: workspace is not 16-byte aligned", __func__);
+    if (ws_bytes < need)
+        return fail(DMPQ_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", __func__, ws_bytes, need);
+    if (n_adapters > 65535) return fail(DMPQ_ERR_UNSUPPORTED, "%s: more than 65535 adapters", __func__);
+    return hip_status(launch_lora_backward(stream, dy, x, t, a, b, B, N, K, dx_base, dx, da, db, ws), __func__);
+}
+
+// ---- AdamW ------------------------------------------------------------------
+
+static int64_t adamw_chunks(const dmpq_adamw_tensor *t, int64_t n) {
+    if (n < 0 || n > INT32_MAX || (n > 0 && !t)) return -1;
+    int64_t chunks = 0;
+    for (int64_t i = 0; i < n; i++) {
+        if (t[i].n < 0 || t[i].n > (int64_t)INT32_MAX * kAdamwChunk) return -1;
+        chunks += (t[i].n + kAdamwChunk - 1) / kAdamwChunk;
+        if (chunks > INT32_MAX) return -1;
+    }
+    return chunks;
+}
+
+size_t dmpq_adamw_table_bytes(const dmpq_adamw_tensor *h_tensors, int64_t n_tensors) {
+    const int64_t c = adamw_chunks(h_tensors, n_tensors);
+    return c < 0 ? 0 : sizeof(AdamwTensor) * (size_t)n_tensors + sizeof(int32_t) * (size_t)c;
+}
+
+static dmpq_status check_adamw_types(const char *fn, int p_dtype, int g_dtype, int state_bits) {
+    if (p_dtype != DMPQ_OUT_F32 && p_dtype != DMPQ_OUT_BF16)
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: p_dtype %d is not F32 or BF16", fn, p_dtype);
+    if (g_dtype != DMPQ_OUT_F32 && g_dtype != DMPQ_OUT_BF16)
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: g_dtype %d is not F32 or BF16", fn, g_dtype);
+    if (state_bits != 32 && state_bits != 8)
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: state_bits %d is not 32 or 8", fn, state_bits);
+    return DMPQ_OK;
+}
+
+dmpq_status dmpq_adamw_table(const dmpq_adamw_tensor *h_tensors, int64_t n_tensors, int p_dtype,
+                             int g_dtype, int state_bits, void *h_table, size_t table_bytes,
+                             int64_t *h_chunks) {
+    if (dmpq_status s = check_adamw_types(__func__, p_dtype, g_dtype, state_bits)) return s;
+    REQUIRE_HOST(h_chunks);
+    const int64_t chunks = adamw_chunks(h_tensors, n_tensors);
+    if (chunks < 0) return fail(DMPQ_ERR_BAD_SHAPE, "%s: a size is negative, missing or too large", __func__);
+    const size_t need = dmpq_adamw_table_bytes(h_tensors, n_tensors);
+    if (need > 0) REQUIRE_HOST(h_table);
+    if (table_bytes < need)
+        return fail(DMPQ_ERR_WORKSPACE, "%s: table has %zu bytes, needs %zu", __func__, table_bytes, need);
+    uint8_t *out = static_cast<uint8_t *>(h_table);
+    int64_t chunk = 0;
+    for (int64_t i = 0; i < n_tensors; i++) {
+        const dmpq_adamw_tensor &t = h_tensors[i];
+        REQUIRE_PTR_N(t.p, t.n);
+        REQUIRE_PTR_N(t.g, t.n);
+        REQUIRE_PTR_N(t.m, t.n);
+        REQUIRE_PTR_N(t.v, t.n);
+        REQUIRE_PTR_N(t.copy, 0);
+        if (state_bits == 8 && t.n > 0) {
+            if (!t.ms || !t.vs) return fail(DMPQ_ERR_INVALID_ARG, "%s: ms or vs is NULL", __func__);
+            if ((reinterpret_cast<uintptr_t>(t.ms) | reinterpret_cast<uintptr_t>(t.vs)) & 3u)
+                return fail(DMPQ_ERR_MISALIGNED, "%s: ms or vs is not 4-byte aligned", __func__);
+        }
+        const AdamwTensor e{t.p, t.g, t.m, t.v, t.ms, t.vs, t.copy, t.n, chunk};
+        memcpy(out + sizeof(AdamwTensor) * (size_t)i, &e, sizeof e);
+        const int64_t c = (t.n + kAdamwChunk - 1) / kAdamwChunk;
+        const int32_t id = (int32_t)i;
+        for (int64_t k = 0; k < c; k++)
+            memcpy(out + sizeof(AdamwTensor) * (size_t)n_tensors + sizeof id * (size_t)(chunk + k), &id, sizeof id);
+        chunk += c;
+    }
+    *h_chunks = chunk;
+    return ok();
+}
+
+static dmpq_status check_adamw_call(const char *fn, const void *d_table, int64_t n_tensors, int64_t chunks,
+                                    int p_dtype, int g_dtype, int state_bits, AdamwTable *out) {
+    if (n_tensors < 0 || chunks < 0)
+        return fail(DMPQ_ERR_BAD_SHAPE, "%s: n_tensors = %lld, chunks = %lld must be >= 0", fn, (long long)n_tensors,
+                    (long long)chunks);
+    if (chunks > INT32_MAX) return fail(DMPQ_ERR_UNSUPPORTED, "%s: more than 2^31 chunks", fn);
+    if (dmpq_status s = check_adamw_types(fn, p_dtype, g_dtype, state_bits)) return s;
+    REQUIRE_PTR_NF(fn, d_table, chunks);
+    const AdamwTensor *t = static_cast<const AdamwTensor *>(d_table);
+    *out = AdamwTable{t, reinterpret_cast<const int32_t *>(t + n_tensors), chunks, p_dtype, g_dtype, state_bits};
+    return DMPQ_OK;
+}
+
+dmpq_status dmpq_grad_norm(hipStream_t stream, const void *d_table, int64_t n_tensors, int64_t chunks,
+                           int g_dtype, double *d_norm, void *ws, size_t ws_bytes) {
+    AdamwTable t;
+    if (dmpq_status s = check_adamw_call(__func__, d_table, n_tensors, chunks, DMPQ_OUT_F32, g_dtype, 32, &t)) return s;
+    REQUIRE_PTR(d_norm);
+    if (dmpq_status s = check_ws(__func__, ws, ws_bytes)) return s;
+    return hip_status(launch_grad_norm(stream, t, d_norm, Workspace(ws)), __func__);
+}
+
+dmpq_status dmpq_adamw_step(hipStream_t stream, const void *d_table, int64_t n_tensors,
+                            int64_t chunks, int p_dtype, int g_dtype, int state_bits, double lr,
+                            double beta1, double beta2, double eps, double weight_decay,
+                            int64_t step, const double *d_norm, double max_norm) {
+    AdamwTable t;
+    if (dmpq_status s = check_adamw_call(__func__, d_table, n_tensors, chunks, p_dtype, g_dtype, state_bits, &t))
+        return s;
+    REQUIRE_PTR_N(d_norm, 0);
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: beta1 = %g, beta2 = %g must lie in [0, 1)", __func__, beta1, beta2);
+    if (!isfinite(lr) || !(eps >= 0.0) || !isfinite(eps) || !isfinite(weight_decay) || isnan(max_norm))
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: lr, eps (>= 0), weight_decay and max_norm must be finite", __func__);
+    if (step < 1) return fail(DMPQ_ERR_INVALID_ARG, "%s: step = %lld must be >= 1", __func__, (long long)step);
+    AdamwHyper h;
+    h.beta1 = (float)beta1;
+    h.omb1 = (float)(1.0 - beta1);
+    h.beta2 = (float)beta2;
+    h.omb2 = (float)(1.0 - beta2);
+    h.eps = (float)eps;
+    h.rbc2 = (float)(1.0 / sqrt(1.0 - pow(beta2, (double)step)));
+    h.decay = (float)(1.0 - lr * weight_decay);
+    h.step = (float)(lr / (1.0 - pow(beta1, (double)step)));
+    h.max_norm = max_norm;
+    return hip_status(launch_adamw(stream, t, h, d_norm), __func__);
 }
 
 }  // extern "C"

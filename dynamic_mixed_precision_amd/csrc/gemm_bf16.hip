@@ -18,7 +18,8 @@ namespace dmpq {
 template <int OUT, bool TAIL, int EPI>
 __global__ __launch_bounds__(256, 1) void gemm_bf16_kernel(
     const uint16_t *__restrict__ x, const uint16_t *__restrict__ w, int64_t M, int64_t N,
-    int64_t K, void *__restrict__ y, unsigned tiles_m, unsigned tiles_n, float *__restrict__ partial) {
+    int64_t K, void *__restrict__ y, unsigned tiles_m, unsigned tiles_n, float *__restrict__ partial,
+    LoraEpi lora) {
     using namespace gdma;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tid = threadIdx.x;
@@ -33,7 +34,7 @@ __global__ __launch_bounds__(256, 1) void gemm_bf16_kernel(
                                     reinterpret_cast<const uint8_t *>(w), M, N, 2 * K, 2 * K, m0, n0,
                                     lds, acc);
     f32_band_epilogue<OUT, EPI>(acc, lds, 1.0f, 1.0f, M, N, m0, n0, wave, wm, wn, lane, y,
-                                (EPI & kEpiAmax) ? partial + pid : nullptr);
+                                (EPI & kEpiAmax) ? partial + pid : nullptr, lora);
 }
 
 // The split workgroups of a SplitPlan launch (see gemm_i8_split_kernel); the
@@ -62,7 +63,7 @@ template <int OUT, int EPI, int S>
 __global__ __launch_bounds__(64) void gemm_f32_fixup_kernel(
     const float *__restrict__ ga, const float *__restrict__ gw, int64_t M, int64_t N,
     void *__restrict__ y, unsigned tiles_m, unsigned tiles_n, unsigned group_m,
-    float *__restrict__ partial, SplitPlan sp, const uint32_t *__restrict__ spart) {
+    float *__restrict__ partial, SplitPlan sp, const uint32_t *__restrict__ spart, LoraEpi lora) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     // workgroup = (tail tile t, quadrant wave, 32-row slice i)
     const int lane = threadIdx.x, i = blockIdx.x & 3, wave = (blockIdx.x >> 2) & 3;
@@ -71,7 +72,7 @@ __global__ __launch_bounds__(64) void gemm_f32_fixup_kernel(
     const int64_t m0 = (int64_t)tc.m * 256, n0 = (int64_t)tc.n * 256;
     EpiScaleF32 sc{ga ? *ga : 1.0f, gw ? *gw : 1.0f};
     split_fixup_epilogue<OUT, EPI, float, S>(spart + (size_t)t * S * kSplitWords, sc, lds, M, N, m0, n0, wave,
-                                             i, lane, y, (EPI & kEpiAmax) ? partial + pid : nullptr);
+                                             i, lane, y, (EPI & kEpiAmax) ? partial + pid : nullptr, lora);
 }
 
 template <class KernelFn>
@@ -83,13 +84,13 @@ static hipError_t allow_lds(KernelFn fn, size_t bytes) {
 template <int OUT, int EPI>
 static hipError_t launch_fixup(hipStream_t s, const float *ga, const float *gw, int64_t M, int64_t N,
                                void *y, unsigned tiles_m, unsigned tiles_n, unsigned group_m,
-                               float *partial, const SplitPlan &sp, const uint32_t *spart) {
+                               float *partial, const SplitPlan &sp, const uint32_t *spart, const LoraEpi &lora) {
     const dim3 fg(16 * sp.tail), fb(64);
     const size_t fl = (size_t)kFixupRows * EpiBand<OUT == 1 ? 2 : 4>::STRIDE;
 #define DMPQ_F32_FIX(S_)                                                                         \
     case S_:                                                                                     \
         hipLaunchKernelGGL((gemm_f32_fixup_kernel<OUT, EPI, S_>), fg, fb, fl, s, ga, gw, M, N, y, tiles_m, \
-                           tiles_n, group_m, partial, sp, spart);                                \
+                           tiles_n, group_m, partial, sp, spart, lora);                          \
         break;
     switch (sp.splits) {
         DMPQ_F32_FIX(2) DMPQ_F32_FIX(3) DMPQ_F32_FIX(4) DMPQ_F32_FIX(8)
@@ -102,22 +103,31 @@ static hipError_t launch_fixup(hipStream_t s, const float *ga, const float *gw, 
 hipError_t launch_f32_fixup(hipStream_t s, const float *ga, const float *gw, int64_t M, int64_t N,
                             void *y, unsigned tiles_m, unsigned tiles_n, unsigned group_m,
                             float *partial, const SplitPlan &sp, const uint32_t *spart,
-                            int out_dtype, int epi) {
-    if (out_dtype == 0 && epi == 0)
-        return launch_fixup<0, 0>(s, ga, gw, M, N, y, tiles_m, tiles_n, group_m, partial, sp, spart);
+                            int out_dtype, int epi, const LoraEpi *lora) {
+    const LoraEpi le = lora ? *lora : LoraEpi{};
+#define DMPQ_F32_FIXUP(OUT_, EPI_) \
+    return launch_fixup<OUT_, EPI_>(s, ga, gw, M, N, y, tiles_m, tiles_n, group_m, partial, sp, spart, le)
+    if (out_dtype == 0 && epi == 0) DMPQ_F32_FIXUP(0, 0);
+    if (out_dtype == 0 && epi == kEpiLora) DMPQ_F32_FIXUP(0, kEpiLora);
     if (out_dtype != 1) return hipErrorInvalidValue;
     switch (epi) {
-        case 0: return launch_fixup<1, 0>(s, ga, gw, M, N, y, tiles_m, tiles_n, group_m, partial, sp, spart);
-        case 1: return launch_fixup<1, 1>(s, ga, gw, M, N, y, tiles_m, tiles_n, group_m, partial, sp, spart);
-        case 2: return launch_fixup<1, 2>(s, ga, gw, M, N, y, tiles_m, tiles_n, group_m, partial, sp, spart);
-        case 3: return launch_fixup<1, 3>(s, ga, gw, M, N, y, tiles_m, tiles_n, group_m, partial, sp, spart);
+        case 0: DMPQ_F32_FIXUP(1, 0);
+        case 1: DMPQ_F32_FIXUP(1, 1);
+        case 2: DMPQ_F32_FIXUP(1, 2);
+        case 3: DMPQ_F32_FIXUP(1, 3);
+        case 4: DMPQ_F32_FIXUP(1, 4);
+        case 5: DMPQ_F32_FIXUP(1, 5);
+        case 6: DMPQ_F32_FIXUP(1, 6);
+        case 7: DMPQ_F32_FIXUP(1, 7);
     }
+#undef DMPQ_F32_FIXUP
     return hipErrorInvalidValue;
 }
 
 template <int OUT, int EPI>
 static hipError_t launch_bf16_paths(hipStream_t s, const uint16_t *x, const uint16_t *w, int64_t M,
-                                    int64_t N, int64_t K, void *y, float *partial, uint32_t *spart) {
+                                    int64_t N, int64_t K, void *y, float *partial, uint32_t *spart,
+                                    const LoraEpi &lora) {
     using namespace gdma;
     static const hipError_t attr = [] {
         hipError_t e = allow_lds(gemm_bf16_kernel<OUT, false, EPI>, LDS_BYTES);
@@ -135,10 +145,10 @@ static hipError_t launch_bf16_paths(hipStream_t s, const uint16_t *x, const uint
     if (sp.full > 0) {
         if (tail)
             hipLaunchKernelGGL((gemm_bf16_kernel<OUT, true, EPI>), dim3(sp.full), block, LDS_BYTES, s, x, w, M, N,
-                               K, y, utm, utn, partial);
+                               K, y, utm, utn, partial, lora);
         else
             hipLaunchKernelGGL((gemm_bf16_kernel<OUT, false, EPI>), dim3(sp.full), block, LDS_BYTES, s, x, w, M, N,
-                               K, y, utm, utn, partial);
+                               K, y, utm, utn, partial, lora);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -152,23 +162,32 @@ static hipError_t launch_bf16_paths(hipStream_t s, const uint16_t *x, const uint
                                sp, spart, (EPI & kEpiAmax) ? partial : nullptr);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        return launch_fixup<OUT, EPI>(s, nullptr, nullptr, M, N, y, utm, utn, GROUP_M, partial, sp, spart);
+        return launch_fixup<OUT, EPI>(s, nullptr, nullptr, M, N, y, utm, utn, GROUP_M, partial, sp, spart, lora);
     }
     return hipSuccess;
 }
 
 hipError_t launch_gemm_bf16(hipStream_t s, const uint16_t *x, const uint16_t *w, int64_t M,
                             int64_t N, int64_t K, int out_dtype, void *y, int epi, float *partial,
-                            uint32_t *spart) {
+                            uint32_t *spart, const LoraEpi *lora) {
     if (M == 0 || N == 0) return hipSuccess;
-    if (out_dtype == 0 && epi == 0) return launch_bf16_paths<0, 0>(s, x, w, M, N, K, y, partial, spart);
+    const LoraEpi le = lora ? *lora : LoraEpi{};
+    if (lora) epi |= kEpiLora;
+#define DMPQ_BF16_PATHS(OUT_, EPI_) return launch_bf16_paths<OUT_, EPI_>(s, x, w, M, N, K, y, partial, spart, le)
+    if (out_dtype == 0 && epi == 0) DMPQ_BF16_PATHS(0, 0);
+    if (out_dtype == 0 && epi == kEpiLora) DMPQ_BF16_PATHS(0, kEpiLora);
     if (out_dtype != 1) return hipErrorInvalidValue;
     switch (epi) {
-        case 0: return launch_bf16_paths<1, 0>(s, x, w, M, N, K, y, partial, spart);
-        case 1: return launch_bf16_paths<1, 1>(s, x, w, M, N, K, y, partial, spart);
-        case 2: return launch_bf16_paths<1, 2>(s, x, w, M, N, K, y, partial, spart);
-        case 3: return launch_bf16_paths<1, 3>(s, x, w, M, N, K, y, partial, spart);
+        case 0: DMPQ_BF16_PATHS(1, 0);
+        case 1: DMPQ_BF16_PATHS(1, 1);
+        case 2: DMPQ_BF16_PATHS(1, 2);
+        case 3: DMPQ_BF16_PATHS(1, 3);
+        case 4: DMPQ_BF16_PATHS(1, 4);
+        case 5: DMPQ_BF16_PATHS(1, 5);
+        case 6: DMPQ_BF16_PATHS(1, 6);
+        case 7: DMPQ_BF16_PATHS(1, 7);
     }
+#undef DMPQ_BF16_PATHS
     return hipErrorInvalidValue;
 }
 

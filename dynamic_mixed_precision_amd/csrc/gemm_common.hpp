@@ -6,6 +6,7 @@
 
 #include "device.hpp"
 #include "internal.hpp"
+#include "lora.hpp"
 
 namespace dmpq {
 
@@ -128,8 +129,10 @@ struct EpiBand {
 // result is rounded again.  kEpiAmax (bf16 output, N % 16 == 0): the maximum
 // of |FWHT16(row block)| over the stored bf16 values of the tile -- the next
 // layer's NVFP4 tensor-amax term, with the same fp32 butterfly order as the
-// quantizer -- is written to the tile's entry of the maxima.
-enum { kEpiGelu = 1, kEpiAmax = 2 };
+// quantizer -- is written to the tile's entry of the maxima.  kEpiLora: the
+// adapter term of the row's request is added to the fp32 value before any of
+// that, so it costs no pass over y of its own.
+enum { kEpiGelu = 1, kEpiAmax = 2, kEpiLora = 4 };
 
 // GELU(v) = v Phi(v) = (v / 2) erfc(-v / sqrt 2) in fp32.  erfc comes from
 // the Chebyshev fit published in Numerical Recipes (Press et al., section
@@ -267,8 +270,9 @@ struct EpiScaleF32 {
 template <int OUT, int EPI, class AccV, class Scale>
 __device__ __forceinline__ void band_epilogue(AccV (&acc)[4][4], Scale &sc, uint8_t *lds, int64_t M,
                                               int64_t N, int64_t m0, int64_t n0, int wave, int wm,
-                                              int wn, int lane, void *y, float *slot) {
+                                              int wn, int lane, void *y, float *slot, const LoraEpi &lora) {
     constexpr int ES = OUT == 1 ? 2 : 4;
+    constexpr bool LORA = (EPI & kEpiLora) != 0;
     constexpr bool AMAX = (EPI & kEpiAmax) != 0;
     static_assert(!AMAX || OUT == 1, "the fused amax needs bf16 output");
     using Band = EpiBand<ES>;
@@ -282,6 +286,15 @@ __device__ __forceinline__ void band_epilogue(AccV (&acc)[4][4], Scale &sc, uint
         for (int ii = 0; ii < 2; ii++) {
             const int i = 2 * h + ii;
             sc.row(m0 + wm * 128 + i * 32 + lm);
+            v16f v[4];
+            if constexpr (LORA) {
+                __builtin_amdgcn_sched_barrier(0);  // one slice's values at a time
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int r = 0; r < 16; r++) v[j][r] = sc((float)acc[i][j][r], j, r >> 2, r & 3);
+                lora_slice<ES == 2 ? 2 : 3>(lora, m0 + wm * 128 + i * 32 + lm, n0 + wn * 128, N, lane, v);
+            }
 #pragma unroll
             for (int j = 0; j < 4; j++) {
 #pragma unroll
@@ -289,7 +302,8 @@ __device__ __forceinline__ void band_epilogue(AccV (&acc)[4][4], Scale &sc, uint
                     uint8_t *dst = band + (ii * 32 + lm) * Band::STRIDE + (j * 32 + 8 * g + 4 * lh) * ES;
                     float v4[4];
 #pragma unroll
-                    for (int e = 0; e < 4; e++) v4[e] = sc((float)acc[i][j][4 * g + e], j, g, e);
+                    for (int e = 0; e < 4; e++)
+                        v4[e] = LORA ? v[j][4 * g + e] : sc((float)acc[i][j][4 * g + e], j, g, e);
                     if constexpr (OUT == 0)
                         *reinterpret_cast<float4 *>(dst) = make_float4(v4[0], v4[1], v4[2], v4[3]);
                     else
@@ -309,9 +323,9 @@ template <int OUT, int EPI = 0>
 __device__ __forceinline__ void f32_band_epilogue(v16f (&acc)[4][4], uint8_t *lds, float gA,
                                                   float gW, int64_t M, int64_t N, int64_t m0,
                                                   int64_t n0, int wave, int wm, int wn, int lane,
-                                                  void *y, float *slot = nullptr) {
+                                                  void *y, float *slot, const LoraEpi &lora) {
     EpiScaleF32 sc{gA, gW};
-    band_epilogue<OUT, EPI>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot);
+    band_epilogue<OUT, EPI>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot, lora);
 }
 
 // The epilogue of one 32-row slice i of a 128 x 128 quadrant of a split
@@ -331,8 +345,10 @@ constexpr int kFixupRows = 32;
 template <int OUT, int EPI, class T, int S, class Scale>
 __device__ __forceinline__ void split_fixup_epilogue(const uint32_t *part, Scale &sc, uint8_t *lds,
                                                      int64_t M, int64_t N, int64_t m0, int64_t n0,
-                                                     int wave, int i, int lane, void *y, float *slot) {
+                                                     int wave, int i, int lane, void *y, float *slot,
+                                                     const LoraEpi &lora) {
     constexpr int ES = OUT == 1 ? 2 : 4;
+    constexpr bool LORA = (EPI & kEpiLora) != 0;
     using Band = EpiBand<ES>;
     constexpr size_t kPieces = kSplitWords / 4;
     const uint4 *p4 = reinterpret_cast<const uint4 *>(part);
@@ -341,6 +357,14 @@ __device__ __forceinline__ void split_fixup_epilogue(const uint32_t *part, Scale
     uint8_t *band = lds;
     const bool vec = ((N * ES) & 15) == 0;
     sc.row(m0 + wm * 128 + i * 32 + lm);
+    v16f add[4];
+    if constexpr (LORA) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int r = 0; r < 16; r++) add[j][r] = 0.0f;
+        lora_slice<ES == 2 ? 2 : 3>(lora, m0 + wm * 128 + i * 32 + lm, n0 + wn * 128, N, lane, add);
+    }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         uint4 v[S][4];
@@ -361,7 +385,10 @@ __device__ __forceinline__ void split_fixup_epilogue(const uint32_t *part, Scale
             }
             float v4[4];
 #pragma unroll
-            for (int e = 0; e < 4; e++) v4[e] = sc((float)x[e], j, g, e);
+            for (int e = 0; e < 4; e++) {
+                v4[e] = sc((float)x[e], j, g, e);
+                if constexpr (LORA) v4[e] += add[j][4 * g + e];
+            }
             uint8_t *dst = band + lm * Band::STRIDE + (j * 32 + 8 * g + 4 * lh) * ES;
             if constexpr (OUT == 0)
                 *reinterpret_cast<float4 *>(dst) = make_float4(v4[0], v4[1], v4[2], v4[3]);

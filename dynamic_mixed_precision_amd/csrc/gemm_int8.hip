@@ -66,15 +66,15 @@ __device__ __forceinline__ void i8_scale_dma(float *scl, const float *sa, const 
 // the fused amax per EPI; OUT 2: the raw int32 accumulators (test mode).  The
 // stage buffers must be free (both main loops end with a barrier).  SCL: the
 // tile's staged scales (i8_scale_dma).  pid: the tile's slot among the
-// fused-amax maxima.
-#define DMPQ_I8_EPILOGUE(SCL)                                                                     \
+// fused-amax maxima.  LORA: the adapter term (kEpiLora).
+#define DMPQ_I8_EPILOGUE(SCL, LORA)                                                               \
     {                                                                                             \
         constexpr int ES = OUT == 1 ? 2 : 4;                                                      \
         using Band = EpiBand<ES>;                                                                 \
         const int lm = lane & 31, lh = lane >> 5;                                                 \
         const float *scl_ = (SCL);                                                                \
         float4 swv[4][4];                                                                         \
-        if constexpr (OUT != 2) {                                                                 \
+        if constexpr (OUT != 2 && (EPI & kEpiLora) == 0) {                                        \
             _Pragma("unroll") for (int j = 0; j < 4; j++)                                         \
                 _Pragma("unroll") for (int g = 0; g < 4; g++) swv[j][g] =                         \
                     *reinterpret_cast<const float4 *>(scl_ + 256 + wn * 128 + j * 32 + 8 * g + 4 * lh); \
@@ -86,6 +86,19 @@ __device__ __forceinline__ void i8_scale_dma(float *scl, const float *sa, const 
             _Pragma("unroll") for (int ii = 0; ii < 2; ii++) {                                    \
                 const int i = 2 * h + ii;                                                         \
                 const float sar = OUT == 2 ? 0.0f : scl_[wm * 128 + i * 32 + lm];                 \
+                v16f v[4];                                                                        \
+                if constexpr ((EPI & kEpiLora) != 0) {                                            \
+                    __builtin_amdgcn_sched_barrier(0);                                            \
+                    _Pragma("unroll") for (int j = 0; j < 4; j++)                                 \
+                        _Pragma("unroll") for (int g = 0; g < 4; g++) {                           \
+                            const float4 w_ = *reinterpret_cast<const float4 *>(scl_ + 256 + wn * 128 + j * 32 + 8 * g + 4 * lh); \
+                            v[j][4 * g + 0] = ((float)acc[i][j][4 * g + 0] * sar) * w_.x;         \
+                            v[j][4 * g + 1] = ((float)acc[i][j][4 * g + 1] * sar) * w_.y;         \
+                            v[j][4 * g + 2] = ((float)acc[i][j][4 * g + 2] * sar) * w_.z;         \
+                            v[j][4 * g + 3] = ((float)acc[i][j][4 * g + 3] * sar) * w_.w;         \
+                        }                                                                         \
+                    lora_slice<ES == 2 ? 2 : 3>(LORA, m0 + wm * 128 + i * 32 + lm, n0 + wn * 128, N, lane, v); \
+                }                                                                                 \
                 _Pragma("unroll") for (int j = 0; j < 4; j++) {                                   \
                     _Pragma("unroll") for (int g = 0; g < 4; g++) {                               \
                         uint8_t *dst = band + (ii * 32 + lm) * Band::STRIDE + (j * 32 + 8 * g + 4 * lh) * ES; \
@@ -95,10 +108,14 @@ __device__ __forceinline__ void i8_scale_dma(float *scl, const float *sa, const 
                                           acc[i][j][4 * g + 3]);                                  \
                         } else {                                                                  \
                             float v4[4];                                                          \
+                            if constexpr ((EPI & kEpiLora) != 0) {                                \
+                                _Pragma("unroll") for (int e = 0; e < 4; e++) v4[e] = v[j][4 * g + e]; \
+                            } else {                                                              \
                             v4[0] = ((float)acc[i][j][4 * g + 0] * sar) * swv[j][g].x;            \
                             v4[1] = ((float)acc[i][j][4 * g + 1] * sar) * swv[j][g].y;            \
                             v4[2] = ((float)acc[i][j][4 * g + 2] * sar) * swv[j][g].z;            \
                             v4[3] = ((float)acc[i][j][4 * g + 3] * sar) * swv[j][g].w;            \
+                            }                                                                     \
                             if constexpr (OUT == 0)                                               \
                                 *reinterpret_cast<float4 *>(dst) = make_float4(v4[0], v4[1], v4[2], v4[3]); \
                             else                                                                  \
@@ -119,7 +136,7 @@ template <int OUT, int EPI>
 __global__ __launch_bounds__(256, 1) void gemm_i8_kernel(
     const int8_t *__restrict__ A, const float *__restrict__ sa, const int8_t *__restrict__ W,
     const float *__restrict__ sw, int64_t M, int64_t N, int64_t K, void *__restrict__ y,
-    unsigned tiles_m, unsigned tiles_n, float *__restrict__ partial) {
+    unsigned tiles_m, unsigned tiles_n, float *__restrict__ partial, LoraEpi lora) {
     using namespace i8gemm;
     extern __shared__ __attribute__((aligned(16))) int8_t lds[];
     const int tid = threadIdx.x;
@@ -209,7 +226,7 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_kernel(
 #undef DMPQ_I8_GLOAD
 #undef DMPQ_I8_SSTORE
 
-    DMPQ_I8_EPILOGUE(scl)
+    DMPQ_I8_EPILOGUE(scl, lora)
 }
 
 // ---------------------------------------------------------------------------
@@ -340,7 +357,7 @@ __global__ __launch_bounds__(256, 1) void gemm_i8w4_kernel(
 #undef DMPQ_I8W4_GLOAD
 #undef DMPQ_I8W4_SSTORE
 
-    DMPQ_I8_EPILOGUE(scl)
+    DMPQ_I8_EPILOGUE(scl, LoraEpi{})
 }
 
 // ---------------------------------------------------------------------------
@@ -351,7 +368,7 @@ template <int OUT, int EPI>
 __global__ __launch_bounds__(256, 1) void gemm_i8_dma_kernel(
     const int8_t *__restrict__ A, const float *__restrict__ sa, const int8_t *__restrict__ W,
     const float *__restrict__ sw, int64_t M, int64_t N, int64_t K, void *__restrict__ y,
-    unsigned tiles_m, unsigned tiles_n, float *__restrict__ partial) {
+    unsigned tiles_m, unsigned tiles_n, float *__restrict__ partial, LoraEpi lora) {
     using namespace gdma;
     extern __shared__ __attribute__((aligned(16))) int8_t lds[];
     const int tid = threadIdx.x;
@@ -367,7 +384,7 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_dma_kernel(
     dma_gemm_mainloop<OpI8, false>(reinterpret_cast<const uint8_t *>(A),
                                    reinterpret_cast<const uint8_t *>(W), M, N, K, K, m0, n0,
                                    reinterpret_cast<uint8_t *>(lds), acc);
-    DMPQ_I8_EPILOGUE(scl)
+    DMPQ_I8_EPILOGUE(scl, lora)
 }
 
 // The split workgroups of a SplitPlan launch: the main loop over this
@@ -431,7 +448,7 @@ template <int OUT, int EPI, int S>
 __global__ __launch_bounds__(64) void gemm_i8_fixup_kernel(
     const float *__restrict__ sa, const float *__restrict__ sw, int64_t M, int64_t N,
     void *__restrict__ y, unsigned tiles_m, unsigned tiles_n, float *__restrict__ partial,
-    SplitPlan sp, const uint32_t *__restrict__ spart) {
+    SplitPlan sp, const uint32_t *__restrict__ spart, LoraEpi lora) {
     using namespace gdma;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
     // workgroup = (tail tile t, quadrant wave, 32-row slice i)
@@ -441,7 +458,7 @@ __global__ __launch_bounds__(64) void gemm_i8_fixup_kernel(
     const int64_t m0 = (int64_t)tc.m * BM, n0 = (int64_t)tc.n * BN;
     EpiScaleI8 sc(sa, sw, M, N, n0 + (wave & 1) * 128 + 4 * (lane >> 5));
     split_fixup_epilogue<OUT, EPI, int, S>(spart + (size_t)t * S * kSplitWords, sc, lds8, M, N, m0, n0, wave,
-                                           i, lane, y, (EPI & kEpiAmax) ? partial + pid : nullptr);
+                                           i, lane, y, (EPI & kEpiAmax) ? partial + pid : nullptr, lora);
 }
 
 template <class KernelFn>
@@ -454,7 +471,7 @@ static hipError_t allow_lds(KernelFn fn, size_t bytes) {
 template <int OUT, int EPI>
 static hipError_t launch_i8_paths(hipStream_t s, const int8_t *qa, const float *sa, const int8_t *qw,
                                   const float *sw, int64_t M, int64_t N, int64_t K, void *y,
-                                  float *partial, uint32_t *spart) {
+                                  float *partial, uint32_t *spart, const LoraEpi &lora) {
     constexpr bool CAN_SPLIT = OUT != 2;
     // Kernels need more dynamic LDS than the default limit: opt in once.
     static const hipError_t attr = [] {
@@ -471,14 +488,14 @@ static hipError_t launch_i8_paths(hipStream_t s, const int8_t *qa, const float *
     if (K % gdma::BK != 0) {
         hipLaunchKernelGGL((gemm_i8_kernel<OUT, EPI>), dim3((unsigned)(tm * tn)), block,
                            2 * i8gemm::STAGE + kI8ScaleBytes, s, qa,
-                           sa, qw, sw, M, N, K, y, utm, utn, partial);
+                           sa, qw, sw, M, N, K, y, utm, utn, partial, lora);
         return hipGetLastError();
     }
     const SplitPlan sp = plan_split(tm * tn, (int)(K / gdma::BK), CAN_SPLIT && spart != nullptr && K >= kSplitMinKInt8);
     if (sp.full > 0) {
         hipLaunchKernelGGL((gemm_i8_dma_kernel<OUT, EPI>), dim3(sp.full), block,
                            gdma::LDS_BYTES + kI8ScaleBytes, s, qa, sa, qw,
-                           sw, M, N, K, y, utm, utn, partial);
+                           sw, M, N, K, y, utm, utn, partial, lora);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -494,7 +511,7 @@ static hipError_t launch_i8_paths(hipStream_t s, const int8_t *qa, const float *
 #define DMPQ_I8_FIX(S_)                                                                          \
     case S_:                                                                                     \
         hipLaunchKernelGGL((gemm_i8_fixup_kernel<OUT, EPI, S_>), fg, fb, fl, s, sa, sw, M, N, y, utm, utn, \
-                           partial, sp, cp);                                                     \
+                           partial, sp, cp, lora);                                               \
         break;
             switch (sp.splits) {
                 DMPQ_I8_FIX(2) DMPQ_I8_FIX(3) DMPQ_I8_FIX(4) DMPQ_I8_FIX(8)
@@ -544,22 +561,32 @@ hipError_t launch_gemm_int8_w4(hipStream_t s, const int8_t *qa, const float *sa,
 
 hipError_t launch_gemm_int8(hipStream_t s, const int8_t *qa, const float *sa, const int8_t *qw,
                             const float *sw, int64_t M, int64_t N, int64_t K, int out_dtype,
-                            void *y, int epi, float *partial, uint32_t *spart) {
+                            void *y, int epi, float *partial, uint32_t *spart, const LoraEpi *lora) {
     if (M == 0 || N == 0) return hipSuccess;
+    const LoraEpi le = lora ? *lora : LoraEpi{};
+    if (lora) epi |= kEpiLora;
+#define DMPQ_I8_PATHS(OUT_, EPI_) \
+    return launch_i8_paths<OUT_, EPI_>(s, qa, sa, qw, sw, M, N, K, y, partial, spart, le)
     if (epi == 0) {
         switch (out_dtype) {
-            case 0: return launch_i8_paths<0, 0>(s, qa, sa, qw, sw, M, N, K, y, partial, spart);
-            case 1: return launch_i8_paths<1, 0>(s, qa, sa, qw, sw, M, N, K, y, partial, spart);
-            case 2: return launch_i8_paths<2, 0>(s, qa, sa, qw, sw, M, N, K, y, partial, spart);
+            case 0: DMPQ_I8_PATHS(0, 0);
+            case 1: DMPQ_I8_PATHS(1, 0);
+            case 2: DMPQ_I8_PATHS(2, 0);
         }
         return hipErrorInvalidValue;
     }
+    if (out_dtype == 0 && epi == kEpiLora) DMPQ_I8_PATHS(0, kEpiLora);
     if (out_dtype != 1) return hipErrorInvalidValue;
     switch (epi) {
-        case 1: return launch_i8_paths<1, 1>(s, qa, sa, qw, sw, M, N, K, y, partial, spart);
-        case 2: return launch_i8_paths<1, 2>(s, qa, sa, qw, sw, M, N, K, y, partial, spart);
-        case 3: return launch_i8_paths<1, 3>(s, qa, sa, qw, sw, M, N, K, y, partial, spart);
+        case 1: DMPQ_I8_PATHS(1, 1);
+        case 2: DMPQ_I8_PATHS(1, 2);
+        case 3: DMPQ_I8_PATHS(1, 3);
+        case 4: DMPQ_I8_PATHS(1, 4);
+        case 5: DMPQ_I8_PATHS(1, 5);
+        case 6: DMPQ_I8_PATHS(1, 6);
+        case 7: DMPQ_I8_PATHS(1, 7);
     }
+#undef DMPQ_I8_PATHS
     return hipErrorInvalidValue;
 }
 

@@ -89,9 +89,9 @@ template <int OUT, int EPI>
 __device__ __forceinline__ void fp4_epilogue(v16f (&acc)[4][4], uint8_t *lds, const float *ga,
                                              const float *gw, int64_t M, int64_t N, int64_t m0,
                                              int64_t n0, int wave, int wm, int wn, int lane,
-                                             void *y, float *partial, unsigned pid) {
+                                             void *y, float *partial, unsigned pid, const LoraEpi &lora) {
     f32_band_epilogue<OUT, EPI>(acc, lds, *ga, *gw, M, N, m0, n0, wave, wm, wn, lane, y,
-                                (EPI & kEpiAmax) ? partial + pid : nullptr);
+                                (EPI & kEpiAmax) ? partial + pid : nullptr, lora);
 }
 
 template <int OUT, int EPI>
@@ -99,7 +99,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_f16_kernel(
     const uint8_t *__restrict__ ca, const uint8_t *__restrict__ sa, const float *__restrict__ ga,
     const uint8_t *__restrict__ cw, const uint8_t *__restrict__ sw, const float *__restrict__ gw,
     int64_t M, int64_t N, int64_t K, void *__restrict__ y, unsigned tiles_m, unsigned tiles_n,
-    float *__restrict__ partial) {
+    float *__restrict__ partial, LoraEpi lora) {
     using namespace fp4gemm;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tid = threadIdx.x;
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_f16_kernel(
 #undef DMPQ_F4_MFMA
 #undef DMPQ_F4_ITER
 
-    fp4_epilogue<OUT, EPI>(acc, lds, ga, gw, M, N, m0, n0, wave, wm, wn, lane, y, partial, pid);
+    fp4_epilogue<OUT, EPI>(acc, lds, ga, gw, M, N, m0, n0, wave, wm, wn, lane, y, partial, pid, lora);
 }
 
 // ---------------------------------------------------------------------------
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_fast_kernel(
     const uint8_t *__restrict__ ca, const uint8_t *__restrict__ sa, const float *__restrict__ ga,
     const uint8_t *__restrict__ cw, const uint8_t *__restrict__ sw, const float *__restrict__ gw,
     int64_t M, int64_t N, int64_t K, void *__restrict__ y, unsigned tiles_m, unsigned tiles_n,
-    float *__restrict__ partial) {
+    float *__restrict__ partial, LoraEpi lora) {
     using namespace fp4gemm;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tid = threadIdx.x;
@@ -358,7 +358,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_fast_kernel(
 #undef DMPQ_F4F_MFMA
 #undef DMPQ_F4F_ITER
 
-    fp4_epilogue<OUT, EPI>(acc, lds, ga, gw, M, N, m0, n0, wave, wm, wn, lane, y, partial, pid);
+    fp4_epilogue<OUT, EPI>(acc, lds, ga, gw, M, N, m0, n0, wave, wm, wn, lane, y, partial, pid, lora);
 }
 
 // One k-step fragment: the 8 codes of 32-bit word S of a 16-byte piece, times
@@ -635,7 +635,7 @@ __device__ __forceinline__ void fp4dma_tile(const uint8_t *__restrict__ ca, cons
                                             const uint8_t *__restrict__ sw, const float *__restrict__ gw,
                                             int64_t M, int64_t N, int64_t K, void *__restrict__ y,
                                             unsigned tiles_m, unsigned tiles_n, float *__restrict__ partial,
-                                            uint8_t *lds) {
+                                            uint8_t *lds, const LoraEpi &lora) {
     using namespace fp4dma;
     const int tid = threadIdx.x;
     const int lane = tid & 63, wave = tid >> 6;
@@ -645,7 +645,7 @@ __device__ __forceinline__ void fp4dma_tile(const uint8_t *__restrict__ ca, cons
     const int64_t m0 = (int64_t)tc.m * BM, n0 = (int64_t)tc.n * BN;
     v16f acc[4][4];
     fp4dma_mainloop<HT>(ca, sa, cw, sw, M, N, K, m0, n0, 0, (int)(K / BKE) + (HT ? 1 : 0), lds, acc);
-    fp4_epilogue<OUT, EPI>(acc, lds, ga, gw, M, N, m0, n0, wave, wm, wn, lane, y, partial, pid);
+    fp4_epilogue<OUT, EPI>(acc, lds, ga, gw, M, N, m0, n0, wave, wm, wn, lane, y, partial, pid, lora);
 }
 
 // The whole-tile kernels: K % 256 == 0, and with the closing half stage
@@ -655,9 +655,9 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_dma_kernel(
     const uint8_t *__restrict__ ca, const uint8_t *__restrict__ sa, const float *__restrict__ ga,
     const uint8_t *__restrict__ cw, const uint8_t *__restrict__ sw, const float *__restrict__ gw,
     int64_t M, int64_t N, int64_t K, void *__restrict__ y, unsigned tiles_m, unsigned tiles_n,
-    float *__restrict__ partial) {
+    float *__restrict__ partial, LoraEpi lora) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    fp4dma_tile<OUT, EPI, false>(ca, sa, ga, cw, sw, gw, M, N, K, y, tiles_m, tiles_n, partial, lds);
+    fp4dma_tile<OUT, EPI, false>(ca, sa, ga, cw, sw, gw, M, N, K, y, tiles_m, tiles_n, partial, lds, lora);
 }
 
 template <int OUT, int EPI>
@@ -665,9 +665,9 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_dma_tail_kernel(
     const uint8_t *__restrict__ ca, const uint8_t *__restrict__ sa, const float *__restrict__ ga,
     const uint8_t *__restrict__ cw, const uint8_t *__restrict__ sw, const float *__restrict__ gw,
     int64_t M, int64_t N, int64_t K, void *__restrict__ y, unsigned tiles_m, unsigned tiles_n,
-    float *__restrict__ partial) {
+    float *__restrict__ partial, LoraEpi lora) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    fp4dma_tile<OUT, EPI, true>(ca, sa, ga, cw, sw, gw, M, N, K, y, tiles_m, tiles_n, partial, lds);
+    fp4dma_tile<OUT, EPI, true>(ca, sa, ga, cw, sw, gw, M, N, K, y, tiles_m, tiles_n, partial, lds, lora);
 }
 
 // The split workgroups of a SplitPlan launch (see gemm_i8_split_kernel).
@@ -845,11 +845,11 @@ template <int OUT, int EPI, bool HT, class TileFn, class SplitFn>
 static hipError_t launch_fp4_dma(hipStream_t s, TileFn tile_kernel, SplitFn split_kernel, const uint8_t *ca,
                                  const uint8_t *sa, const float *ga, const uint8_t *cw, const uint8_t *sw,
                                  const float *gw, int64_t M, int64_t N, int64_t K, void *y, float *partial,
-                                 uint32_t *spart, unsigned utm, unsigned utn) {
+                                 uint32_t *spart, unsigned utm, unsigned utn, const LoraEpi &lora) {
     const SplitPlan sp = plan_split((int64_t)utm * utn, (int)(K / fp4dma::BKE) + (HT ? 1 : 0), spart != nullptr);
     if (sp.full > 0) {
         hipLaunchKernelGGL(tile_kernel, dim3(sp.full), dim3(256), fp4dma::LDS_BYTES, s, ca, sa, ga, cw, sw, gw, M,
-                           N, K, y, utm, utn, partial);
+                           N, K, y, utm, utn, partial, lora);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -858,7 +858,7 @@ static hipError_t launch_fp4_dma(hipStream_t s, TileFn tile_kernel, SplitFn spli
                            M, N, K, utm, utn, sp, spart, (EPI & kEpiAmax) ? partial : nullptr);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        return launch_f32_fixup(s, ga, gw, M, N, y, utm, utn, fp4dma::GROUP_M, partial, sp, spart, OUT, EPI);
+        return launch_f32_fixup(s, ga, gw, M, N, y, utm, utn, fp4dma::GROUP_M, partial, sp, spart, OUT, EPI, &lora);
     }
     return hipGetLastError();
 }
@@ -867,7 +867,7 @@ template <int OUT, int EPI>
 static hipError_t launch_fp4_paths(hipStream_t s, const uint8_t *ca, const uint8_t *sa,
                                    const float *ga, const uint8_t *cw, const uint8_t *sw,
                                    const float *gw, int64_t M, int64_t N, int64_t K, void *y,
-                                   float *partial, uint32_t *spart) {
+                                   float *partial, uint32_t *spart, const LoraEpi &lora) {
     using namespace fp4gemm;
     static const hipError_t attr = [] {
         hipError_t e = allow_lds(gemm_fp4_f16_kernel<OUT, EPI>, 2 * STAGE);
@@ -884,16 +884,16 @@ static hipError_t launch_fp4_paths(hipStream_t s, const uint8_t *ca, const uint8
     const unsigned utm = (unsigned)tm, utn = (unsigned)tn;
     if (K % 256 == 0)
         return launch_fp4_dma<OUT, EPI, false>(s, gemm_fp4_dma_kernel<OUT, EPI>, gemm_fp4_split_kernel, ca, sa, ga,
-                                               cw, sw, gw, M, N, K, y, partial, spart, utm, utn);
+                                               cw, sw, gw, M, N, K, y, partial, spart, utm, utn, lora);
     if (K % 128 == 0 && K >= 384)
         return launch_fp4_dma<OUT, EPI, true>(s, gemm_fp4_dma_tail_kernel<OUT, EPI>, gemm_fp4_split_tail_kernel, ca,
-                                              sa, ga, cw, sw, gw, M, N, K, y, partial, spart, utm, utn);
+                                              sa, ga, cw, sw, gw, M, N, K, y, partial, spart, utm, utn, lora);
     if (K % (4 * 16) == 0) {
         hipLaunchKernelGGL((gemm_fp4_fast_kernel<OUT, EPI>), grid, block, 2 * STAGE, s, ca, sa, ga, cw,
-                           sw, gw, M, N, K, y, utm, utn, partial);
+                           sw, gw, M, N, K, y, utm, utn, partial, lora);
     } else {
         hipLaunchKernelGGL((gemm_fp4_f16_kernel<OUT, EPI>), grid, block, 2 * STAGE, s, ca, sa, ga, cw,
-                           sw, gw, M, N, K, y, utm, utn, partial);
+                           sw, gw, M, N, K, y, utm, utn, partial, lora);
     }
     return hipGetLastError();
 }
@@ -901,10 +901,11 @@ static hipError_t launch_fp4_paths(hipStream_t s, const uint8_t *ca, const uint8
 hipError_t launch_gemm_nvfp4(hipStream_t s, const uint8_t *ca, const uint8_t *sa,
                              const float *ga, const uint8_t *cw, const uint8_t *sw,
                              const float *gw, int64_t M, int64_t N, int64_t K, int out_dtype,
-                             void *y, int variant, int epi, float *partial, uint32_t *spart) {
+                             void *y, int variant, int epi, float *partial, uint32_t *spart,
+                             const LoraEpi *lora) {
     if (M == 0 || N == 0) return hipSuccess;
     if (variant == 1) {
-        if (epi != 0) return hipErrorInvalidValue;
+        if (epi != 0 || lora) return hipErrorInvalidValue;
         const int64_t sm = (M + fp4scaled::BM - 1) / fp4scaled::BM, sn = (N + fp4scaled::BN - 1) / fp4scaled::BN;
         const dim3 block(256);
         if (out_dtype == 0)
@@ -913,15 +914,24 @@ hipError_t launch_gemm_nvfp4(hipStream_t s, const uint8_t *ca, const uint8_t *sa
             hipLaunchKernelGGL(gemm_fp4_scaled_kernel<1>, dim3((unsigned)(sm * sn)), block, 0, s, ca, sa, ga, cw, sw, gw, M, N, K, y, (unsigned)sn);
         return hipGetLastError();
     }
-    if (out_dtype == 0 && epi == 0)
-        return launch_fp4_paths<0, 0>(s, ca, sa, ga, cw, sw, gw, M, N, K, y, partial, spart);
+    const LoraEpi le = lora ? *lora : LoraEpi{};
+    if (lora) epi |= kEpiLora;
+#define DMPQ_FP4_PATHS(OUT_, EPI_) \
+    return launch_fp4_paths<OUT_, EPI_>(s, ca, sa, ga, cw, sw, gw, M, N, K, y, partial, spart, le)
+    if (out_dtype == 0 && epi == 0) DMPQ_FP4_PATHS(0, 0);
+    if (out_dtype == 0 && epi == kEpiLora) DMPQ_FP4_PATHS(0, kEpiLora);
     if (out_dtype != 1) return hipErrorInvalidValue;
     switch (epi) {
-        case 0: return launch_fp4_paths<1, 0>(s, ca, sa, ga, cw, sw, gw, M, N, K, y, partial, spart);
-        case 1: return launch_fp4_paths<1, 1>(s, ca, sa, ga, cw, sw, gw, M, N, K, y, partial, spart);
-        case 2: return launch_fp4_paths<1, 2>(s, ca, sa, ga, cw, sw, gw, M, N, K, y, partial, spart);
-        case 3: return launch_fp4_paths<1, 3>(s, ca, sa, ga, cw, sw, gw, M, N, K, y, partial, spart);
+        case 0: DMPQ_FP4_PATHS(1, 0);
+        case 1: DMPQ_FP4_PATHS(1, 1);
+        case 2: DMPQ_FP4_PATHS(1, 2);
+        case 3: DMPQ_FP4_PATHS(1, 3);
+        case 4: DMPQ_FP4_PATHS(1, 4);
+        case 5: DMPQ_FP4_PATHS(1, 5);
+        case 6: DMPQ_FP4_PATHS(1, 6);
+        case 7: DMPQ_FP4_PATHS(1, 7);
     }
+#undef DMPQ_FP4_PATHS
     return hipErrorInvalidValue;
 }
 

@@ -83,12 +83,32 @@ constexpr int64_t kSplitMinKInt8 = 4096;
 // operand (at most 2 bytes per element) from a scalar base by 32-bit offsets.
 constexpr int64_t kMaxGemmK = int64_t(1) << 22;
 
+// ---- low-rank adapters -----------------------------------------------------
+// The rows of a batch by request (lora.hpp) and the pool's shape: R is the
+// pool's rank (a multiple of 16, at most kMaxLoraRank), rank[n] <= R and
+// scale[n] each adapter's own.
+struct LoraBatch {
+    const int32_t *rank;
+    const float *scale;
+    const int32_t *seg_start, *seg_adapter;
+    int M, R, S, nA;
+};
+constexpr int kMaxLoraRank = 128;
+// The adapter term of a GEMM's epilogue: y += scale * t b^T by request
+// (t [M x R] fp32, b [n x N x R] bf16).
+struct LoraEpi {
+    const float *t;
+    const uint16_t *b;
+    LoraBatch batch;
+};
+
 // epi: bit 0 GELU, bit 1 fused NVFP4 amax of the output into partial[tile]
 // (bf16 output only); the GEMM tile is 256 x 256 on every path.  spart: the
-// split area (kSplitAreaBytes), or NULL to run every tile whole.
+// split area (kSplitAreaBytes), or NULL to run every tile whole.  lora: the
+// adapter term added before the epilogue's rounding, or NULL.
 hipError_t launch_gemm_int8(hipStream_t s, const int8_t *qa, const float *sa, const int8_t *qw,
                             const float *sw, int64_t M, int64_t N, int64_t K, int out_dtype,
-                            void *y, int epi, float *partial, uint32_t *spart);
+                            void *y, int epi, float *partial, uint32_t *spart, const LoraEpi *lora = nullptr);
 // The INT8 GEMM against an NVFP4 weight (cw, sw, gw) converted to INT8 in
 // the weight-tile load with the row scales of launch_w8_row_scales; the
 // same result as launch_gemm_int8 on the converted weight.  K % 128 == 0;
@@ -99,13 +119,13 @@ hipError_t launch_gemm_int8_w4(hipStream_t s, const int8_t *qa, const float *sa,
                                void *y, int epi, float *partial);
 hipError_t launch_gemm_bf16(hipStream_t s, const uint16_t *x, const uint16_t *w, int64_t M,
                             int64_t N, int64_t K, int out_dtype, void *y, int epi, float *partial,
-                            uint32_t *spart);
+                            uint32_t *spart, const LoraEpi *lora = nullptr);
 // Fixup of a split launch with fp32 accumulators: y = (sum * gA) * gW (gA, gW
 // read from device memory; NULL reads as 1).
 hipError_t launch_f32_fixup(hipStream_t s, const float *ga, const float *gw, int64_t M, int64_t N,
                             void *y, unsigned tiles_m, unsigned tiles_n, unsigned group_m,
                             float *partial, const SplitPlan &sp, const uint32_t *spart,
-                            int out_dtype, int epi);
+                            int out_dtype, int epi, const LoraEpi *lora);
 hipError_t launch_outlier_count(hipStream_t s, const uint16_t *x, int64_t M, int64_t K,
                                 double kappa, double *count, const Workspace &ws);
 // Sum ns values per partial over nparts partials, in a fixed order, into out[ns].
@@ -114,7 +134,46 @@ hipError_t launch_finalize_sums(hipStream_t s, const double *partial, int nparts
 hipError_t launch_gemm_nvfp4(hipStream_t s, const uint8_t *ca, const uint8_t *sa,
                              const float *ga, const uint8_t *cw, const uint8_t *sw,
                              const float *gw, int64_t M, int64_t N, int64_t K, int out_dtype,
-                             void *y, int variant, int epi, float *partial, uint32_t *spart);
+                             void *y, int variant, int epi, float *partial, uint32_t *spart,
+                             const LoraEpi *lora = nullptr);
+
+// ---- low-rank adapters: launchers ------------------------------------------
+// t = x a^T by request (fp32, [M x R])
+hipError_t launch_lora_shrink(hipStream_t s, const uint16_t *x, const uint16_t *a, const LoraBatch &B, int64_t K,
+                              float *t);
+// y = base + scale * t b^T by request; base NULL reads as 0; base may be y
+hipError_t launch_lora_expand(hipStream_t s, const float *t, const void *base, const uint16_t *b,
+                              const LoraBatch &B, int64_t N, int out_dtype, void *y);
+size_t lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t S, int64_t nA);
+hipError_t launch_lora_backward(hipStream_t s, const uint16_t *dy, const uint16_t *x, const float *t,
+                                const uint16_t *a, const uint16_t *b, const LoraBatch &B, int64_t N, int64_t K,
+                                const uint16_t *dx_base, uint16_t *dx, float *da, float *db, void *ws);
+
+// ---- AdamW over many tensors -------------------------------------------------
+// A device table: the tensors, then the tensor of each chunk of kAdamwChunk
+// values (chunks are numbered tensor by tensor).
+struct AdamwTensor {
+    void *p;
+    const void *g;
+    void *m, *v;
+    float *ms, *vs;
+    uint16_t *copy;
+    int64_t n, first_chunk;
+};
+constexpr int kAdamwChunk = 4096;
+constexpr int kAdamwBlock = 256;  // values that share a scale of 8-bit states
+struct AdamwTable {
+    const AdamwTensor *tensors;
+    const int32_t *chunk_tensor;
+    int64_t chunks;
+    int p_dtype, g_dtype, state_bits;
+};
+struct AdamwHyper {
+    float beta1, omb1, beta2, omb2, eps, rbc2, decay, step;
+    double max_norm;
+};
+hipError_t launch_grad_norm(hipStream_t s, const AdamwTable &t, double *norm, const Workspace &ws);
+hipError_t launch_adamw(hipStream_t s, const AdamwTable &t, const AdamwHyper &h, const double *norm);
 
 // Per-code (lowest, highest, count) of input bit patterns in [lo, hi) for the
 // device converters (codec 0: E4M3 encoder; 1: hardware E2M1 converter).

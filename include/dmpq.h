@@ -92,7 +92,8 @@ enum { DMPQ_TDC_SKIP = 0, DMPQ_TDC_REFRESH = 1 };
 enum { DMPQ_FP4_BF16_DEQUANT = 0, DMPQ_FP4_SCALED_MFMA = 1 };
 /* Workspace users. */
 enum { DMPQ_OP_GAMMA = 0, DMPQ_OP_QUANT_NVFP4 = 1, DMPQ_OP_TDC = 2, DMPQ_OP_PREP_WEIGHT = 3,
-       DMPQ_OP_OUTLIER = 4, DMPQ_OP_GEMM_AMAX = 5, DMPQ_OP_GEMM = 6, DMPQ_OP_GEMM_W4 = 7 };
+       DMPQ_OP_OUTLIER = 4, DMPQ_OP_GEMM_AMAX = 5, DMPQ_OP_GEMM = 6, DMPQ_OP_GEMM_W4 = 7,
+       DMPQ_OP_GRAD_NORM = 8 };
 
 /* Message describing the calling thread's last error ("" if none). */
 const char *dmpq_last_error(void);
@@ -410,6 +411,133 @@ dmpq_status dmpq_gemm_bf16_ex(hipStream_t stream, const uint16_t *x, const uint1
 enum { DMPQ_CODEC_E4M3 = 0, DMPQ_CODEC_E2M1 = 1 };
 dmpq_status dmpq_selftest_codec(hipStream_t stream, int codec, uint32_t lo, uint32_t hi,
                                 uint32_t *d_stats);
+
+/* ===========================================================================
+ * Low-rank adapters beside a shared linear.  The linear itself is frozen (and
+ * usually quantized); each request of a batch adds its own adapter's
+ * scale * (x a^T) b^T, on the activations x before they are rotated and
+ * quantized.  The method's pages do not treat adapters: this group is the
+ * library's own.
+ *
+ * Pool: n adapters of a common padded rank R (a multiple of 16, at most 128):
+ *   a [n x R x K] bf16, b [n x N x R] bf16, rank [n] int32 (the adapter's own,
+ *   0 .. R; others are taken as the nearest of these), scale [n] fp32.  What
+ *   a and b hold past an adapter's rank is ignored, whatever it is.
+ * Batch: M rows of S requests.  Request s owns the rows seg_start[s] ..
+ *   seg_start[s+1]-1 (int32 [S+1], ascending, on the device) and uses adapter
+ *   seg_adapter[s] (int32 [S]; negative or >= n: none).  A request may be
+ *   empty, several may share an adapter, and rows before seg_start[0] or from
+ *   seg_start[S] on have no adapter.  Boundaries outside 0 .. M are clamped;
+ *   if they do not ascend the results are unspecified, and no access is out
+ *   of bounds.
+ * Sums are fp32 in a fixed order (the same bits on every call).  t is fp32;
+ * where it enters a product it is split into bf16 parts that keep 16 bits of
+ * it for a bf16 result and all 24 for an fp32 one.  A value that is not finite
+ * stays within its own row (forward) or its own adapter (gradients).
+ * ========================================================================= */
+
+/* t [M x R] fp32 = x a^T, each row through its own adapter's a; zeros past the
+ * adapter's rank and in rows without adapter.  x [M x K] bf16. */
+dmpq_status dmpq_lora_shrink(hipStream_t stream, const uint16_t *x, const uint16_t *a,
+                             const int32_t *rank, const int32_t *seg_start,
+                             const int32_t *seg_adapter, int64_t M, int64_t K, int64_t R, int64_t S,
+                             int64_t n_adapters, float *t);
+/* t as above, and y [M x N] = base + scale * t b^T (out_dtype F32 or BF16, of
+ * base and y both).  base may be y (in place) or NULL (zeros); rows without
+ * adapter are base bit for bit.  N >= 0 is any. */
+dmpq_status dmpq_lora_forward(hipStream_t stream, const uint16_t *x, const void *base,
+                              const uint16_t *a, const uint16_t *b, const int32_t *rank,
+                              const float *scale, const int32_t *seg_start,
+                              const int32_t *seg_adapter, int64_t M, int64_t N, int64_t K, int64_t R,
+                              int64_t S, int64_t n_adapters, int out_dtype, float *t, void *y);
+/* The *_ex GEMMs with the adapter term in their epilogue: y = projection +
+ * scale * t b^T in fp32, then the epilogue (GELU, amax) and the rounding, in
+ * one pass over y.  t comes from dmpq_lora_shrink on the same batch; out_dtype
+ * F32 or BF16; the other arguments are those of the *_ex entry points. */
+dmpq_status dmpq_gemm_bf16_lora(hipStream_t stream, const uint16_t *x, const uint16_t *w,
+                                const float *t, const uint16_t *b, const int32_t *rank,
+                                const float *scale, const int32_t *seg_start,
+                                const int32_t *seg_adapter, int64_t M, int64_t N, int64_t K,
+                                int64_t R, int64_t S, int64_t n_adapters, int out_dtype, void *y,
+                                int epilogue, void *ws, size_t ws_bytes);
+dmpq_status dmpq_qgemm_int8_lora(hipStream_t stream, const int8_t *qa, const float *sa,
+                                 const int8_t *qw, const float *sw, const float *t,
+                                 const uint16_t *b, const int32_t *rank, const float *scale,
+                                 const int32_t *seg_start, const int32_t *seg_adapter, int64_t M,
+                                 int64_t N, int64_t K, int64_t R, int64_t S, int64_t n_adapters,
+                                 int out_dtype, void *y, int epilogue, void *ws, size_t ws_bytes);
+dmpq_status dmpq_qgemm_nvfp4_lora(hipStream_t stream, const uint8_t *ca, const uint8_t *sa,
+                                  const float *d_ga, const uint8_t *cw, const uint8_t *sw,
+                                  const float *d_gw, const float *t, const uint16_t *b,
+                                  const int32_t *rank, const float *scale, const int32_t *seg_start,
+                                  const int32_t *seg_adapter, int64_t M, int64_t N, int64_t K,
+                                  int64_t R, int64_t S, int64_t n_adapters, int out_dtype, void *y,
+                                  int epilogue, void *ws, size_t ws_bytes);
+/* Gradients.  dy [M x N] bf16, x [M x K] bf16 and t (of the forward pass):
+ *   u  = scale * dy b          (per request; not stored for the caller)
+ *   dx = dx_base + u a         [M x K] bf16; dx_base may be dx or NULL (zeros);
+ *                              dx NULL: not computed
+ *   da = sum of u^T x          [n x R x K] fp32, over all rows of each adapter
+ *   db = sum of scale * dy^T t [n x N x R] fp32
+ * da and db are written whole: zeros past a rank and for adapters without
+ * rows.  N must be a multiple of 16 (it is summed over).  ws:
+ * dmpq_lora_backward_bytes() bytes. */
+size_t dmpq_lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t S,
+                                int64_t n_adapters);
+dmpq_status dmpq_lora_backward(hipStream_t stream, const uint16_t *dy, const uint16_t *x,
+                               const float *t, const uint16_t *a, const uint16_t *b,
+                               const int32_t *rank, const float *scale, const int32_t *seg_start,
+                               const int32_t *seg_adapter, const uint16_t *dx_base, int64_t M,
+                               int64_t N, int64_t K, int64_t R, int64_t S, int64_t n_adapters,
+                               uint16_t *dx, float *da, float *db, void *ws, size_t ws_bytes);
+
+/* ===========================================================================
+ * AdamW over many tensors in one launch (Loshchilov and Hutter: decoupled
+ * weight decay).  With g' = clip * g and t = step, all in fp32, each operation
+ * rounded by itself:
+ *   m = beta1 m + (1 - beta1) g'          v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * Tensors of a table share their types: p fp32 or bf16 (in place; a bf16 p is
+ * rounded to nearest even each step), g fp32 or bf16, states of 32 or 8 bits,
+ * and copy, a bf16 copy of the new p (NULL: none).
+ * 8-bit states: m and v are uint8 [n]; each 256 consecutive values (the last
+ * block of a tensor may be shorter) share a scale, ms and vs fp32
+ * [ceil(n / 256)]: m = E4M3(m code) * ms with ms = max |m| / 448, and
+ * v = (E4M3(v code) * vs)^2 with vs = max sqrt(v) / 448; a v that is not zero
+ * keeps at least the smallest code.  All zeros is the start of both forms.
+ * A gradient that is not finite makes its value (8 bits: an infinity, its
+ * block) NaN for good, unless the step is guarded by the norm.
+ * ========================================================================= */
+typedef struct dmpq_adamw_tensor {
+    void *p;
+    const void *g;
+    void *m, *v;
+    float *ms, *vs; /* 8-bit states only */
+    uint16_t *copy;
+    int64_t n;
+} dmpq_adamw_tensor;
+/* Bytes of a table of the n_tensors tensors, 0 if a size is negative or the
+ * tensors are too many or too large (2^31 chunks of 4096 values). */
+size_t dmpq_adamw_table_bytes(const dmpq_adamw_tensor *h_tensors, int64_t n_tensors);
+/* Host, pure: fills h_table (the caller copies it to the device, 16-byte
+ * aligned, and keeps it as long as the tensors keep their places).  p_dtype
+ * and g_dtype: DMPQ_OUT_F32 or DMPQ_OUT_BF16; state_bits 32 or 8.  Pointers of
+ * tensors are 16-byte aligned, ms and vs 4-byte.  h_chunks: the number of
+ * chunks, which the calls below take. */
+dmpq_status dmpq_adamw_table(const dmpq_adamw_tensor *h_tensors, int64_t n_tensors, int p_dtype,
+                             int g_dtype, int state_bits, void *h_table, size_t table_bytes,
+                             int64_t *h_chunks);
+/* d_norm[0] = sqrt of the sum of all squared gradients (fp64, the same bits on
+ * every call).  ws: dmpq_workspace_bytes(DMPQ_OP_GRAD_NORM, 0, 0) bytes. */
+dmpq_status dmpq_grad_norm(hipStream_t stream, const void *d_table, int64_t n_tensors, int64_t chunks,
+                           int g_dtype, double *d_norm, void *ws, size_t ws_bytes);
+/* One step.  d_norm NULL: clip = 1.  Otherwise clip = max_norm / norm where
+ * norm > max_norm > 0, else 1, and a norm that is not finite leaves every
+ * tensor as it is.  step >= 1. */
+dmpq_status dmpq_adamw_step(hipStream_t stream, const void *d_table, int64_t n_tensors,
+                            int64_t chunks, int p_dtype, int g_dtype, int state_bits, double lr,
+                            double beta1, double beta2, double eps, double weight_decay,
+                            int64_t step, const double *d_norm, double max_norm);
 
 #ifdef __cplusplus
 }
