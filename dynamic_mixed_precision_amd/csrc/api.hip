@@ -537,8 +537,11 @@ static dmpq_status check_lora(const char *fn, int64_t M, int64_t N, int64_t K, i
     if (dmpq_status s = check_k(fn, K)) return s;
     if (R > kMaxLoraRank)
         return fail(DMPQ_ERR_UNSUPPORTED, "%s: R = %lld exceeds %d", fn, (long long)R, kMaxLoraRank);
-    if (M > INT32_MAX / 2 || N > INT32_MAX / 2 || K > INT32_MAX / 2 || S > INT32_MAX / 4 || n_adapters > INT32_MAX / 2)
-        return fail(DMPQ_ERR_UNSUPPORTED, "%s: M, N, K, S or n_adapters too large", fn);
+    if (M > INT32_MAX / 2 || S > INT32_MAX / 4 || n_adapters > INT32_MAX / 2)
+        return fail(DMPQ_ERR_UNSUPPORTED, "%s: M, S or n_adapters too large", fn);
+    if (N > kMaxLoraWidth || K > kMaxLoraWidth)
+        return fail(DMPQ_ERR_UNSUPPORTED, "%s: N = %lld or K = %lld exceeds %lld", fn, (long long)N, (long long)K,
+                    (long long)kMaxLoraWidth);
     REQUIRE_PTR_NF(fn, rank, n_adapters);
     REQUIRE_PTR_NF(fn, scale, scaled ? n_adapters : 0);
     REQUIRE_PTR_NF(fn, seg_start, 1);
@@ -663,8 +666,8 @@ dmpq_status dmpq_qgemm_nvfp4_lora(hipStream_t stream, const uint8_t *ca, const u
 size_t dmpq_lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t S,
                                 int64_t n_adapters) {
     const int64_t most = INT32_MAX / 2;
-    if (M < 0 || N < 0 || K < 0 || R < 0 || S < 0 || n_adapters < 0 || M > most || N > most || K > most ||
-        R > kMaxLoraRank || S > most / 2 || n_adapters > most)
+    if (M < 0 || N < 0 || K < 0 || R < 0 || S < 0 || n_adapters < 0 || M > most || N > kMaxLoraWidth ||
+        K > kMaxLoraWidth || R > kMaxLoraRank || S > most / 2 || n_adapters > most)
         return 0;
     return lora_backward_bytes(M, N, K, R, S, n_adapters);
 }

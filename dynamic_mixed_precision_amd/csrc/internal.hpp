@@ -94,6 +94,9 @@ struct LoraBatch {
     int M, R, S, nA;
 };
 constexpr int kMaxLoraRank = 128;
+// Widest K and N of the adapter calls: rows of a tile are addressed from a
+// scalar base by 32-bit offsets.
+constexpr int64_t kMaxLoraWidth = int64_t(1) << 26;
 // The adapter term of a GEMM's epilogue: y += scale * t b^T by request
 // (t [M x R] fp32, b [n x N x R] bf16).
 struct LoraEpi {

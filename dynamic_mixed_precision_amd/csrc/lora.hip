@@ -13,6 +13,7 @@
 // Sums are fp32 in a fixed order: no atomics, the same bits on every call.
 #include "device.hpp"
 #include "gemm_common.hpp"
+#include "gemm_dma.hpp"
 #include "internal.hpp"
 #include "lora.hpp"
 
@@ -23,13 +24,17 @@ namespace {
 __device__ __forceinline__ v4i ld16(const void *p) { return *reinterpret_cast<const v4i *>(p); }
 
 // ---------------------------------------------------------------------------
-// Shrink: t[m, j] = sum_k x[m, k] a[j, k] for a tile of 16 RT rows of one
-// request and 16 RC of its ranks (part blockIdx.y).  The WAVES waves share the
-// K steps of 32 (16x16x32 MFMA, fragments straight from global memory: lane l
-// holds 8 k of row l % 16, so a row's 64 bytes are one segment) and their sums
-// meet in LDS, added in wave order.  UP: the same product for u = scale dy b
-// (x is dy, a the transposed b), stored times scale, and once more as 3 bf16
-// parts [part][j][m] for the gradients' products over m.
+// Shrink: t[m, j] = sum_k x[m, k] a[j, k] for `tile` <= 16 RT rows of one
+// request and 16 RC of its ranks (part blockIdx.y).  The WAVES waves share K
+// in stages of 64: a wave loads whole 128-byte lines (8 lanes a row) of its
+// own stages, two stages ahead in registers, passes them through an LDS area
+// of its own (no barrier) and reads them back as 16x16x32 MFMA fragments.
+// Loading the fragments straight from memory, where neighbouring lanes hold
+// different rows, ran at 1.9 TB/s however many loads were in flight.  The
+// waves' sums meet in LDS at the end, added in wave order.  UP: the same
+// product for u = scale dy b (x is dy, a the transposed b), stored times
+// scale, and once more as 3 bf16 parts [part][j][m] for the gradients'
+// products over m.
 // ---------------------------------------------------------------------------
 struct PackedOut {
     uint16_t *p;   // [3][R][ld]
@@ -39,75 +44,103 @@ struct PackedOut {
 template <int RT, int RC, int WAVES, bool UP>
 __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(const uint16_t *__restrict__ x,
                                                                  const uint16_t *__restrict__ a, LoraBatch B,
-                                                                 int64_t K, float *__restrict__ t, PackedOut pk) {
-    constexpr int TM = 16 * RT, TJ = 16 * RC;
-    __shared__ float part[WAVES][TM][TJ + 4];
+                                                                 int64_t K, int tile, float *__restrict__ t,
+                                                                 PackedOut pk) {
+    constexpr int TM = 16 * RT, TJ = 16 * RC, ROWS = TM + TJ, LOADS = ROWS / 8;
+    constexpr int STRIDE = TJ + 4;  // of the sums
+    constexpr int STAGE = ROWS * 128, SUMS = TM * STRIDE * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[WAVES * (STAGE > SUMS ? STAGE : SUMS)];
     SegTile st;
-    if (!seg_tile(B, blockIdx.x, TM, st)) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (!seg_tile(B, blockIdx.x, tile, st)) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j0 = blockIdx.y * TJ;
     const int rank = st.adapter < 0 ? 0 : adapter_rank(B, st.adapter);
+    float *part = reinterpret_cast<float *>(lds);
     if (rank > j0) {  // workgroup-uniform
         const int c = lane & 15, q = lane >> 4;
-        const uint16_t *xr[RT], *ar[RC];
+        const int lr = lane >> 3, lc = lane & 7;  // the lane's row of 8 and its 16-byte piece of a stage
+        const uint16_t *src[LOADS];
 #pragma unroll
-        for (int i = 0; i < RT; i++) {
-            const int r = 16 * i + c;
-            xr[i] = x + (int64_t)(st.row0 + (r < st.rows ? r : st.rows - 1)) * K + 8 * q;
-        }
-#pragma unroll
-        for (int i = 0; i < RC; i++) {
-            const int j = j0 + 16 * i + c;
-            ar[i] = a + ((int64_t)st.adapter * B.R + (j < B.R ? j : B.R - 1)) * K + 8 * q;
+        for (int i = 0; i < LOADS; i++) {
+            const int r = 8 * i + lr;
+            if (r < TM) {
+                src[i] = x + (int64_t)(st.row0 + (r < st.rows ? r : st.rows - 1)) * K + 8 * lc;
+            } else {
+                const int jj = j0 + r - TM;
+                src[i] = a + ((int64_t)st.adapter * B.R + (jj < B.R ? jj : B.R - 1)) * K + 8 * lc;
+            }
         }
         v4f acc[RT][RC];
 #pragma unroll
         for (int i = 0; i < RT; i++)
 #pragma unroll
             for (int k = 0; k < RC; k++) acc[i][k] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-        const int64_t full = K / 32;  // whole steps; K % 32 == 16 leaves half a step to the last wave
-        const int64_t k1 = full * (wave + 1) / WAVES;
-#pragma unroll 4
-        for (int64_t s = full * wave / WAVES; s < k1; s++) {
-            v4i xf[RT], af[RC];
+        const int stages = (int)((K + 63) / 64);
+        uint8_t *own = lds + wave * STAGE;
+        // a piece past K (the last stage of a K that is no multiple of 64) is
+        // loaded from the stage's first piece and written as zeros
+        auto load = [&](v4i(&v)[LOADS], int s) {
+            const int64_t o = 64 * (int64_t)s - (64 * (int64_t)s + 8 * lc < K ? 0 : 8 * lc);
 #pragma unroll
-            for (int i = 0; i < RT; i++) xf[i] = ld16(xr[i] + 32 * s);
+            for (int i = 0; i < LOADS; i++) v[i] = ld16(src[i] + o);
+        };
+        auto use = [&](v4i(&v)[LOADS], int s) {
+            const bool in = 64 * (int64_t)s + 8 * lc < K;
 #pragma unroll
-            for (int i = 0; i < RC; i++) af[i] = ld16(ar[i] + 32 * s);
+            for (int i = 0; i < LOADS; i++)
+                *reinterpret_cast<v4i *>(own + (8 * i + lr) * 128 + swz128(8 * i + lr, lc) * 16) =
+                    in ? v[i] : (v4i){0, 0, 0, 0};
+        };
+        auto mul = [&]() {
 #pragma unroll
-            for (int i = 0; i < RT; i++)
+            for (int u = 0; u < 2; u++) {
+                v4i xf[RT], af[RC];
 #pragma unroll
-                for (int k = 0; k < RC; k++) acc[i][k] = mfma16(af[k], xf[i], acc[i][k]);
+                for (int i = 0; i < RT; i++)
+                    xf[i] = *reinterpret_cast<const v4i *>(own + (16 * i + c) * 128 + swz128(c, 4 * u + q) * 16);
+#pragma unroll
+                for (int k = 0; k < RC; k++)
+                    af[k] = *reinterpret_cast<const v4i *>(own + (TM + 16 * k + c) * 128 + swz128(c, 4 * u + q) * 16);
+#pragma unroll
+                for (int i = 0; i < RT; i++)
+#pragma unroll
+                    for (int k = 0; k < RC; k++) acc[i][k] = mfma16(af[k], xf[i], acc[i][k]);
+            }
+        };
+        v4i va[LOADS], vb[LOADS];
+        // every WAVES-th stage: at a time the workgroup reads WAVES neighbouring
+        // lines of each row
+        if (wave < stages) load(va, wave);
+        if (wave + WAVES < stages) load(vb, wave + WAVES);
+        for (int s = wave; s < stages; s += 2 * WAVES) {
+            use(va, s);
+            if (s + 2 * WAVES < stages) load(va, s + 2 * WAVES);
+            mul();
+            if (s + WAVES < stages) {
+                use(vb, s + WAVES);
+                if (s + 3 * WAVES < stages) load(vb, s + 3 * WAVES);
+                mul();
+            }
         }
-        if (wave == WAVES - 1 && (K & 16)) {
-            v4i xf[RT], af[RC];
-            const v4i zero = {0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < RT; i++) xf[i] = q < 2 ? ld16(xr[i] + 32 * full) : zero;
-#pragma unroll
-            for (int i = 0; i < RC; i++) af[i] = q < 2 ? ld16(ar[i] + 32 * full) : zero;
-#pragma unroll
-            for (int i = 0; i < RT; i++)
-#pragma unroll
-                for (int k = 0; k < RC; k++) acc[i][k] = mfma16(af[k], xf[i], acc[i][k]);
-        }
+        __syncthreads();  // the stages' LDS becomes the sums'
         // D: lane column = token, registers = 4 consecutive ranks
 #pragma unroll
         for (int i = 0; i < RT; i++)
 #pragma unroll
             for (int k = 0; k < RC; k++)
-                *reinterpret_cast<v4f *>(&part[wave][16 * i + c][16 * k + 4 * q]) = acc[i][k];
+                *reinterpret_cast<v4f *>(part + (wave * TM + 16 * i + c) * STRIDE + 16 * k + 4 * q) = acc[i][k];
     }
     __syncthreads();
     const float sc = UP && st.adapter >= 0 ? B.scale[st.adapter] : 1.0f;
     for (int e = threadIdx.x; e < TM * TJ; e += 64 * WAVES) {
-        const int r = e / TJ, j = e % TJ;
+        // UP: lanes along the rows, as the parts are stored
+        const int r = UP ? e % TM : e / TJ, j = UP ? e / TM : e % TJ;
         if (r >= st.rows || j0 + j >= B.R) continue;
         float v = 0.0f;
         if (j0 + j < rank) {
-            v = part[0][r][j];
+            v = part[r * STRIDE + j];
 #pragma unroll
-            for (int w = 1; w < WAVES; w++) v += part[w][r][j];
+            for (int w = 1; w < WAVES; w++) v += part[(w * TM + r) * STRIDE + j];
             v *= sc;
         }
         t[(int64_t)(st.row0 + r) * B.R + j0 + j] = v;
@@ -125,133 +158,173 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(const uint16_t 
 }
 
 // ---------------------------------------------------------------------------
-// Expand: y = base + scale t b^T for a tile of 32 rows of one request.  A wave
-// keeps its rows' t as MFMA fragments (2 bf16 parts for a bf16 y, 3 for fp32)
-// and walks over 128-column blocks: the block's base rows are loaded first
-// (row-contiguous, 16 bytes per lane), the 32x32x16 MFMAs with b's rows as
-// the first operand leave each lane 4 consecutive columns of one row, the
-// wave's LDS band turns them row-contiguous, and base + scale * delta goes out
-// in 16-byte pieces.
+// Expand: y = base + scale t b^T for 128 rows of one request, 32 to each wave,
+// and 128 columns.  A workgroup does one such block and ends: base and y are
+// all the traffic, and a wave that goes on to another block waits for its
+// stores before the next loads (one counter holds both), which a copy of the
+// same shape showed to cost a quarter to a third (5.0 TB/s against 3.8 with
+// four blocks a workgroup, at 17776 x 12288 bf16).  Neighbouring workgroups
+// take neighbouring columns (rows first: 4.5 TB/s).  The block's b, one
+// contiguous piece of memory, goes through registers into LDS, entries past
+// the rank as zeros.  t, as 2 bf16 parts for a bf16 y and 3 for fp32, is the
+// 32x32x16 MFMA's first operand, so a lane's 16 accumulators are 16 rows of
+// one column; the second operand of MFMA p holds b's rows n0 + 4 i + p for
+// lanes i, so the four MFMAs leave every lane four consecutive columns of
+// those rows, and base and y move in 8- or 16-byte pieces, 32 lanes a row,
+// straight between memory and registers.
 // ---------------------------------------------------------------------------
-template <int ES>
-__device__ __forceinline__ void expand_piece(const float *d, float sc, const void *base, void *y, int64_t at, bool vec,
-                                             int left) {
-    constexpr int PER = 16 / ES;
-    const uint8_t *bp = static_cast<const uint8_t *>(base) + at * ES;
-    uint8_t *yp = static_cast<uint8_t *>(y) + at * ES;
-    if (vec && left >= PER) {
-        const uint4 bv = base ? *reinterpret_cast<const uint4 *>(bp) : make_uint4(0u, 0u, 0u, 0u);
-        uint4 o;
-        if constexpr (ES == 2) {
-            o.x = cvt_pk_bf16(bf16_lo(bv.x) + sc * d[0], bf16_hi(bv.x) + sc * d[1]);
-            o.y = cvt_pk_bf16(bf16_lo(bv.y) + sc * d[2], bf16_hi(bv.y) + sc * d[3]);
-            o.z = cvt_pk_bf16(bf16_lo(bv.z) + sc * d[4], bf16_hi(bv.z) + sc * d[5]);
-            o.w = cvt_pk_bf16(bf16_lo(bv.w) + sc * d[6], bf16_hi(bv.w) + sc * d[7]);
-        } else {
-            o.x = __float_as_uint(__uint_as_float(bv.x) + sc * d[0]);
-            o.y = __float_as_uint(__uint_as_float(bv.y) + sc * d[1]);
-            o.z = __float_as_uint(__uint_as_float(bv.z) + sc * d[2]);
-            o.w = __float_as_uint(__uint_as_float(bv.w) + sc * d[3]);
-        }
-        *reinterpret_cast<uint4 *>(yp) = o;
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < PER; e++) {
-        if (e >= left) break;
-        if constexpr (ES == 2) {
-            const float b = base ? bf16_lo(reinterpret_cast<const uint16_t *>(bp)[e]) : 0.0f;
-            reinterpret_cast<uint16_t *>(yp)[e] = (uint16_t)cvt_pk_bf16(b + sc * d[e], 0.0f);
-        } else {
-            const float b = base ? reinterpret_cast<const float *>(bp)[e] : 0.0f;
-            reinterpret_cast<float *>(yp)[e] = b + sc * d[e];
-        }
-    }
-}
+constexpr int kExpandRows = 128, kExpandCols = 128, kExpandWaves = 4;
 
-constexpr int kExpandRows = 32, kExpandCols = 128, kExpandWaves = 4;
+// Four values of base or y.  Rows of an odd N start anywhere, so the accesses
+// ask for no more than the value's own alignment (the hardware takes them).
+template <int ES>
+struct Quad {
+    typedef uint32_t V __attribute__((ext_vector_type(ES), aligned(ES)));
+    V v;
+    static __device__ __forceinline__ Quad load(const uint8_t *p) {
+        return Quad{__builtin_nontemporal_load(reinterpret_cast<const V *>(p))};
+    }
+    __device__ __forceinline__ void store(uint8_t *p) const { __builtin_nontemporal_store(v, reinterpret_cast<V *>(p)); }
+    // the first n < 4 values
+    static __device__ __forceinline__ Quad load_some(const uint8_t *p, int n) {
+        Quad q = zero();
+        if constexpr (ES == 2) {
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+            q.v[0] = h[0] | (n > 1 ? (uint32_t)h[1] << 16 : 0u);
+            if (n > 2) q.v[1] = h[2];
+        } else {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
+            q.v[0] = w[0];
+            if (n > 1) q.v[1] = w[1];
+            if (n > 2) q.v[2] = w[2];
+        }
+        return q;
+    }
+    __device__ __forceinline__ void store_some(uint8_t *p, int n) const {
+        if constexpr (ES == 2) {
+            uint16_t *h = reinterpret_cast<uint16_t *>(p);
+            h[0] = (uint16_t)v[0];
+            if (n > 1) h[1] = (uint16_t)(v[0] >> 16);
+            if (n > 2) h[2] = (uint16_t)v[1];
+        } else {
+            uint32_t *w = reinterpret_cast<uint32_t *>(p);
+            w[0] = v[0];
+            if (n > 1) w[1] = v[1];
+            if (n > 2) w[2] = v[2];
+        }
+    }
+    static __device__ __forceinline__ Quad zero() {
+        Quad q;
+#pragma unroll
+        for (int e = 0; e < ES; e++) q.v[e] = 0u;
+        return q;
+    }
+    __device__ __forceinline__ Quad plus(float sc, float d0, float d1, float d2, float d3) const {
+        Quad q;
+        if constexpr (ES == 2) {
+            q.v[0] = cvt_pk_bf16(bf16_lo(v[0]) + sc * d0, bf16_hi(v[0]) + sc * d1);
+            q.v[1] = cvt_pk_bf16(bf16_lo(v[1]) + sc * d2, bf16_hi(v[1]) + sc * d3);
+        } else {
+            q.v[0] = __float_as_uint(__uint_as_float(v[0]) + sc * d0);
+            q.v[1] = __float_as_uint(__uint_as_float(v[1]) + sc * d1);
+            q.v[2] = __float_as_uint(__uint_as_float(v[2]) + sc * d2);
+            q.v[3] = __float_as_uint(__uint_as_float(v[3]) + sc * d3);
+        }
+        return q;
+    }
+};
 
 template <int ES, int RC>
-__global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(const float *__restrict__ t,
-                                                                        const void *base, const uint16_t *__restrict__ b,
-                                                                        LoraBatch B, int64_t N, int blocks, void *y) {
+__global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const float *__restrict__ t,
+                                                                           const void *base,
+                                                                           const uint16_t *__restrict__ b, LoraBatch B,
+                                                                           int64_t N, unsigned cols, void *y) {
     constexpr int NS = ES == 2 ? 2 : 3;
-    constexpr int PER = 16 / ES, LPR = kExpandCols / PER, RPP = 64 / LPR;  // lanes a row, rows a pass
-    constexpr int STRIDE = kExpandCols + 4;
-    __shared__ float band[kExpandWaves][kExpandRows * STRIDE];
+    // b's row 4 i + p of the block lies at LDS row 32 p + i; 16 bytes of
+    // padding spread the lanes' 16-byte reads over the banks
+    constexpr int ROW = 32 * RC + 16;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kExpandCols * ROW];
+    typedef Quad<ES> Q;
+    const unsigned tile = blockIdx.x / cols, cb = blockIdx.x - tile * cols;
     SegTile st;
-    if (!seg_tile(B, blockIdx.x, kExpandRows, st)) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int lm = lane & 31, lh = lane >> 5;
-    const int rank = st.adapter < 0 ? 0 : adapter_rank(B, st.adapter);
-    if (rank == 0 && base == y) return;
-    // rows of no adapter: base + 1 * -0, which is base bit for bit
-    const float sc = rank == 0 || !B.scale ? 1.0f : B.scale[st.adapter];
-    const bool vec = ((N * ES) & 15) == 0;
-    v4i tf[RC][NS];
-    if (rank > 0) {
-        const float *tr = t + (int64_t)(st.row0 + (lm < st.rows ? lm : st.rows - 1)) * B.R + 8 * lh;
+    if (!seg_tile(B, (int)tile, kExpandRows, st)) return;
+    if (st.adapter < 0 && base == y) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 31, lh = lane >> 5;
+    const int row0 = st.row0 + 32 * wave, wrows = st.rows - 32 * wave;  // this wave's; <= 0: none
+    // row of accumulator r: 8 (r / 4) + r % 4 from a scalar base, + 4 lh and
+    // the column in the lane's 32-bit offset (N <= 2^26)
+    const int64_t ld = N * ES, coff = (int64_t)cb * kExpandCols * ES;
+    const uint8_t *bp = static_cast<const uint8_t *>(base) + row0 * ld + coff;
+    uint8_t *yp = static_cast<uint8_t *>(y) + row0 * ld + coff;
+    const uint32_t lane_off = (uint32_t)(4 * lh * ld + 4 * li * ES);
+    const int rows = wrows - 4 * lh;
+    const int left = (int)(N - (int64_t)cb * kExpandCols) - 4 * li;  // the lane's columns
+    Q bv[16];
+#pragma unroll
+    for (int r = 0; r < 16; r++) {
+        const int m = 8 * (r >> 2) + (r & 3);
+        bv[r] = Q::zero();
+        if (base && m < rows && left > 0)
+            bv[r] = left >= 4 ? Q::load(bp + m * ld + lane_off) : Q::load_some(bp + m * ld + lane_off, left);
+    }
+    v16f acc[4];
+    float sc = 1.0f;
+#pragma unroll
+    for (int p = 0; p < 4; p++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) acc[p][e] = st.adapter < 0 ? -0.0f : 0.0f;  // base + -0 is base bit for bit
+    if (st.adapter >= 0) {
+        const int64_t bn = N * B.R;  // values of one adapter's b
+        const uint16_t *bw = b + st.adapter * bn;
+        v4i piece[RC];
+#pragma unroll
+        for (int k = 0; k < RC; k++) {
+            const int64_t at = (int64_t)cb * kExpandCols * B.R + 8 * (tid + 256 * k);
+            piece[k] = ld16(bw + (at < bn ? at : 0));  // past b: of columns past N
+        }
+        const float *tr = t + (int64_t)(st.row0 + (32 * wave + li < st.rows ? 32 * wave + li : st.rows - 1)) * B.R + 8 * lh;
+        v4f a0[RC], a1[RC];
 #pragma unroll
         for (int c = 0; c < RC; c++) {
-            float v[8];
-            const bool in = 16 * c < B.R;
-            const v4f a0 = in ? *reinterpret_cast<const v4f *>(tr + 16 * c) : (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-            const v4f a1 = in ? *reinterpret_cast<const v4f *>(tr + 16 * c + 4) : (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+            a0[c] = *reinterpret_cast<const v4f *>(tr + (16 * c < B.R ? 16 * c : 0));
+            a1[c] = *reinterpret_cast<const v4f *>(tr + (16 * c < B.R ? 16 * c : 0) + 4);
+        }
+        const int rank = adapter_rank(B, st.adapter);
+        if (B.scale) sc = B.scale[st.adapter];
+        const int per_row = B.R / 8;  // 16-byte pieces of a row of b
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                v[e] = a0[e];
-                v[4 + e] = a1[e];
-            }
-            split8<NS>(v, tf[c]);
+        for (int k = 0; k < RC; k++) {
+            const int e = tid + 256 * k, n = e / per_row, c = e - n * per_row;
+            if (n < kExpandCols)
+                *reinterpret_cast<v4i *>(lds + (32 * (n & 3) + (n >> 2)) * ROW + 16 * c) = keep8(piece[k], rank - 8 * c);
+        }
+        __syncthreads();
+        if (wrows <= 0) return;
+#pragma unroll
+        for (int c = 0; c < RC; c++) {
+            if (16 * c >= rank) break;  // workgroup-uniform
+            const float v[8] = {a0[c][0], a0[c][1], a0[c][2], a0[c][3], a1[c][0], a1[c][1], a1[c][2], a1[c][3]};
+            v4i tf[NS], bf[4];
+            split8<NS>(v, tf);
+#pragma unroll
+            for (int p = 0; p < 4; p++)
+                bf[p] = *reinterpret_cast<const v4i *>(lds + (32 * p + li) * ROW + 32 * c + 16 * lh);
+#pragma unroll
+            for (int s = NS - 1; s >= 0; s--)
+#pragma unroll
+                for (int p = 0; p < 4; p++) acc[p] = mfma32(tf[s], bf[p], acc[p]);
         }
     }
-    const uint16_t *bw = b + (int64_t)(st.adapter < 0 ? 0 : st.adapter) * N * B.R;
-    float *bd = band[wave];
-    const int cols_blocks = (int)((N + kExpandCols - 1) / kExpandCols);
-    const int first = blockIdx.y * blocks;
-    const int last = first + blocks < cols_blocks ? first + blocks : cols_blocks;
-    for (int cb = first + wave; cb < last; cb += kExpandWaves) {
-        const int64_t n0 = (int64_t)cb * kExpandCols;
-        if (rank > 0) {
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                v16f acc;
-#pragma unroll
-                for (int e = 0; e < 16; e++) acc[e] = 0.0f;
-                const int64_t n = n0 + 32 * j + lm;
-                const uint16_t *br = bw + (n < N ? n : N - 1) * B.R + 8 * lh;
-#pragma unroll
-                for (int c = 0; c < RC; c++) {
-                    if (16 * c >= rank) break;  // wave-uniform
-                    v4i bf = ld16(br + 16 * c);
-                    if (16 * c + 16 > rank) bf = keep8(bf, rank - 16 * c - 8 * lh);
-#pragma unroll
-                    for (int p = 0; p < NS; p++) acc = mfma32(bf, tf[c][p], acc);
-                }
-#pragma unroll
-                for (int g = 0; g < 4; g++)
-                    *reinterpret_cast<float4 *>(bd + lm * STRIDE + 32 * j + 8 * g + 4 * lh) =
-                        make_float4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
-            }
-        }
-        const int64_t col = n0 + (lane % LPR) * PER;
-#pragma unroll 4
-        for (int p = 0; p < kExpandRows / RPP; p++) {
-            const int r = p * RPP + lane / LPR;
-            float d[PER];
-#pragma unroll
-            for (int e = 0; e < PER; e++) d[e] = -0.0f;
-            if (rank > 0) {
-#pragma unroll
-                for (int e = 0; e < PER; e += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(bd + r * STRIDE + (lane % LPR) * PER + e);
-                    d[e] = f.x, d[e + 1] = f.y, d[e + 2] = f.z, d[e + 3] = f.w;
-                }
-            }
-            if (r < st.rows && col < N)
-                expand_piece<ES>(d, sc, base, y, (int64_t)(st.row0 + r) * N + col, vec,
-                                 (int)(N - col < PER ? N - col : PER));
-        }
+    for (int r = 0; r < 16; r++) {
+        const int m = 8 * (r >> 2) + (r & 3);
+        if (m >= rows || left <= 0) continue;
+        const Q o = bv[r].plus(sc, acc[0][r], acc[1][r], acc[2][r], acc[3][r]);
+        if (left >= 4)
+            o.store(yp + m * ld + lane_off);
+        else
+            o.store_some(yp + m * ld + lane_off, left);
     }
 }
 
@@ -552,41 +625,46 @@ unsigned seg_tiles(const LoraBatch &B, int TM) {
     return (unsigned)(n < B.M ? n : B.M);
 }
 
-// Two forms by the number of 64-row tiles: from 128 on the card is filled by
-// tiles of 64 rows (32 from rank 48 on) whose 4 waves share K; below, a
-// workgroup of 16 waves takes 16 rows and 16 ranks, so that one token's K is
-// read by 16 waves at once and ranks spread over workgroups.
+// Two forms by the number of rows.  From 8192 on, one tile of 48 to 80 rows to
+// each compute unit, or to each of a multiple of them (M / 256 rows: with 64
+// each, 17776 rows made 278 tiles, and the 22 units with two set the time:
+// 75 us where 16384 rows took 49).  Below, tiles of 16 rows and 16 ranks with
+// 16 waves, so that one token's K is read by 16 waves at once and ranks spread
+// over workgroups.
 template <bool UP>
 hipError_t shrink(hipStream_t st, const uint16_t *x, const uint16_t *a, const LoraBatch &B, int64_t K, float *t,
                   const PackedOut &pk) {
     if (B.M == 0) return hipSuccess;
-    if (B.M < 128 * 64) {
+    if (B.M < 8192) {
         hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, UP>), dim3(seg_tiles(B, 16), B.R / 16), dim3(1024), 0, st, x,
-                           a, B, K, t, pk);
-    } else if (B.R <= 16) {
-        hipLaunchKernelGGL((lora_shrink_kernel<4, 1, 4, UP>), dim3(seg_tiles(B, 64)), dim3(256), 0, st, x, a, B, K, t, pk);
-    } else if (B.R <= 32) {
-        hipLaunchKernelGGL((lora_shrink_kernel<4, 2, 4, UP>), dim3(seg_tiles(B, 64)), dim3(256), 0, st, x, a, B, K, t, pk);
-    } else if (B.R <= 64) {
-        hipLaunchKernelGGL((lora_shrink_kernel<2, 4, 4, UP>), dim3(seg_tiles(B, 32)), dim3(256), 0, st, x, a, B, K, t, pk);
-    } else {
-        hipLaunchKernelGGL((lora_shrink_kernel<2, 8, 2, UP>), dim3(seg_tiles(B, 32)), dim3(128), 0, st, x, a, B, K, t, pk);
+                           a, B, K, 16, t, pk);
+        return hipGetLastError();
     }
+    const int64_t rounds = ((int64_t)B.M + 256 * 80 - 1) / (256 * 80);
+    const int64_t ragged = B.S < 64 ? B.S : 64;  // a request may end in a short tile
+    int64_t tile = (B.M + 256 * rounds - ragged - 1) / (256 * rounds - ragged);
+    if (tile > 80) tile = 80;
+    const dim3 grid(seg_tiles(B, (int)tile), (B.R + 63) / 64);
+#define DMPQ_SHRINK(RC_) \
+    hipLaunchKernelGGL((lora_shrink_kernel<5, RC_, 4, UP>), grid, dim3(256), 0, st, x, a, B, K, (int)tile, t, pk)
+    if (B.R <= 16)
+        DMPQ_SHRINK(1);
+    else if (B.R <= 32)
+        DMPQ_SHRINK(2);
+    else
+        DMPQ_SHRINK(4);
+#undef DMPQ_SHRINK
     return hipGetLastError();
 }
 
 template <int ES>
 hipError_t expand(hipStream_t st, const float *t, const void *base, const uint16_t *b, const LoraBatch &B, int64_t N,
                   void *y) {
-    const int64_t cb = (N + kExpandCols - 1) / kExpandCols;
-    const unsigned tiles = seg_tiles(B, kExpandRows);
-    // 1 to 8 blocks a wave: as many as leave 4 workgroups to every compute unit
-    int64_t per = (int64_t)tiles * cb / (4 * 1024);
-    per = per < 1 ? 1 : per > 8 ? 8 : per;
-    const int blocks = (int)per * kExpandWaves;
-    const dim3 grid(tiles, (unsigned)((cb + blocks - 1) / blocks));
+    const int64_t cols = (N + kExpandCols - 1) / kExpandCols, grid = seg_tiles(B, kExpandRows) * cols;
+    if (grid > INT32_MAX) return hipErrorInvalidValue;
 #define DMPQ_EXPAND(RC_) \
-    hipLaunchKernelGGL((lora_expand_kernel<ES, RC_>), grid, dim3(64 * kExpandWaves), 0, st, t, base, b, B, N, blocks, y)
+    hipLaunchKernelGGL((lora_expand_kernel<ES, RC_>), dim3((unsigned)grid), dim3(64 * kExpandWaves), 0, st, t, base, b, \
+                       B, N, (unsigned)cols, y)
     if (B.R <= 16)
         DMPQ_EXPAND(1);
     else if (B.R <= 32)

@@ -44,11 +44,11 @@ __device__ __forceinline__ bool seg_tile(const LoraBatch &B, int idx, int TM, Se
     int base = 0;
     for (int c = 0; c < B.S + 2; c += 64) {
         const int p = c + lane;  // 0: rows before the first request; s + 1: request s; S + 1: the rest
-        int lo = 0, hi = 0;
-        if (p <= B.S + 1) {
-            lo = p == 0 ? 0 : seg_clamp(B.seg_start[p - 1], B.M);
-            hi = p == B.S + 1 ? B.M : seg_clamp(B.seg_start[p], B.M);
-        }
+        const int before = p == 0 ? 0 : p - 1 < B.S ? p - 1 : B.S;
+        const int v0 = B.seg_start[before], v1 = B.seg_start[p < B.S ? p : B.S];
+        const int ad = B.S > 0 ? B.seg_adapter[before < B.S ? before : B.S - 1] : -1;
+        const int lo = p == 0 ? 0 : seg_clamp(v0, B.M);
+        const int hi = p > B.S + 1 ? 0 : p == B.S + 1 ? B.M : seg_clamp(v1, B.M);
         const int n = hi > lo ? (hi - lo + TM - 1) / TM : 0;
         int inc = n;
 #pragma unroll
@@ -63,8 +63,8 @@ __device__ __forceinline__ bool seg_tile(const LoraBatch &B, int idx, int TM, Se
             const int l = __builtin_amdgcn_readlane(lo, src), h = __builtin_amdgcn_readlane(hi, src);
             out.row0 = l + k * TM;
             out.rows = h - out.row0 < TM ? h - out.row0 : TM;
-            const int q = c + src;
-            out.adapter = q >= 1 && q <= B.S ? seg_adapter_of(B, q - 1) : -1;
+            const int q = c + src, a = __builtin_amdgcn_readlane(ad, src);
+            out.adapter = q >= 1 && q <= B.S && a >= 0 && a < B.nA ? a : -1;
             return true;
         }
         base += total;

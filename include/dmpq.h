@@ -422,7 +422,8 @@ dmpq_status dmpq_selftest_codec(hipStream_t stream, int codec, uint32_t lo, uint
  * Pool: n adapters of a common padded rank R (a multiple of 16, at most 128):
  *   a [n x R x K] bf16, b [n x N x R] bf16, rank [n] int32 (the adapter's own,
  *   0 .. R; others are taken as the nearest of these), scale [n] fp32.  What
- *   a and b hold past an adapter's rank is ignored, whatever it is.
+ *   a and b hold past an adapter's rank is ignored, whatever it is.  K and N are
+ *   at most 2^26 (of the *_lora GEMMs, K at most 2^22).
  * Batch: M rows of S requests.  Request s owns the rows seg_start[s] ..
  *   seg_start[s+1]-1 (int32 [S+1], ascending, on the device) and uses adapter
  *   seg_adapter[s] (int32 [S]; negative or >= n: none).  A request may be
