@@ -21,6 +21,14 @@ namespace dmpq {
 
 namespace {
 
+// t and u as the gradients' products read them: 3 bf16 parts, for each 32 rows
+// and 16 ranks the 64 lanes' 16-byte pieces of a 16x16x32 MFMA operand (lane
+// c + 16 q: rank c, rows 8 q .. 8 q + 7) one after the other, so that a
+// fragment is one contiguous load.  The place of rank j of row m in part p:
+__device__ __forceinline__ int64_t packed_at(int m, int p, int j, int R) {
+    return ((((int64_t)(m >> 5) * 3 + p) * (R >> 4) + (j >> 4)) * 64 + ((m >> 3) & 3) * 16 + (j & 15)) * 8 + (m & 7);
+}
+
 __device__ __forceinline__ v4i ld16(const void *p) { return *reinterpret_cast<const v4i *>(p); }
 
 // ---------------------------------------------------------------------------
@@ -33,19 +41,14 @@ __device__ __forceinline__ v4i ld16(const void *p) { return *reinterpret_cast<co
 // different rows, ran at 1.9 TB/s however many loads were in flight.  The
 // waves' sums meet in LDS at the end, added in wave order.  UP: the same
 // product for u = scale dy b (x is dy, a the transposed b), stored times
-// scale, and once more as 3 bf16 parts [part][j][m] for the gradients'
-// products over m.
+// scale, and once more packed for the gradients' products over the rows.
 // ---------------------------------------------------------------------------
-struct PackedOut {
-    uint16_t *p;   // [3][R][ld]
-    int64_t ld;
-};
 
 template <int RT, int RC, int WAVES, bool UP>
 __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(const uint16_t *__restrict__ x,
                                                                  const uint16_t *__restrict__ a, LoraBatch B,
                                                                  int64_t K, int tile, float *__restrict__ t,
-                                                                 PackedOut pk) {
+                                                                 uint16_t *__restrict__ packed) {
     constexpr int TM = 16 * RT, TJ = 16 * RC, ROWS = TM + TJ, LOADS = ROWS / 8;
     constexpr int STRIDE = TJ + 4;  // of the sums
     constexpr int STAGE = ROWS * 128, SUMS = TM * STRIDE * 4;
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(const uint16_t 
 #pragma unroll
             for (int p = 0; p < 3; p++) {
                 const uint32_t h = f32_to_bf16(rest);
-                pk.p[((int64_t)p * B.R + j0 + j) * pk.ld + st.row0 + r] = (uint16_t)h;
+                packed[packed_at(st.row0 + r, p, j0 + j, B.R)] = (uint16_t)h;
                 const float f = bf16_lo(h);
                 rest = __builtin_isfinite(f) ? rest - f : 0.0f;
             }
@@ -244,6 +247,8 @@ __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const
     // padding spread the lanes' 16-byte reads over the banks
     constexpr int ROW = 32 * RC + 16;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kExpandCols * ROW];
+    constexpr int TROW = 16 * 4 + 16;  // 16 ranks of a row of t and padding
+    __shared__ __attribute__((aligned(16))) uint8_t tlds[kExpandWaves][32 * TROW];
     typedef Quad<ES> Q;
     const unsigned tile = blockIdx.x / cols, cb = blockIdx.x - tile * cols;
     SegTile st;
@@ -283,12 +288,14 @@ __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const
             const int64_t at = (int64_t)cb * kExpandCols * B.R + 8 * (tid + 256 * k);
             piece[k] = ld16(bw + (at < bn ? at : 0));  // past b: of columns past N
         }
-        const float *tr = t + (int64_t)(st.row0 + (32 * wave + li < st.rows ? 32 * wave + li : st.rows - 1)) * B.R + 8 * lh;
-        v4f a0[RC], a1[RC];
+        // t: 4 lanes a row (64 bytes), rows l / 4 and 16 + l / 4
+        v4f tv[RC][2];
 #pragma unroll
-        for (int c = 0; c < RC; c++) {
-            a0[c] = *reinterpret_cast<const v4f *>(tr + (16 * c < B.R ? 16 * c : 0));
-            a1[c] = *reinterpret_cast<const v4f *>(tr + (16 * c < B.R ? 16 * c : 0) + 4);
+        for (int h = 0; h < 2; h++) {
+            const int r = 32 * wave + 16 * h + (lane >> 2);
+            const float *tr = t + (int64_t)(st.row0 + (r < st.rows ? r : st.rows - 1)) * B.R + 4 * (lane & 3);
+#pragma unroll
+            for (int c = 0; c < RC; c++) tv[c][h] = *reinterpret_cast<const v4f *>(tr + (16 * c < B.R ? 16 * c : 0));
         }
         const int rank = adapter_rank(B, st.adapter);
         if (B.scale) sc = B.scale[st.adapter];
@@ -304,7 +311,15 @@ __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const
 #pragma unroll
         for (int c = 0; c < RC; c++) {
             if (16 * c >= rank) break;  // workgroup-uniform
-            const float v[8] = {a0[c][0], a0[c][1], a0[c][2], a0[c][3], a1[c][0], a1[c][1], a1[c][2], a1[c][3]};
+            // the wave turns its 16 ranks of t into fragments in its own LDS
+            // (a wave's LDS operations keep their order)
+            uint8_t *tw = tlds[wave];
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                *reinterpret_cast<v4f *>(tw + (16 * h + (lane >> 2)) * TROW + 16 * (lane & 3)) = tv[c][h];
+            const v4f a0 = *reinterpret_cast<const v4f *>(tw + li * TROW + 32 * lh);
+            const v4f a1 = *reinterpret_cast<const v4f *>(tw + li * TROW + 32 * lh + 16);
+            const float v[8] = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
             v4i tf[NS], bf[4];
             split8<NS>(v, tf);
 #pragma unroll
@@ -332,12 +347,11 @@ __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const
 // Backward, first launch: what the products over the other dimension need.
 //   blocks 0 ..            b [N x R] -> bt [R x N], 64 x R tiles through LDS
 //   then                   a [R x K] -> at [K x R]
-//   then                   t [M x R] -> 3 bf16 parts [part][j][m]
+//   then                   t [M x R] packed
 // Entries past an adapter's rank become zeros.
 // ---------------------------------------------------------------------------
 struct PrepPlan {
-    int nb, na;      // tiles of one adapter's b and a
-    int64_t ld;      // row length of the packed t
+    int nb, na;  // tiles of one adapter's b and a
 };
 
 __global__ __launch_bounds__(256) void lora_prep_kernel(const uint16_t *__restrict__ a, const uint16_t *__restrict__ b,
@@ -392,7 +406,7 @@ __global__ __launch_bounds__(256) void lora_prep_kernel(const uint16_t *__restri
     v4i p[3];
     split8<3>(v, p);
 #pragma unroll
-    for (int i = 0; i < 3; i++) *reinterpret_cast<v4i *>(tp + ((int64_t)i * R + j) * pl.ld + m0) = p[i];
+    for (int i = 0; i < 3; i++) *reinterpret_cast<v4i *>(tp + packed_at((int)m0, i, j, R)) = p[i];
 }
 
 // ---------------------------------------------------------------------------
@@ -414,7 +428,6 @@ constexpr int kGradRows = 128;  // rows of a chunk: a multiple of 4 waves x 32
 struct GradPlan {
     int chunk;       // rows of a chunk
     int strips_n, strips_k;  // 128-column strips of dy and x
-    int64_t ld;      // row length of the packed operands
 };
 
 template <int RC, bool WIDE>
@@ -438,29 +451,37 @@ __device__ __forceinline__ void grad_strip(const uint16_t *__restrict__ src, con
         for (int i = 0; i < 8; i++)
 #pragma unroll
             for (int k = 0; k < RC; k++) acc[i][k] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-        for (int m0 = (lo & ~31) + 32 * wave; m0 < hi; m0 += 128) {
+        v4i wa[8], wb[8], pf[RC][3];
+        auto load = [&](v4i(&w)[8], int m0) {
             const int m = m0 + 8 * q;  // the lane's 8 rows
-            v4i w[8], pf[RC][3];
             const bool edge = m0 < lo || m0 + 32 > hi;  // wave-uniform
 #pragma unroll
             for (int r = 0; r < 8; r++) {
                 const bool ok = in_col && (!edge || (m + r >= lo && m + r < hi));
                 w[r] = ok ? ld16(src + (int64_t)(m + r) * C + col) : (v4i){0, 0, 0, 0};
             }
+        };
+        auto parts = [&](int m0) {
 #pragma unroll
             for (int k = 0; k < RC; k++)
 #pragma unroll
-                for (int p = 0; p < 3; p++) {
-                    const int j = j0 + 16 * k + c;
-                    v4i f = ld16(pk + ((int64_t)p * B.R + (j < B.R ? j : B.R - 1)) * pl.ld + m);
-                    if (edge) {
-                        f = keep8(f, hi - m);                 // rows from hi on
-                        const v4i low = keep8(f, lo - m);     // rows before lo
+                for (int p = 0; p < 3; p++)
+                    pf[k][p] = ld16(pk + packed_at(m0 + 8 * q, p, (j0 + 16 * k < B.R ? j0 + 16 * k : 0) + c, B.R));
+        };
+        auto mul = [&](v4i(&w)[8], int m0) {
+            const int m = m0 + 8 * q;
+            if (m0 < lo || m0 + 32 > hi) {  // wave-uniform
+#pragma unroll
+                for (int k = 0; k < RC; k++)
+#pragma unroll
+                    for (int p = 0; p < 3; p++) {
+                        v4i f = keep8(pf[k][p], hi - m);   // without the rows from hi on
+                        const v4i low = keep8(f, lo - m);  // and those before lo
 #pragma unroll
                         for (int d = 0; d < 4; d++) f[d] &= ~low[d];
+                        pf[k][p] = f;
                     }
-                    pf[k][p] = f;
-                }
+            }
 #pragma unroll
             for (int d = 0; d < 4; d++) {
                 v4i f0, f1;  // columns 2d and 2d + 1: 8 rows each
@@ -481,6 +502,19 @@ __device__ __forceinline__ void grad_strip(const uint16_t *__restrict__ src, con
                             acc[2 * d + 1][k] = mfma16(pf[k][p], f1, acc[2 * d + 1][k]);
                         }
                     }
+            }
+        };
+        // the next step's rows go out before this step's products
+        const int first = (lo & ~31) + 32 * wave;
+        if (first < hi) load(wa, first);
+        for (int m0 = first; m0 < hi; m0 += 256) {
+            parts(m0);
+            if (m0 + 128 < hi) load(wb, m0 + 128);
+            mul(wa, m0);
+            if (m0 + 128 < hi) {
+                parts(m0 + 128);
+                if (m0 + 256 < hi) load(wa, m0 + 256);
+                mul(wb, m0 + 128);
             }
         }
         // waves 1..3 add to wave 0 in order, 8 * RC pieces of 64 x 16 bytes
@@ -531,7 +565,7 @@ __device__ __forceinline__ void grad_strip(const uint16_t *__restrict__ src, con
 }
 
 template <int RC>
-__global__ __launch_bounds__(256) void lora_grad_kernel(const uint16_t *__restrict__ dy,
+__global__ __launch_bounds__(256, RC < 4 ? 2 : 1) void lora_grad_kernel(const uint16_t *__restrict__ dy,
                                                         const uint16_t *__restrict__ x,
                                                         const uint16_t *__restrict__ tp,
                                                         const uint16_t *__restrict__ up, LoraBatch B, int64_t N,
@@ -579,20 +613,18 @@ __global__ __launch_bounds__(256) void lora_grad_sum_kernel(const float *__restr
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-// Rows of a chunk: enough chunks that strips x chunks keep the card's 256
-// compute units busy, each at least kGradRows.
+// Rows of a chunk, a multiple of kGradRows: strips x chunks up to 1024
+// workgroups (two rounds of the two that a compute unit holds), not more,
+// since each writes a partial that is read again.
 int grad_chunk(int64_t M, int64_t N, int64_t K) {
     const int64_t strips = (N + 127) / 128 + (K + 127) / 128;
-    int64_t chunks = 2048 / (strips > 0 ? strips : 1) + 1;
-    const int64_t most = (M + kGradRows - 1) / kGradRows;
-    if (chunks > most) chunks = most;
+    int64_t chunks = 1024 / (strips > 0 ? strips : 1);
     if (chunks < 1) chunks = 1;
     return (int)round_up(M > 0 ? (M + chunks - 1) / chunks : 1, kGradRows);
 }
 
 struct BackwardLayout {
     int chunk, slots;
-    int64_t ld;
     size_t at, bt, tp, up, u, pb, pa, total;
 };
 
@@ -600,7 +632,7 @@ BackwardLayout backward_layout(int64_t M, int64_t N, int64_t K, int64_t R, int64
     BackwardLayout L;
     L.chunk = grad_chunk(M, N, K);
     L.slots = (int)((M + L.chunk - 1) / L.chunk + S);
-    L.ld = round_up(M, 64);
+    const size_t packed = 2 * 3 * (size_t)R * round_up(M, 32);
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -609,8 +641,8 @@ BackwardLayout backward_layout(int64_t M, int64_t N, int64_t K, int64_t R, int64
     };
     L.at = take(2 * (size_t)nA * R * K);
     L.bt = take(2 * (size_t)nA * R * N);
-    L.tp = take(2 * 3 * (size_t)R * L.ld);
-    L.up = take(2 * 3 * (size_t)R * L.ld);
+    L.tp = take(packed);
+    L.up = take(packed);
     L.u = take(4 * (size_t)M * R);
     L.pb = take(4 * (size_t)L.slots * N * R);
     L.pa = take(4 * (size_t)L.slots * K * R);
@@ -633,11 +665,11 @@ unsigned seg_tiles(const LoraBatch &B, int TM) {
 // over workgroups.
 template <bool UP>
 hipError_t shrink(hipStream_t st, const uint16_t *x, const uint16_t *a, const LoraBatch &B, int64_t K, float *t,
-                  const PackedOut &pk) {
+                  uint16_t *packed) {
     if (B.M == 0) return hipSuccess;
     if (B.M < 8192) {
         hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, UP>), dim3(seg_tiles(B, 16), B.R / 16), dim3(1024), 0, st, x,
-                           a, B, K, 16, t, pk);
+                           a, B, K, 16, t, packed);
         return hipGetLastError();
     }
     const int64_t rounds = ((int64_t)B.M + 256 * 80 - 1) / (256 * 80);
@@ -646,7 +678,7 @@ hipError_t shrink(hipStream_t st, const uint16_t *x, const uint16_t *a, const Lo
     if (tile > 80) tile = 80;
     const dim3 grid(seg_tiles(B, (int)tile), (B.R + 63) / 64);
 #define DMPQ_SHRINK(RC_) \
-    hipLaunchKernelGGL((lora_shrink_kernel<5, RC_, 4, UP>), grid, dim3(256), 0, st, x, a, B, K, (int)tile, t, pk)
+    hipLaunchKernelGGL((lora_shrink_kernel<5, RC_, 4, UP>), grid, dim3(256), 0, st, x, a, B, K, (int)tile, t, packed)
     if (B.R <= 16)
         DMPQ_SHRINK(1);
     else if (B.R <= 32)
@@ -681,7 +713,7 @@ hipError_t expand(hipStream_t st, const float *t, const void *base, const uint16
 
 hipError_t launch_lora_shrink(hipStream_t s, const uint16_t *x, const uint16_t *a, const LoraBatch &B, int64_t K,
                               float *t) {
-    return shrink<false>(s, x, a, B, K, t, PackedOut{nullptr, 0});
+    return shrink<false>(s, x, a, B, K, t, nullptr);
 }
 
 hipError_t launch_lora_expand(hipStream_t s, const float *t, const void *base, const uint16_t *b, const LoraBatch &B,
@@ -704,14 +736,14 @@ hipError_t launch_lora_backward(hipStream_t s, const uint16_t *dy, const uint16_
     float *u = reinterpret_cast<float *>(w + L.u);
     float *pb = reinterpret_cast<float *>(w + L.pb), *pa = reinterpret_cast<float *>(w + L.pa);
     if (B.M > 0) {
-        PrepPlan pp{(int)((N + 63) / 64), (int)((K + 63) / 64), L.ld};
+        PrepPlan pp{(int)((N + 63) / 64), (int)((K + 63) / 64)};
         const int64_t pack = ((int64_t)(B.M + 7) / 8 * B.R + 255) / 256;
         hipLaunchKernelGGL(lora_prep_kernel, dim3((unsigned)((int64_t)(pp.nb + pp.na) * B.nA + pack)), dim3(256), 0, s, a,
                            b, t, B, N, K, pp, at, bt, tp);
         hipError_t e = hipGetLastError();
-        if (e == hipSuccess) e = shrink<true>(s, dy, bt, B, N, u, PackedOut{up, L.ld});
+        if (e == hipSuccess) e = shrink<true>(s, dy, bt, B, N, u, up);
         if (e != hipSuccess) return e;
-        GradPlan gp{L.chunk, (int)((N + 127) / 128), (int)((K + 127) / 128), L.ld};
+        GradPlan gp{L.chunk, (int)((N + 127) / 128), (int)((K + 127) / 128)};
         const unsigned strips = (unsigned)(gp.strips_n + gp.strips_k), chunks = (unsigned)((B.M + L.chunk - 1) / L.chunk);
         if (B.R <= 16)
             hipLaunchKernelGGL(lora_grad_kernel<1>, dim3(strips, chunks, 1), dim3(256), 0, s, dy, x, tp, up, B, N, K, gp, pb, pa);
