@@ -29,6 +29,7 @@ __global__ __launch_bounds__(256, 1) void gemm_bf16_kernel(
     const TileCoord tc = tile_at(pid, tiles_m, tiles_n, GROUP_M);
     const int64_t m0 = (int64_t)tc.m * BM, n0 = (int64_t)tc.n * BN;
 
+    if constexpr ((EPI & kEpiLora) != 0) lora_meta_dma(lora.batch, lds + kLoraMetaOff, tid);
     v16f acc[4][4];
     dma_gemm_mainloop<OpBF16, TAIL>(reinterpret_cast<const uint8_t *>(x),
                                     reinterpret_cast<const uint8_t *>(w), M, N, 2 * K, 2 * K, m0, n0,
@@ -130,8 +131,8 @@ static hipError_t launch_bf16_paths(hipStream_t s, const uint16_t *x, const uint
                                     const LoraEpi &lora) {
     using namespace gdma;
     static const hipError_t attr = [] {
-        hipError_t e = allow_lds(gemm_bf16_kernel<OUT, false, EPI>, LDS_BYTES);
-        if (e == hipSuccess) e = allow_lds(gemm_bf16_kernel<OUT, true, EPI>, LDS_BYTES);
+        hipError_t e = allow_lds(gemm_bf16_kernel<OUT, false, EPI>, epi_lds<EPI>(LDS_BYTES));
+        if (e == hipSuccess) e = allow_lds(gemm_bf16_kernel<OUT, true, EPI>, epi_lds<EPI>(LDS_BYTES));
         if (e == hipSuccess) e = allow_lds(gemm_bf16_split_kernel<false>, LDS_BYTES);
         if (e == hipSuccess) e = allow_lds(gemm_bf16_split_kernel<true>, LDS_BYTES);
         return e;
@@ -144,10 +145,10 @@ static hipError_t launch_bf16_paths(hipStream_t s, const uint16_t *x, const uint
     const SplitPlan sp = plan_split(tm * tn, (int)((2 * K + BK - 1) / BK), spart != nullptr);
     if (sp.full > 0) {
         if (tail)
-            hipLaunchKernelGGL((gemm_bf16_kernel<OUT, true, EPI>), dim3(sp.full), block, LDS_BYTES, s, x, w, M, N,
+            hipLaunchKernelGGL((gemm_bf16_kernel<OUT, true, EPI>), dim3(sp.full), block, epi_lds<EPI>(LDS_BYTES), s, x, w, M, N,
                                K, y, utm, utn, partial, lora);
         else
-            hipLaunchKernelGGL((gemm_bf16_kernel<OUT, false, EPI>), dim3(sp.full), block, LDS_BYTES, s, x, w, M, N,
+            hipLaunchKernelGGL((gemm_bf16_kernel<OUT, false, EPI>), dim3(sp.full), block, epi_lds<EPI>(LDS_BYTES), s, x, w, M, N,
                                K, y, utm, utn, partial, lora);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;

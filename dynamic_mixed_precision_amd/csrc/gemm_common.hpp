@@ -164,8 +164,9 @@ __device__ __forceinline__ float gelu_f32(float v) {
 // kEpiGelu: each value passes through GELU on its way out.  kEpiAmax (bf16
 // only): the two lanes holding one 16-block finish its Hadamard (stages 1,
 // 2, 4 in-lane, stage 8 across the lane pair, then * 1/4) and the lane's max
-// |value| over valid blocks is returned.
-template <int ESIZE, int EPI = 0, int ROWS = kEpiRows>
+// |value| over valid blocks is returned.  BAND32: the band holds fp32 (rows of
+// kLoraBandStride bytes) whatever the output type.
+template <int ESIZE, int EPI = 0, int ROWS = kEpiRows, bool BAND32 = false>
 __device__ __forceinline__ float epi_band_to_global(const uint8_t *band, void *y, int64_t M,
                                                     int64_t N, int64_t row0, int64_t col0,
                                                     int lane, bool vec) {
@@ -180,7 +181,14 @@ __device__ __forceinline__ float epi_band_to_global(const uint8_t *band, void *y
     for (int p = 0; p < ROWS / B::ROWS_PER_PASS; p++) {
         const int r = p * B::ROWS_PER_PASS + lane / B::LANES_PER_ROW;
         const int64_t row = row0 + r;
-        uint4 v = *reinterpret_cast<const uint4 *>(band + r * B::STRIDE + chunk * 16);
+        uint4 v;
+        if constexpr (BAND32 && ESIZE == 2) {
+            const float4 a = *reinterpret_cast<const float4 *>(band + r * kLoraBandStride + chunk * 32);
+            const float4 b = *reinterpret_cast<const float4 *>(band + r * kLoraBandStride + chunk * 32 + 16);
+            v = make_uint4(cvt_pk_bf16(a.x, a.y), cvt_pk_bf16(a.z, a.w), cvt_pk_bf16(b.x, b.y), cvt_pk_bf16(b.z, b.w));
+        } else {
+            v = *reinterpret_cast<const uint4 *>(band + r * B::STRIDE + chunk * 16);
+        }
         if constexpr ((EPI & kEpiGelu) != 0) {
             if constexpr (ESIZE == 2) {
                 v.x = cvt_pk_bf16(gelu_f32(bf16_lo(v.x)), gelu_f32(bf16_hi(v.x)));
@@ -270,9 +278,8 @@ struct EpiScaleF32 {
 template <int OUT, int EPI, class AccV, class Scale>
 __device__ __forceinline__ void band_epilogue(AccV (&acc)[4][4], Scale &sc, uint8_t *lds, int64_t M,
                                               int64_t N, int64_t m0, int64_t n0, int wave, int wm,
-                                              int wn, int lane, void *y, float *slot, const LoraEpi &lora) {
+                                              int wn, int lane, void *y, float *slot) {
     constexpr int ES = OUT == 1 ? 2 : 4;
-    constexpr bool LORA = (EPI & kEpiLora) != 0;
     constexpr bool AMAX = (EPI & kEpiAmax) != 0;
     static_assert(!AMAX || OUT == 1, "the fused amax needs bf16 output");
     using Band = EpiBand<ES>;
@@ -286,15 +293,6 @@ __device__ __forceinline__ void band_epilogue(AccV (&acc)[4][4], Scale &sc, uint
         for (int ii = 0; ii < 2; ii++) {
             const int i = 2 * h + ii;
             sc.row(m0 + wm * 128 + i * 32 + lm);
-            v16f v[4];
-            if constexpr (LORA) {
-                __builtin_amdgcn_sched_barrier(0);  // one slice's values at a time
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-#pragma unroll
-                    for (int r = 0; r < 16; r++) v[j][r] = sc((float)acc[i][j][r], j, r >> 2, r & 3);
-                lora_slice<ES == 2 ? 2 : 3>(lora, m0 + wm * 128 + i * 32 + lm, n0 + wn * 128, N, lane, v);
-            }
 #pragma unroll
             for (int j = 0; j < 4; j++) {
 #pragma unroll
@@ -303,7 +301,7 @@ __device__ __forceinline__ void band_epilogue(AccV (&acc)[4][4], Scale &sc, uint
                     float v4[4];
 #pragma unroll
                     for (int e = 0; e < 4; e++)
-                        v4[e] = LORA ? v[j][4 * g + e] : sc((float)acc[i][j][4 * g + e], j, g, e);
+                        v4[e] = sc((float)acc[i][j][4 * g + e], j, g, e);
                     if constexpr (OUT == 0)
                         *reinterpret_cast<float4 *>(dst) = make_float4(v4[0], v4[1], v4[2], v4[3]);
                     else
@@ -317,6 +315,50 @@ __device__ __forceinline__ void band_epilogue(AccV (&acc)[4][4], Scale &sc, uint
     if constexpr (AMAX) epi_tile_amax(amax, wave, lane, slot);
 }
 
+// Dynamic LDS of a GEMM kernel whose main loop takes `bytes` (the INT8 scales
+// lie after them, without the adapter term and with it).
+constexpr int kLoraMetaOff = kLoraLds + 2048;
+template <int EPI>
+constexpr size_t epi_lds(size_t bytes) {
+    return (EPI & kEpiLora) != 0 ? (size_t)kLoraMetaOff + kLoraMeta : bytes;
+}
+
+// The epilogue with the adapter term: as band_epilogue, but in slices of 32
+// rows through fp32 bands, to which the adapters' products are added before
+// GELU, the amax and the rounding.  lds: kLoraLds bytes, and at kLoraMetaOff
+// the words that lora_meta_dma copied before the main loop.
+template <int OUT, int EPI, int AHEAD, class AccV, class Scale>
+__device__ __forceinline__ void lora_epilogue(AccV (&acc)[4][4], Scale &sc, uint8_t *lds, int64_t M, int64_t N,
+                                              int64_t m0, int64_t n0, int wave, int wm, int wn, int lane, void *y,
+                                              float *slot, const LoraEpi &lora) {
+    constexpr int ES = OUT == 1 ? 2 : 4;
+    const int lm = lane & 31, lh = lane >> 5;
+    uint8_t *band = lds + wave * kLoraBandBytes;
+    const bool vec = ((N * ES) & 15) == 0;
+    LoraRows<AHEAD> t;
+    LoraTile T = lora_tile_begin(lora, m0, n0, N, lds, lds + kLoraMetaOff, t);
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        sc.row(m0 + wm * 128 + i * 32 + lm);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int g = 0; g < 4; g++)
+                *reinterpret_cast<float4 *>(band + lm * kLoraBandStride + (j * 32 + 8 * g + 4 * lh) * 4) = make_float4(
+                    sc((float)acc[i][j][4 * g], j, g, 0), sc((float)acc[i][j][4 * g + 1], j, g, 1),
+                    sc((float)acc[i][j][4 * g + 2], j, g, 2), sc((float)acc[i][j][4 * g + 3], j, g, 3));
+        LoraRows<AHEAD> next;
+        if (i < 3) T.load_t(lora, i + 1, next);
+        lora_band_add<ES == 2 ? 2 : 3, AHEAD>(lora, T, i, n0, N, lds, t);
+        if (i < 3) t = next;
+        amax = fmaxf(amax, epi_band_to_global<ES, EPI, 32, true>(band, y, M, N, m0 + wm * 128 + i * 32,
+                                                                 n0 + wn * 128, lane, vec));
+        __builtin_amdgcn_sched_barrier(0);  // one slice at a time: its accumulators are free now
+    }
+    if constexpr ((EPI & kEpiAmax) != 0) epi_tile_amax(amax, wave, lane, slot);
+}
+
 // fp32 accumulators -> y = (acc * gA) * gW (fp32 or bf16).  slot: the tile's
 // entry of the fused-amax maxima (used with kEpiAmax only).
 template <int OUT, int EPI = 0>
@@ -324,8 +366,13 @@ __device__ __forceinline__ void f32_band_epilogue(v16f (&acc)[4][4], uint8_t *ld
                                                   float gW, int64_t M, int64_t N, int64_t m0,
                                                   int64_t n0, int wave, int wm, int wn, int lane,
                                                   void *y, float *slot, const LoraEpi &lora) {
-    EpiScaleF32 sc{gA, gW};
-    band_epilogue<OUT, EPI>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot, lora);
+    if constexpr ((EPI & kEpiLora) != 0) {
+        EpiScaleF32 sc{gA, gW};
+        lora_epilogue<OUT, EPI, 4>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot, lora);
+    } else {
+        EpiScaleF32 sc{gA, gW};
+        band_epilogue<OUT, EPI>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot);
+    }
 }
 
 // The epilogue of one 32-row slice i of a 128 x 128 quadrant of a split

@@ -66,15 +66,15 @@ __device__ __forceinline__ void i8_scale_dma(float *scl, const float *sa, const 
 // the fused amax per EPI; OUT 2: the raw int32 accumulators (test mode).  The
 // stage buffers must be free (both main loops end with a barrier).  SCL: the
 // tile's staged scales (i8_scale_dma).  pid: the tile's slot among the
-// fused-amax maxima.  LORA: the adapter term (kEpiLora).
-#define DMPQ_I8_EPILOGUE(SCL, LORA)                                                               \
+// fused-amax maxima.
+#define DMPQ_I8_EPILOGUE(SCL)                                                                     \
     {                                                                                             \
         constexpr int ES = OUT == 1 ? 2 : 4;                                                      \
         using Band = EpiBand<ES>;                                                                 \
         const int lm = lane & 31, lh = lane >> 5;                                                 \
         const float *scl_ = (SCL);                                                                \
         float4 swv[4][4];                                                                         \
-        if constexpr (OUT != 2 && (EPI & kEpiLora) == 0) {                                        \
+        if constexpr (OUT != 2) {                                                                 \
             _Pragma("unroll") for (int j = 0; j < 4; j++)                                         \
                 _Pragma("unroll") for (int g = 0; g < 4; g++) swv[j][g] =                         \
                     *reinterpret_cast<const float4 *>(scl_ + 256 + wn * 128 + j * 32 + 8 * g + 4 * lh); \
@@ -86,19 +86,6 @@ __device__ __forceinline__ void i8_scale_dma(float *scl, const float *sa, const 
             _Pragma("unroll") for (int ii = 0; ii < 2; ii++) {                                    \
                 const int i = 2 * h + ii;                                                         \
                 const float sar = OUT == 2 ? 0.0f : scl_[wm * 128 + i * 32 + lm];                 \
-                v16f v[4];                                                                        \
-                if constexpr ((EPI & kEpiLora) != 0) {                                            \
-                    __builtin_amdgcn_sched_barrier(0);                                            \
-                    _Pragma("unroll") for (int j = 0; j < 4; j++)                                 \
-                        _Pragma("unroll") for (int g = 0; g < 4; g++) {                           \
-                            const float4 w_ = *reinterpret_cast<const float4 *>(scl_ + 256 + wn * 128 + j * 32 + 8 * g + 4 * lh); \
-                            v[j][4 * g + 0] = ((float)acc[i][j][4 * g + 0] * sar) * w_.x;         \
-                            v[j][4 * g + 1] = ((float)acc[i][j][4 * g + 1] * sar) * w_.y;         \
-                            v[j][4 * g + 2] = ((float)acc[i][j][4 * g + 2] * sar) * w_.z;         \
-                            v[j][4 * g + 3] = ((float)acc[i][j][4 * g + 3] * sar) * w_.w;         \
-                        }                                                                         \
-                    lora_slice<ES == 2 ? 2 : 3>(LORA, m0 + wm * 128 + i * 32 + lm, n0 + wn * 128, N, lane, v); \
-                }                                                                                 \
                 _Pragma("unroll") for (int j = 0; j < 4; j++) {                                   \
                     _Pragma("unroll") for (int g = 0; g < 4; g++) {                               \
                         uint8_t *dst = band + (ii * 32 + lm) * Band::STRIDE + (j * 32 + 8 * g + 4 * lh) * ES; \
@@ -108,14 +95,10 @@ __device__ __forceinline__ void i8_scale_dma(float *scl, const float *sa, const 
                                           acc[i][j][4 * g + 3]);                                  \
                         } else {                                                                  \
                             float v4[4];                                                          \
-                            if constexpr ((EPI & kEpiLora) != 0) {                                \
-                                _Pragma("unroll") for (int e = 0; e < 4; e++) v4[e] = v[j][4 * g + e]; \
-                            } else {                                                              \
                             v4[0] = ((float)acc[i][j][4 * g + 0] * sar) * swv[j][g].x;            \
                             v4[1] = ((float)acc[i][j][4 * g + 1] * sar) * swv[j][g].y;            \
                             v4[2] = ((float)acc[i][j][4 * g + 2] * sar) * swv[j][g].z;            \
                             v4[3] = ((float)acc[i][j][4 * g + 3] * sar) * swv[j][g].w;            \
-                            }                                                                     \
                             if constexpr (OUT == 0)                                               \
                                 *reinterpret_cast<float4 *>(dst) = make_float4(v4[0], v4[1], v4[2], v4[3]); \
                             else                                                                  \
@@ -130,6 +113,34 @@ __device__ __forceinline__ void i8_scale_dma(float *scl, const float *sa, const 
             if constexpr ((EPI & kEpiAmax) != 0) amax = fmaxf(amax, m);                           \
         }                                                                                         \
         if constexpr ((EPI & kEpiAmax) != 0) epi_tile_amax(amax, wave, lane, partial + pid);      \
+    }
+
+// The same scaling for the epilogue with the adapter term; scl: the tile's
+// staged scales, in LDS past what that epilogue uses.
+struct EpiScaleI8Lds {
+    const float *rows, *cols;  // the lane's: sA from the wave's first row on, sW of its (j, g) groups
+    int64_t row0;
+    float sar;
+    __device__ __forceinline__ void row(int64_t r) { sar = rows[r - row0]; }
+    __device__ __forceinline__ float operator()(float a, int j, int g, int e) const {
+        return (a * sar) * cols[j * 32 + 8 * g + e];
+    }
+};
+static_assert(kLoraLds + kI8ScaleBytes <= kLoraMetaOff && kLoraLds % 16 == 0 && 2 * i8gemm::STAGE <= kLoraLds &&
+                  gdma::LDS_BYTES <= kLoraLds, "LDS of the adapter epilogue");
+
+// Where the scales are staged: past the stage buffers, with the adapter term
+// past its area too.
+template <int EPI>
+constexpr size_t i8_scale_off(size_t bytes) {
+    return (EPI & kEpiLora) != 0 ? (size_t)kLoraLds : bytes;
+}
+
+#define DMPQ_I8_LORA_EPILOGUE(SCL)                                                                \
+    {                                                                                             \
+        EpiScaleI8Lds sc{(SCL), (SCL) + 256 + wn * 128 + 4 * (lane >> 5), m0, 0.0f};              \
+        lora_epilogue<OUT, EPI, 1>(acc, sc, reinterpret_cast<uint8_t *>(lds), M, N, m0, n0, wave, wm, wn, lane, y, \
+                                (EPI & kEpiAmax) ? partial + pid : nullptr, lora);                \
     }
 
 template <int OUT, int EPI>
@@ -189,7 +200,8 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_kernel(
             make_uint4(iw ? rw[j].x : 0u, iw ? rw[j].y : 0u, iw ? rw[j].z : 0u, iw ? rw[j].w : 0u); \
     }
 
-    float *scl = reinterpret_cast<float *>(lds + 2 * STAGE);
+    float *scl = reinterpret_cast<float *>(lds + i8_scale_off<EPI>(2 * STAGE));
+    if constexpr ((EPI & kEpiLora) != 0) lora_meta_dma(lora.batch, reinterpret_cast<uint8_t *>(lds) + kLoraMetaOff, tid);
     i8_scale_dma(scl, sa, sw, M, N, m0, n0, tid);
     DMPQ_I8_GLOAD(0)
     DMPQ_I8_SSTORE(0)
@@ -226,7 +238,11 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_kernel(
 #undef DMPQ_I8_GLOAD
 #undef DMPQ_I8_SSTORE
 
-    DMPQ_I8_EPILOGUE(scl, lora)
+    if constexpr ((EPI & kEpiLora) != 0) {
+        DMPQ_I8_LORA_EPILOGUE(scl)
+    } else {
+        DMPQ_I8_EPILOGUE(scl)
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -357,7 +373,7 @@ __global__ __launch_bounds__(256, 1) void gemm_i8w4_kernel(
 #undef DMPQ_I8W4_GLOAD
 #undef DMPQ_I8W4_SSTORE
 
-    DMPQ_I8_EPILOGUE(scl, LoraEpi{})
+    DMPQ_I8_EPILOGUE(scl)
 }
 
 // ---------------------------------------------------------------------------
@@ -378,13 +394,18 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_dma_kernel(
     const TileCoord tc = tile_at(pid, tiles_m, tiles_n, GROUP_M);
     const int64_t m0 = (int64_t)tc.m * BM, n0 = (int64_t)tc.n * BN;
 
-    float *scl = reinterpret_cast<float *>(lds + LDS_BYTES);
+    float *scl = reinterpret_cast<float *>(lds + i8_scale_off<EPI>(LDS_BYTES));
+    if constexpr ((EPI & kEpiLora) != 0) lora_meta_dma(lora.batch, reinterpret_cast<uint8_t *>(lds) + kLoraMetaOff, tid);
     i8_scale_dma(scl, sa, sw, M, N, m0, n0, tid);  // older than the first stage's DMA
     v16i acc[4][4];
     dma_gemm_mainloop<OpI8, false>(reinterpret_cast<const uint8_t *>(A),
                                    reinterpret_cast<const uint8_t *>(W), M, N, K, K, m0, n0,
                                    reinterpret_cast<uint8_t *>(lds), acc);
-    DMPQ_I8_EPILOGUE(scl, lora)
+    if constexpr ((EPI & kEpiLora) != 0) {
+        DMPQ_I8_LORA_EPILOGUE(scl)
+    } else {
+        DMPQ_I8_EPILOGUE(scl)
+    }
 }
 
 // The split workgroups of a SplitPlan launch: the main loop over this
@@ -475,8 +496,9 @@ static hipError_t launch_i8_paths(hipStream_t s, const int8_t *qa, const float *
     constexpr bool CAN_SPLIT = OUT != 2;
     // Kernels need more dynamic LDS than the default limit: opt in once.
     static const hipError_t attr = [] {
-        hipError_t e = allow_lds(gemm_i8_kernel<OUT, EPI>, 2 * i8gemm::STAGE + kI8ScaleBytes);
-        if (e == hipSuccess) e = allow_lds(gemm_i8_dma_kernel<OUT, EPI>, gdma::LDS_BYTES + kI8ScaleBytes);
+        hipError_t e = allow_lds(gemm_i8_kernel<OUT, EPI>, epi_lds<EPI>(2 * i8gemm::STAGE + kI8ScaleBytes));
+        if (e == hipSuccess)
+            e = allow_lds(gemm_i8_dma_kernel<OUT, EPI>, epi_lds<EPI>(gdma::LDS_BYTES + kI8ScaleBytes));
         if (e == hipSuccess) e = allow_lds(gemm_i8_split_kernel, gdma::LDS_BYTES);
 
         return e;
@@ -487,15 +509,15 @@ static hipError_t launch_i8_paths(hipStream_t s, const int8_t *qa, const float *
     const unsigned utm = (unsigned)tm, utn = (unsigned)tn;
     if (K % gdma::BK != 0) {
         hipLaunchKernelGGL((gemm_i8_kernel<OUT, EPI>), dim3((unsigned)(tm * tn)), block,
-                           2 * i8gemm::STAGE + kI8ScaleBytes, s, qa,
-                           sa, qw, sw, M, N, K, y, utm, utn, partial, lora);
+                           epi_lds<EPI>(2 * i8gemm::STAGE + kI8ScaleBytes), s, qa, sa, qw, sw, M, N, K, y, utm, utn,
+                           partial, lora);
         return hipGetLastError();
     }
     const SplitPlan sp = plan_split(tm * tn, (int)(K / gdma::BK), CAN_SPLIT && spart != nullptr && K >= kSplitMinKInt8);
     if (sp.full > 0) {
         hipLaunchKernelGGL((gemm_i8_dma_kernel<OUT, EPI>), dim3(sp.full), block,
-                           gdma::LDS_BYTES + kI8ScaleBytes, s, qa, sa, qw,
-                           sw, M, N, K, y, utm, utn, partial, lora);
+                           epi_lds<EPI>(gdma::LDS_BYTES + kI8ScaleBytes), s, qa, sa, qw, sw, M, N, K, y, utm, utn,
+                           partial, lora);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

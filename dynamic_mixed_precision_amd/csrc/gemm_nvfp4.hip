@@ -111,6 +111,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_f16_kernel(
     const int64_t nb = K / 16;  // scale groups per row
     const int64_t rb = K / 2;   // code bytes per row
 
+    if constexpr ((EPI & kEpiLora) != 0) lora_meta_dma(lora.batch, lds + kLoraMetaOff, tid);
     v16f acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; i++)
@@ -259,6 +260,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_fast_kernel(
     const int64_t nb = K / 16, rb = K / 2;
     const int nk = (int)(nb / 4);
 
+    if constexpr ((EPI & kEpiLora) != 0) lora_meta_dma(lora.batch, lds + kLoraMetaOff, tid);
     v16f acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; i++)
@@ -643,6 +645,7 @@ __device__ __forceinline__ void fp4dma_tile(const uint8_t *__restrict__ ca, cons
     const unsigned pid = xcd_order(blockIdx.x, gridDim.x);
     const TileCoord tc = tile_at(pid, tiles_m, tiles_n, GROUP_M);
     const int64_t m0 = (int64_t)tc.m * BM, n0 = (int64_t)tc.n * BN;
+    if constexpr ((EPI & kEpiLora) != 0) lora_meta_dma(lora.batch, lds + kLoraMetaOff, tid);
     v16f acc[4][4];
     fp4dma_mainloop<HT>(ca, sa, cw, sw, M, N, K, m0, n0, 0, (int)(K / BKE) + (HT ? 1 : 0), lds, acc);
     fp4_epilogue<OUT, EPI>(acc, lds, ga, gw, M, N, m0, n0, wave, wm, wn, lane, y, partial, pid, lora);
@@ -848,7 +851,7 @@ static hipError_t launch_fp4_dma(hipStream_t s, TileFn tile_kernel, SplitFn spli
                                  uint32_t *spart, unsigned utm, unsigned utn, const LoraEpi &lora) {
     const SplitPlan sp = plan_split((int64_t)utm * utn, (int)(K / fp4dma::BKE) + (HT ? 1 : 0), spart != nullptr);
     if (sp.full > 0) {
-        hipLaunchKernelGGL(tile_kernel, dim3(sp.full), dim3(256), fp4dma::LDS_BYTES, s, ca, sa, ga, cw, sw, gw, M,
+        hipLaunchKernelGGL(tile_kernel, dim3(sp.full), dim3(256), epi_lds<EPI>(fp4dma::LDS_BYTES), s, ca, sa, ga, cw, sw, gw, M,
                            N, K, y, utm, utn, partial, lora);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -870,11 +873,11 @@ static hipError_t launch_fp4_paths(hipStream_t s, const uint8_t *ca, const uint8
                                    float *partial, uint32_t *spart, const LoraEpi &lora) {
     using namespace fp4gemm;
     static const hipError_t attr = [] {
-        hipError_t e = allow_lds(gemm_fp4_f16_kernel<OUT, EPI>, 2 * STAGE);
-        if (e == hipSuccess) e = allow_lds(gemm_fp4_fast_kernel<OUT, EPI>, 2 * STAGE);
-        if (e == hipSuccess) e = allow_lds(gemm_fp4_dma_kernel<OUT, EPI>, fp4dma::LDS_BYTES);
+        hipError_t e = allow_lds(gemm_fp4_f16_kernel<OUT, EPI>, epi_lds<EPI>(2 * STAGE));
+        if (e == hipSuccess) e = allow_lds(gemm_fp4_fast_kernel<OUT, EPI>, epi_lds<EPI>(2 * STAGE));
+        if (e == hipSuccess) e = allow_lds(gemm_fp4_dma_kernel<OUT, EPI>, epi_lds<EPI>(fp4dma::LDS_BYTES));
         if (e == hipSuccess) e = allow_lds(gemm_fp4_split_kernel, fp4dma::LDS_BYTES);
-        if (e == hipSuccess) e = allow_lds(gemm_fp4_dma_tail_kernel<OUT, EPI>, fp4dma::LDS_BYTES);
+        if (e == hipSuccess) e = allow_lds(gemm_fp4_dma_tail_kernel<OUT, EPI>, epi_lds<EPI>(fp4dma::LDS_BYTES));
         if (e == hipSuccess) e = allow_lds(gemm_fp4_split_tail_kernel, fp4dma::LDS_BYTES);
         return e;
     }();
@@ -889,10 +892,10 @@ static hipError_t launch_fp4_paths(hipStream_t s, const uint8_t *ca, const uint8
         return launch_fp4_dma<OUT, EPI, true>(s, gemm_fp4_dma_tail_kernel<OUT, EPI>, gemm_fp4_split_tail_kernel, ca,
                                               sa, ga, cw, sw, gw, M, N, K, y, partial, spart, utm, utn, lora);
     if (K % (4 * 16) == 0) {
-        hipLaunchKernelGGL((gemm_fp4_fast_kernel<OUT, EPI>), grid, block, 2 * STAGE, s, ca, sa, ga, cw,
+        hipLaunchKernelGGL((gemm_fp4_fast_kernel<OUT, EPI>), grid, block, epi_lds<EPI>(2 * STAGE), s, ca, sa, ga, cw,
                            sw, gw, M, N, K, y, utm, utn, partial, lora);
     } else {
-        hipLaunchKernelGGL((gemm_fp4_f16_kernel<OUT, EPI>), grid, block, 2 * STAGE, s, ca, sa, ga, cw,
+        hipLaunchKernelGGL((gemm_fp4_f16_kernel<OUT, EPI>), grid, block, epi_lds<EPI>(2 * STAGE), s, ca, sa, ga, cw,
                            sw, gw, M, N, K, y, utm, utn, partial, lora);
     }
     return hipGetLastError();

@@ -137,6 +137,7 @@ __device__ __forceinline__ v4f mfma16(const v4i &a, const v4i &b, const v4f &c) 
 }
 
 // ---- the adapter term of a GEMM's epilogue -----------------------------------
+// Of one 32-row slice, run by one wave on its own (the fixup of split tiles):
 // v += scale * t b^T for 32 rows x 128 columns in the GEMMs' accumulator
 // layout: lane l holds row l % 32 (`row`; past M: nothing is added) and, in
 // v[j][4g + e], column n0 + 32 j + 8 g + 4 (l / 32) + e.  b's rows are the
@@ -204,6 +205,220 @@ __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_
                 for (int e = 0; e < 16; e++) v[j][e] = mine == a ? v[j][e] + d[e] : v[j][e];
             }
         }
+    }
+}
+
+// Of a 256 x 256 tile of 2 x 2 waves, slice by slice: the epilogue writes 32
+// rows of every wave's scaled fp32 values to LDS bands, and lora_band_add adds
+// the adapters' products to the bands.  (Onto the accumulators themselves the
+// products need no LDS traffic, but whatever stood between the main loop and
+// them made the compiler spill accumulators: 26 to 130 us more on a GEMM of
+// 237 us even without any adapter.)
+//
+// The workgroup copies b's 256 rows of one request into LDS (entries past the
+// rank as zeros); a tile that belongs to one request does so once.  A lane
+// loads its row of t straight from memory, a slice ahead of its use and so
+// before the stores of the slice between.  The products of a request start
+// from zero and are added to its own rows only, never zero times b: one
+// adapter's infinity must not reach another request's rows.
+constexpr int kLoraBandStride = 128 * 4 + 16;             // an fp32 band row of 128 columns
+constexpr int kLoraBandBytes = 32 * kLoraBandStride;      // one wave's slice
+constexpr int kLoraBOff = 4 * kLoraBandBytes;
+constexpr int kLoraMeta = 4 * 64 * 4;  // the first 64 of seg_start, seg_adapter, rank and scale
+// beside it: the INT8 GEMM's scales, the meta words, the amax words
+constexpr int kLoraLds = 160 * 1024 - 2048 - kLoraMeta - 256;
+
+// Copies the meta words by LDS DMA, one array a wave, in the kernel's prologue:
+// they land during the main loop and are visible after its barriers, so that
+// the epilogue starts without a chain of dependent loads.
+__device__ __forceinline__ void lora_meta_dma(const LoraBatch &B, uint8_t *meta, int tid) {
+    typedef __attribute__((address_space(3))) void lds_void;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const void *src = nullptr;
+    if (wave == 0) src = B.seg_start + (lane < B.S ? lane : B.S);
+    if (wave == 1 && B.S > 0) src = B.seg_adapter + (lane < B.S ? lane : B.S - 1);
+    if (wave == 2 && B.nA > 0) src = B.rank + (lane < B.nA ? lane : B.nA - 1);
+    if (wave == 3 && B.nA > 0) src = B.scale + (lane < B.nA ? lane : B.nA - 1);
+    if (src) __builtin_amdgcn_global_load_lds(src, (lds_void *)(meta + 256 * wave), 4, 0, 0);
+}
+
+// Request s's first row, its adapter, and an adapter's rank and scale: from
+// the meta words where they are among the first 64.  All wave-uniform.
+struct LoraWords {
+    const int *w;
+    __device__ __forceinline__ int start(const LoraBatch &B, int s) const {
+        return __builtin_amdgcn_readfirstlane(s < 64 ? w[s] : B.seg_start[s]);
+    }
+    __device__ __forceinline__ int adapter(const LoraBatch &B, int s) const {
+        const int a = __builtin_amdgcn_readfirstlane(s < 64 ? w[64 + s] : B.seg_adapter[s]);
+        return a >= 0 && a < B.nA ? a : -1;
+    }
+    __device__ __forceinline__ int rank(const LoraBatch &B, int a) const {
+        const int r = __builtin_amdgcn_readfirstlane(a < 64 ? w[128 + a] : B.rank[a]);
+        return r < 0 ? 0 : r > B.R ? B.R : r;
+    }
+    __device__ __forceinline__ float scale(const LoraBatch &B, int a) const {
+        return __int_as_float(__builtin_amdgcn_readfirstlane(a < 64 ? w[192 + a] : __float_as_int(B.scale[a])));
+    }
+};
+
+// AHEAD: the 16-rank pieces of t that a lane holds a slice ahead; the others
+// are loaded as they are used.  4 (a rank of 64) in the fp32-accumulator
+// GEMMs.  The INT8 GEMM's registers hold no more than 1: with 4 its kernel
+// spills 34 and takes 302 us without any adapter where it takes 252 with 1.
+static_assert(kLoraBOff + 256 * (2 * kMaxLoraRank + 16) <= kLoraLds, "bands and b fit");
+
+template <int AHEAD>
+struct LoraRows {
+    v4f v[AHEAD][2];
+};
+
+// What a workgroup keeps over the slices of its tile: the tile's rows, the
+// first request that may have some, and the request whose b is in LDS with
+// its rows of the tile, rank and scale.
+struct LoraTile {
+    LoraWords words;
+    int r0, r1, s0, staged;
+    int lo, hi, rank;
+    float sc;
+
+    // request s's rows of the tile; false if there are none or no adapter
+    __device__ __forceinline__ bool rows_of(const LoraBatch &B, int s, int &l, int &h, int &a) const {
+        const int start = words.start(B, s), end = words.start(B, s + 1);
+        a = words.adapter(B, s);
+        l = start > r0 ? start : r0;
+        h = end < r1 ? end : r1;
+        return l < h && a >= 0;
+    }
+    // its b into LDS; the barriers around the copy are the caller's
+    __device__ __forceinline__ void stage_b(const LoraEpi &L, int s, int l, int h, int a, int64_t n0, int64_t N,
+                                            uint8_t *lds) {
+        const LoraBatch &B = L.batch;
+        const int brow = 2 * B.R + 16, per_row = B.R >> 3;
+        const uint16_t *bw = L.b + (int64_t)a * N * B.R;
+        staged = s, lo = l, hi = h;
+        rank = words.rank(B, a);
+        sc = words.scale(B, a);
+#pragma unroll 4
+        for (int e = threadIdx.x; e < 256 * per_row; e += 256) {
+            const int n = e / per_row, c = e - n * per_row;
+            const int64_t g = n0 + n < N ? n0 + n : N - 1;
+            const v4i f = *reinterpret_cast<const v4i *>(bw + g * B.R + 8 * c);
+            *reinterpret_cast<v4i *>(lds + kLoraBOff + n * brow + 16 * c) = keep8(f, rank - 8 * c);
+        }
+    }
+    // the lane's row of t in slice i of its wave
+    __device__ __forceinline__ const float *row(const LoraEpi &L, int i) const {
+        const int r = r0 + (threadIdx.x >> 7) * 128 + 32 * i + (threadIdx.x & 31);
+        return L.t + (int64_t)(r < L.batch.M ? r : L.batch.M - 1) * L.batch.R + 8 * ((threadIdx.x >> 5) & 1);
+    }
+    template <int AHEAD>
+    __device__ __forceinline__ void load_t(const LoraEpi &L, int i, LoraRows<AHEAD> &t) const {
+        const float *p = row(L, i);
+#pragma unroll
+        for (int c = 0; c < AHEAD; c++)
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                t.v[c][h] = *reinterpret_cast<const v4f *>(p + (16 * c < L.batch.R ? 16 * c : 0) + 4 * h);
+    }
+};
+
+// meta: the words of lora_meta_dma.
+template <int AHEAD>
+__device__ __forceinline__ LoraTile lora_tile_begin(const LoraEpi &L, int64_t m0, int64_t n0, int64_t N, uint8_t *lds,
+                                                    const uint8_t *meta, LoraRows<AHEAD> &t) {
+    const LoraBatch &B = L.batch;
+    const int lane = threadIdx.x & 63;
+    LoraTile T;
+    T.words.w = reinterpret_cast<const int *>(meta);
+    T.r0 = (int)m0;
+    T.r1 = m0 + 256 < B.M ? (int)m0 + 256 : B.M;
+    T.s0 = 0;
+    T.staged = -1;
+    T.lo = T.hi = T.rank = 0;
+    T.sc = 0.0f;
+    T.load_t(L, 0, t);
+    for (int c = 0; c <= B.S; c += 64) {  // the last request that starts at or before the tile
+        const int at = c + lane <= B.S ? c + lane : B.S;
+        const uint64_t below = __ballot(c + lane <= B.S && (c == 0 ? T.words.w[lane] : B.seg_start[at]) <= T.r0);
+        const int n = __builtin_popcountll(below);
+        T.s0 = c + n - 1;
+        if (n < 64) break;
+    }
+    if (T.s0 < 0) T.s0 = 0;
+    int l, h, a;
+    if (T.s0 < B.S && T.rows_of(B, T.s0, l, h, a)) T.stage_b(L, T.s0, l, h, a, n0, N, lds);
+    __syncthreads();
+    return T;
+}
+
+// Slice i of every wave.  Called by all four waves after they wrote their
+// bands (lds + wave * kLoraBandBytes); returns with the wave's own band ready.
+template <int NS, int AHEAD>
+__device__ __forceinline__ void lora_band_add(const LoraEpi &L, LoraTile &T, int i, int64_t n0, int64_t N,
+                                              uint8_t *lds, const LoraRows<AHEAD> &t) {
+    const LoraBatch &B = L.batch;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lm = lane & 31, lh = lane >> 5, wm = wave >> 1, wn = wave & 1;
+    const int brow = 2 * B.R + 16;
+    uint8_t *band = lds + wave * kLoraBandBytes, *bs = lds + kLoraBOff;
+    const int q0 = T.r0 + 32 * i, q1 = q0 + 128;  // the first rows of the two slices of this step
+    const int mine0 = wm ? q1 : q0;
+    for (int s = T.s0; s < B.S; s++) {
+        if (T.staged != s || T.hi < T.r1) {  // (the staged request may be the tile's last)
+            int l, h, a;
+            const bool some = T.rows_of(B, s, l, h, a);
+            if (T.words.start(B, s) >= T.r1) break;
+            const bool in0 = l < q0 + 32 && h > q0, in1 = l < q1 + 32 && h > q1;
+            if (!some || !(in0 || in1)) continue;  // workgroup-uniform
+            if (T.staged != s) {
+                __syncthreads();  // every wave is done with the last request's b
+                T.stage_b(L, s, l, h, a, n0, N, lds);
+                __syncthreads();
+            }
+        }
+        const bool last = T.hi >= T.r1;
+        if (T.rank > 0 && T.lo < mine0 + 32 && T.hi > mine0) {  // wave-uniform, no barrier inside
+            v16f d[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int e = 0; e < 16; e++) d[j][e] = 0.0f;
+            auto piece = [&](int c, const v4f &a0, const v4f &a1) {
+                const float v[8] = {T.sc * a0[0], T.sc * a0[1], T.sc * a0[2], T.sc * a0[3],
+                                    T.sc * a1[0], T.sc * a1[1], T.sc * a1[2], T.sc * a1[3]};
+                v4i tf[NS], bf[4];
+                split8<NS>(v, tf);
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    bf[j] = *reinterpret_cast<const v4i *>(bs + (wn * 128 + 32 * j + lm) * brow + 2 * c + 16 * lh);
+#pragma unroll
+                for (int p = NS - 1; p >= 0; p--)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) d[j] = mfma32(bf[j], tf[p], d[j]);
+            };
+#pragma unroll
+            for (int k = 0; k < AHEAD; k++)
+                if (16 * k < T.rank) piece(16 * k, t.v[k][0], t.v[k][1]);
+            if (T.rank > 16 * AHEAD) {
+                const float *p = T.row(L, i);
+                for (int c = 16 * AHEAD; c < T.rank; c += 16)
+                    piece(c, *reinterpret_cast<const v4f *>(p + c), *reinterpret_cast<const v4f *>(p + c + 4));
+            }
+            const bool own = mine0 + lm >= T.lo && mine0 + lm < T.hi;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int g = 0; g < 4; g++) {
+                    float4 *p = reinterpret_cast<float4 *>(band + lm * kLoraBandStride + (32 * j + 8 * g + 4 * lh) * 4);
+                    float4 o = *p;
+                    if (own) {
+                        o.x += d[j][4 * g], o.y += d[j][4 * g + 1], o.z += d[j][4 * g + 2], o.w += d[j][4 * g + 3];
+                        *p = o;
+                    }
+                }
+        }
+        if (T.staged == s && last) break;
     }
 }
 
