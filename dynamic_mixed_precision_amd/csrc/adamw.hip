@@ -24,24 +24,33 @@ namespace dmpq {
 
 namespace {
 
-constexpr int kUnits = kAdamwChunk / kAdamwBlock / 4;  // 256-value blocks per wave of a chunk
+// The table's pointers come out of memory: without their address space the
+// compiler takes flat accesses, which also occupy the LDS path.
+#define DMPQ_GLOBAL __attribute__((address_space(1)))
+template <class T>
+__device__ __forceinline__ DMPQ_GLOBAL T *global_ptr(const void *p) {
+    return (DMPQ_GLOBAL T *)(uintptr_t)p;
+}
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// 4 values at p + i (fp32 or bf16), of which n are there.
-template <int DT>
+// 4 values at p + i (DT 0: fp32, 1: bf16).  ALL: all four are there, else the
+// first n are (n may be 0 or less).
+template <int DT, bool ALL>
 __device__ __forceinline__ void load4(const void *p, int64_t i, int n, float v[4]) {
     if constexpr (DT == 0) {
-        const float *f = static_cast<const float *>(p) + i;
-        if (n >= 4) {
-            const float4 q = *reinterpret_cast<const float4 *>(f);
+        const DMPQ_GLOBAL float *f = global_ptr<const float>(p) + i;
+        if constexpr (ALL) {
+            const f32x4 q = *reinterpret_cast<const DMPQ_GLOBAL f32x4 *>(f);
             v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
         } else {
 #pragma unroll
             for (int e = 0; e < 4; e++) v[e] = e < n ? f[e] : 0.0f;
         }
     } else {
-        const uint16_t *h = static_cast<const uint16_t *>(p) + i;
-        if (n >= 4) {
-            const uint2 q = *reinterpret_cast<const uint2 *>(h);
+        const DMPQ_GLOBAL uint16_t *h = global_ptr<const uint16_t>(p) + i;
+        if constexpr (ALL) {
+            const u32x2 q = *reinterpret_cast<const DMPQ_GLOBAL u32x2 *>(h);
             v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
         } else {
 #pragma unroll
@@ -50,22 +59,23 @@ __device__ __forceinline__ void load4(const void *p, int64_t i, int n, float v[4
     }
 }
 
-template <int DT>
+template <int DT, bool ALL>
 __device__ __forceinline__ void store4(void *p, int64_t i, int n, const float v[4]) {
     if constexpr (DT == 0) {
-        float *f = static_cast<float *>(p) + i;
-        if (n >= 4) {
-            *reinterpret_cast<float4 *>(f) = make_float4(v[0], v[1], v[2], v[3]);
+        DMPQ_GLOBAL float *f = global_ptr<float>(p) + i;
+        if constexpr (ALL) {
+            const f32x4 q = {v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<DMPQ_GLOBAL f32x4 *>(f) = q;
         } else {
 #pragma unroll
             for (int e = 0; e < 4; e++)
                 if (e < n) f[e] = v[e];
         }
     } else {
-        uint16_t *h = static_cast<uint16_t *>(p) + i;
-        const uint2 q = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
-        if (n >= 4) {
-            *reinterpret_cast<uint2 *>(h) = q;
+        DMPQ_GLOBAL uint16_t *h = global_ptr<uint16_t>(p) + i;
+        const u32x2 q = {cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+        if constexpr (ALL) {
+            *reinterpret_cast<DMPQ_GLOBAL u32x2 *>(h) = q;
         } else {
 #pragma unroll
             for (int e = 0; e < 4; e++)
@@ -75,9 +85,10 @@ __device__ __forceinline__ void store4(void *p, int64_t i, int n, const float v[
 }
 
 // 4 codes (one word) and back.
+template <bool ALL>
 __device__ __forceinline__ uint32_t load_codes(const void *p, int64_t i, int n) {
-    const uint8_t *c = static_cast<const uint8_t *>(p) + i;
-    if (n >= 4) return *reinterpret_cast<const uint32_t *>(c);
+    const DMPQ_GLOBAL uint8_t *c = global_ptr<const uint8_t>(p) + i;
+    if constexpr (ALL) return *reinterpret_cast<const DMPQ_GLOBAL uint32_t *>(c);
     uint32_t w = 0;
 #pragma unroll
     for (int e = 0; e < 4; e++)
@@ -85,15 +96,16 @@ __device__ __forceinline__ uint32_t load_codes(const void *p, int64_t i, int n) 
     return w;
 }
 
+template <bool ALL>
 __device__ __forceinline__ void store_codes(void *p, int64_t i, int n, uint32_t w) {
-    uint8_t *c = static_cast<uint8_t *>(p) + i;
-    if (n >= 4) {
-        *reinterpret_cast<uint32_t *>(c) = w;
-        return;
-    }
+    DMPQ_GLOBAL uint8_t *c = global_ptr<uint8_t>(p) + i;
+    if constexpr (ALL) {
+        *reinterpret_cast<DMPQ_GLOBAL uint32_t *>(c) = w;
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; e++)
-        if (e < n) c[e] = (uint8_t)(w >> (8 * e));
+        for (int e = 0; e < 4; e++)
+            if (e < n) c[e] = (uint8_t)(w >> (8 * e));
+    }
 }
 
 __device__ __forceinline__ void decode4(uint32_t w, float s, float v[4]) {
@@ -103,10 +115,26 @@ __device__ __forceinline__ void decode4(uint32_t w, float s, float v[4]) {
     v[3] = __builtin_amdgcn_cvt_f32_fp8(w, 3) * s;
 }
 
-__device__ __forceinline__ uint32_t encode4(const float v[4], float inv) {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, w, true);
+__device__ __forceinline__ uint32_t encode4(const float v[4]) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
     return (uint32_t)w;
+}
+
+// The maximum of the wave's values, none negative (NaN counts as none), by DPP
+// shifts within the rows of 16 lanes and broadcasts between them: lane 63 ends
+// up with all.
+__device__ __forceinline__ float wave_max_dpp(float v) {
+#define DMPQ_DPP_MAX(CTRL, ROWS)                                                                        \
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false)))
+    DMPQ_DPP_MAX(0x111, 0xF);  // row_shr 1, 2, 4, 8
+    DMPQ_DPP_MAX(0x112, 0xF);
+    DMPQ_DPP_MAX(0x114, 0xF);
+    DMPQ_DPP_MAX(0x118, 0xF);
+    DMPQ_DPP_MAX(0x142, 0xA);  // the last lane of row 0 to row 1, of row 2 to row 3
+    DMPQ_DPP_MAX(0x143, 0xC);  // lane 31 to rows 2 and 3
+#undef DMPQ_DPP_MAX
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 // A block's scale and its reciprocal from its largest magnitude; a block whose
@@ -118,93 +146,115 @@ __device__ __forceinline__ void block_scale(float top, float &scale, float &inv)
     inv = fine ? inv : 0.0f;
 }
 
+// One block of 256 values, 4 to a lane: i is the lane's first, n what is left
+// of the tensor from there.
+template <int PT, int GT, int BITS, bool ALL>
+__device__ __forceinline__ void adamw_block(const AdamwTensor &t, const AdamwHyper &h, float clip, int64_t i, int n) {
+    float p[4], g[4], m[4], v[4], root[4];
+    const int64_t blk = i / kAdamwBlock;  // the same for all lanes
+    load4<PT, ALL>(t.p, i, n, p);
+    load4<GT, ALL>(t.g, i, n, g);
+    if constexpr (BITS == 32) {
+        load4<0, ALL>(t.m, i, n, m);
+        load4<0, ALL>(t.v, i, n, v);
+    } else {
+        const uint32_t cm = load_codes<ALL>(t.m, i, n), cv = load_codes<ALL>(t.v, i, n);
+        decode4(cm, global_ptr<const float>(t.ms)[blk], m);
+        decode4(cv, global_ptr<const float>(t.vs)[blk], v);
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] = v[e] * v[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const float gc = g[e] * clip;
+        m[e] = h.beta1 * m[e] + h.omb1 * gc;
+        v[e] = h.beta2 * v[e] + h.omb2 * (gc * gc);
+        root[e] = __builtin_sqrtf(v[e]);
+        const float den = root[e] * h.rbc2 + h.eps;
+        p[e] = p[e] * h.decay - h.step * (m[e] / den);
+    }
+    store4<PT, ALL>(t.p, i, n, p);
+    if (t.copy) store4<1, ALL>(t.copy, i, n, p);
+    if constexpr (BITS == 32) {
+        store4<0, ALL>(t.m, i, n, m);
+        store4<0, ALL>(t.v, i, n, v);
+    } else {
+        float tm = 0.0f, tv = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            if (ALL || e < n) {
+                tm = fmaxf(tm, __builtin_fabsf(m[e]));
+                tv = fmaxf(tv, root[e]);
+            }
+        }
+        float sm, im, sv, iv;
+        block_scale(wave_max_dpp(tm), sm, im);
+        block_scale(wave_max_dpp(tv), sv, iv);
+        const float least = sv > 0.0f ? 0.001953125f : 0.0f;  // 2^-9, code 1
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            m[e] = m[e] * im;
+            const float q = root[e] * iv;
+            root[e] = root[e] > 0.0f && q < least ? least : q;
+        }
+        store_codes<ALL>(t.m, i, n, encode4(m));
+        store_codes<ALL>(t.v, i, n, encode4(root));
+        if ((threadIdx.x & 63) == 0) {
+            global_ptr<float>(t.ms)[blk] = sm;
+            global_ptr<float>(t.vs)[blk] = sv;
+        }
+    }
+}
+
+// One workgroup to a chunk of 1024 values, a block to each wave: a wave's
+// loads all go out at once and nothing waits for its stores.
 template <int PT, int GT, int BITS>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamwTable T, AdamwHyper h, const double *__restrict__ norm) {
+    const AdamwTensor t = T.tensors[T.chunk_tensor[blockIdx.x]];
     float clip = 1.0f;
     if (norm) {
         const double nv = *norm;
         if (!__builtin_isfinite(nv)) return;  // nothing of this step is taken
         if (h.max_norm > 0.0 && nv > h.max_norm) clip = (float)(h.max_norm / nv);
     }
-    const AdamwTensor &t = T.tensors[T.chunk_tensor[blockIdx.x]];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t base = ((int64_t)blockIdx.x - t.first_chunk) * kAdamwChunk;
-#pragma unroll
-    for (int u = 0; u < kUnits; u++) {
-        const int64_t b0 = base + (int64_t)(wave * kUnits + u) * kAdamwBlock;
-        if (b0 >= t.n) break;
-        const int64_t i = b0 + 4 * lane;
-        const int n = (int)(t.n - i < 4 ? t.n - i : 4);  // <= 0: this lane has none
-        float p[4], g[4], m[4], v[4], root[4];
-        load4<PT>(t.p, i, n, p);
-        load4<GT>(t.g, i, n, g);
-        if constexpr (BITS == 32) {
-            load4<0>(t.m, i, n, m);
-            load4<0>(t.v, i, n, v);
-        } else {
-            decode4(load_codes(t.m, i, n), t.ms[b0 / kAdamwBlock], m);
-            decode4(load_codes(t.v, i, n), t.vs[b0 / kAdamwBlock], v);
-#pragma unroll
-            for (int e = 0; e < 4; e++) v[e] = v[e] * v[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const float gc = g[e] * clip;
-            m[e] = h.beta1 * m[e] + h.omb1 * gc;
-            v[e] = h.beta2 * v[e] + h.omb2 * (gc * gc);
-            root[e] = __builtin_sqrtf(v[e]);
-            const float den = root[e] * h.rbc2 + h.eps;
-            p[e] = p[e] * h.decay - h.step * (m[e] / den);
-        }
-        store4<PT>(t.p, i, n, p);
-        if (t.copy) store4<1>(t.copy, i, n, p);
-        if constexpr (BITS == 32) {
-            store4<0>(t.m, i, n, m);
-            store4<0>(t.v, i, n, v);
-        } else {
-            float tm = 0.0f, tv = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                if (e < n) {
-                    tm = fmaxf(tm, __builtin_fabsf(m[e]));
-                    tv = fmaxf(tv, root[e]);
-                }
-            }
-            float sm, im, sv, iv;
-            block_scale(wave_max(tm), sm, im);
-            block_scale(wave_max(tv), sv, iv);
-            uint32_t cv = encode4(root, iv);
-            if (sv > 0.0f) {
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    if (root[e] > 0.0f && ((cv >> (8 * e)) & 0xFFu) == 0u) cv |= 1u << (8 * e);
-            }
-            store_codes(t.m, i, n, encode4(m, im));
-            store_codes(t.v, i, n, cv);
-            if (lane == 0) {
-                t.ms[b0 / kAdamwBlock] = sm;
-                t.vs[b0 / kAdamwBlock] = sv;
-            }
-        }
-    }
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t b0 = ((int64_t)blockIdx.x - t.first_chunk) * kAdamwChunk + wave * kAdamwBlock;
+    if (b0 >= t.n) return;
+    const int64_t i = b0 + 4 * (threadIdx.x & 63);
+    if (b0 + kAdamwBlock <= t.n)  // wave-uniform
+        adamw_block<PT, GT, BITS, true>(t, h, clip, i, 4);
+    else
+        adamw_block<PT, GT, BITS, false>(t, h, clip, i, (int)(t.n - i < 4 ? t.n - i : 4));
 }
 
 // Sum of squares in fp64 (an fp32 gradient's square overflows fp32 above
-// 1.8e19): each workgroup walks over chunks, then one workgroup adds the
-// partials in order and takes the root.
+// 1.8e19): each workgroup takes a run of neighbouring chunks, tensor by
+// tensor, then one workgroup adds the partials in order and takes the root.
 template <int GT>
 __global__ __launch_bounds__(256) void grad_squares_kernel(AdamwTable T, double *__restrict__ partial) {
     __shared__ double red[4];
+    static_assert(kAdamwChunk == 1024, "a chunk is 4 values a thread");
     double acc = 0.0;
-    for (int64_t c = blockIdx.x; c < T.chunks; c += gridDim.x) {
-        const AdamwTensor &t = T.tensors[T.chunk_tensor[c]];
-        const int64_t base = (c - t.first_chunk) * kAdamwChunk;
+    const int64_t c1 = T.chunks * (blockIdx.x + 1) / gridDim.x;
+    int64_t c = T.chunks * blockIdx.x / gridDim.x;
+    int id = c < c1 ? __builtin_amdgcn_readfirstlane(T.chunk_tensor[c]) : 0;
+    while (c < c1) {
+        const AdamwTensor t = T.tensors[id++];
+        const int64_t end = t.first_chunk + (t.n + kAdamwChunk - 1) / kAdamwChunk;
+        const int64_t stop = end < c1 ? end : c1;
+        int64_t i = (c - t.first_chunk) * kAdamwChunk + 4 * (int64_t)threadIdx.x;
+        for (; c + 4 <= stop && (c + 4 - t.first_chunk) * kAdamwChunk <= t.n; c += 4, i += 4 * kAdamwChunk) {
+            float g[4][4];
 #pragma unroll
-        for (int u = 0; u < kAdamwChunk / 1024; u++) {
-            const int64_t i = base + 1024 * u + 4 * (int64_t)threadIdx.x;
-            const int n = (int)(t.n - i < 4 ? t.n - i : 4);
+            for (int u = 0; u < 4; u++) load4<GT, true>(t.g, i + u * kAdamwChunk, 4, g[u]);
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc += (double)g[u][e] * (double)g[u][e];
+        }
+        for (; c < stop; c++, i += kAdamwChunk) {
             float g[4];
-            load4<GT>(t.g, i, n, g);
+            load4<GT, false>(t.g, i, (int)(t.n - i < 4 ? t.n - i : 4), g);
 #pragma unroll
             for (int e = 0; e < 4; e++) acc += (double)g[e] * (double)g[e];
         }

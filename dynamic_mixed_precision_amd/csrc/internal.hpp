@@ -163,7 +163,7 @@ struct AdamwTensor {
     uint16_t *copy;
     int64_t n, first_chunk;
 };
-constexpr int kAdamwChunk = 4096;
+constexpr int kAdamwChunk = 1024;
 constexpr int kAdamwBlock = 256;  // values that share a scale of 8-bit states
 struct AdamwTable {
     const AdamwTensor *tensors;

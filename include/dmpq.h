@@ -518,7 +518,7 @@ typedef struct dmpq_adamw_tensor {
     int64_t n;
 } dmpq_adamw_tensor;
 /* Bytes of a table of the n_tensors tensors, 0 if a size is negative or the
- * tensors are too many or too large (2^31 chunks of 4096 values). */
+ * tensors are too many or too large (2^31 chunks of 1024 values). */
 size_t dmpq_adamw_table_bytes(const dmpq_adamw_tensor *h_tensors, int64_t n_tensors);
 /* Host, pure: fills h_table (the caller copies it to the device, 16-byte
  * aligned, and keeps it as long as the tensors keep their places).  p_dtype

@@ -111,7 +111,7 @@ def table(rows, p=0, g=0, bits=32, room=None):
 def test_table():
     sizes = [5, 0, 4096, 4097, 300000]
     st, chunks, raw = table([dict(n=n, p=P + 64 * i) for i, n in enumerate(sizes)])
-    per = [-(-n // 4096) for n in sizes]
+    per = [-(-n // 1024) for n in sizes]
     assert st == 0 and chunks == sum(per)
     rows = np.frombuffer(raw[:72 * len(sizes)], np.uint64).reshape(-1, 9)
     assert list(rows[:, 0]) == [P + 64 * i for i in range(len(sizes))]
