@@ -137,10 +137,20 @@ def _check(status: int, fn: str) -> None:
         raise DmpqError(status, fn, lib().dmpq_last_error().decode())
 
 
+_torch_c = None
+
+
 def _stream(stream=None) -> int:
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    """The stream's handle; None: the current stream of the current device (by
+    torch's raw query: building a Stream object takes longer than a launch)."""
+    global _torch_c
+    if stream is not None:
+        return stream.cuda_stream
+    if _torch_c is None:
+        import torch
+        torch.cuda.current_stream()  # initializes CUDA, or says why it cannot
+        _torch_c = torch._C
+    return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
 
 
 def _ptr(t) -> int | None:
@@ -164,7 +174,7 @@ def _need(t, name: str, nbytes: int, esize: int | None = None) -> None:
         raise ValueError(f"{name} is missing")
     if esize is not None and t.element_size() != esize:
         raise ValueError(f"{name} has {t.element_size()}-byte elements, needs {esize}-byte ones")
-    have = t.numel() * t.element_size()
+    have = t.nbytes
     if have < nbytes:
         raise ValueError(f"{name} holds {have} bytes, needs {nbytes}")
 
@@ -462,19 +472,15 @@ def selftest_codec(codec: int, lo: int, hi: int, stats, stream=None) -> None:
 
 def _need_lora(x_rows: int, a, b, rank, scale, seg_start, seg_adapter, t, K=None, N=None):
     """The pool and batch that every adapter call shares; returns (R, S, n)."""
-    pool = a if a is not None else b
-    if len(pool.shape) != 3:
-        raise ValueError(f"the adapter pool has shape {tuple(pool.shape)}, needs 3 dimensions")
-    n = pool.shape[0]
-    R = a.shape[1] if a is not None else b.shape[2]
+    n, R = _pool_shape(a if a is not None else b, a is not None)
     if a is not None:
-        _need(a, "a", 2 * n * R * K, 2)
-        if tuple(a.shape) != (n, R, K):
+        if a.shape != (n, R, K):
             raise ValueError(f"a has shape {tuple(a.shape)}, needs {(n, R, K)}")
+        _need(a, "a", 2 * n * R * K, 2)
     if b is not None:
-        _need(b, "b", 2 * n * N * R, 2)
-        if tuple(b.shape) != (n, N, R):
+        if b.shape != (n, N, R):
             raise ValueError(f"b has shape {tuple(b.shape)}, needs {(n, N, R)}")
+        _need(b, "b", 2 * n * N * R, 2)
     _need(rank, "rank", 4 * n, 4)
     if scale is not None:
         _need(scale, "scale", 4 * n, 4)
@@ -485,6 +491,13 @@ def _need_lora(x_rows: int, a, b, rank, scale, seg_start, seg_adapter, t, K=None
     _need(seg_adapter, "seg_adapter", 4 * S, 4)
     _need(t, "t", 4 * x_rows * R, 4)
     return R, S, n
+
+
+def _pool_shape(pool, is_a: bool):
+    shape = pool.shape
+    if len(shape) != 3:
+        raise ValueError(f"the adapter pool has shape {tuple(shape)}, needs 3 dimensions")
+    return shape[0], shape[1 if is_a else 2]
 
 
 def new_lora_workspace(M: int, N: int, K: int, R: int, S: int, n_adapters: int, device="cuda"):
