@@ -657,19 +657,29 @@ unsigned seg_tiles(const LoraBatch &B, int TM) {
     return (unsigned)(n < B.M ? n : B.M);
 }
 
-// Two forms by the number of rows.  From 8192 on, one tile of 48 to 80 rows to
-// each compute unit, or to each of a multiple of them (M / 256 rows: with 64
-// each, 17776 rows made 278 tiles, and the 22 units with two set the time:
-// 75 us where 16384 rows took 49).  Below, tiles of 16 rows and 16 ranks with
-// 16 waves, so that one token's K is read by 16 waves at once and ranks spread
-// over workgroups.
+// From 8192 rows on, one tile of 48 to 80 rows to each compute unit, or to
+// each of a multiple of them (M / 256 rows: with 64 each, 17776 rows made 278
+// tiles, and the 22 units with two set the time: 75 us where 16384 rows took
+// 49).  Below, by the number of 16 x 16 pieces of t: few, and each is a
+// workgroup of 16 waves, so that one token's K is read by 16 waves at once;
+// more, and 2 or 8 pieces share a workgroup's reads of x and a (1693 x 1920,
+// rank 64, 424 pieces: 6.9 us with 2, 9.3 with 1, 9.9 with 8; 8000 x 1920, rank
+// 64, 2000 pieces: 16.8, 31.4, 12.5).
 template <bool UP>
 hipError_t shrink(hipStream_t st, const uint16_t *x, const uint16_t *a, const LoraBatch &B, int64_t K, float *t,
                   uint16_t *packed) {
     if (B.M == 0) return hipSuccess;
     if (B.M < 8192) {
-        hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, UP>), dim3(seg_tiles(B, 16), B.R / 16), dim3(1024), 0, st, x,
-                           a, B, K, 16, t, packed);
+        const int pieces = (B.M + 15) / 16 * (B.R / 16);
+        if (pieces < 256)
+            hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, UP>), dim3(seg_tiles(B, 16), B.R / 16), dim3(1024), 0, st,
+                               x, a, B, K, 16, t, packed);
+        else if (pieces < 1024)
+            hipLaunchKernelGGL((lora_shrink_kernel<1, 2, 8, UP>), dim3(seg_tiles(B, 16), (B.R + 31) / 32), dim3(512), 0,
+                               st, x, a, B, K, 16, t, packed);
+        else
+            hipLaunchKernelGGL((lora_shrink_kernel<2, 4, 8, UP>), dim3(seg_tiles(B, 32), (B.R + 63) / 64), dim3(512), 0,
+                               st, x, a, B, K, 32, t, packed);
         return hipGetLastError();
     }
     const int64_t rounds = ((int64_t)B.M + 256 * 80 - 1) / (256 * 80);

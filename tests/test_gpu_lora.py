@@ -48,6 +48,8 @@ SHAPES = [
     (37, 80, 33, 32, "ragged", 4, 3), (16, 1920, 256, 64, "each", 16, 9), (200, 528, 257, 48, "ragged", 7, 4),
     (131, 272, 384, 96, "inside", 5, 2), (64, 112, 640, 128, "ragged", 3, 3), (150, 64, 136, 16, "each", 150, 11),
     (90, 96, 72, 112, "outside", 6, 3), (700, 32, 264, 80, "ragged", 130, 5),
+    # the middle forms of the shrink: 2 and 8 pieces a workgroup
+    (1000, 208, 40, 80, "ragged", 6, 3), (2100, 144, 24, 128, "inside", 5, 3),
     # enough rows for the large-tile shrink, every rank class
     (8200, 80, 72, 16, "ragged", 6, 3), (8200, 112, 40, 32, "inside", 9, 3), (8200, 64, 24, 64, "ragged", 70, 4),
     (8200, 144, 56, 128, "ragged", 3, 2),
@@ -298,7 +300,7 @@ class Grads:
 
 BACKWARD = [(1, 16, 16, 16, "one", 1, 1), (5, 48, 32, 16, "each", 5, 3), (37, 80, 48, 32, "ragged", 4, 3),
             (200, 528, 272, 48, "ragged", 7, 4), (131, 272, 384, 96, "inside", 5, 2), (64, 112, 640, 128, "ragged", 3, 3),
-            (900, 1008, 176, 64, "outside", 6, 3), (2500, 64, 144, 16, "ragged", 130, 5), (8200, 80, 144, 32, "ragged", 6, 3),
+            (900, 1008, 176, 64, "outside", 6, 3), (2100, 48, 208, 128, "ragged", 5, 3), (2500, 64, 144, 16, "ragged", 130, 5), (8200, 80, 144, 32, "ragged", 6, 3),
             (8200, 272, 48, 16, "one", 1, 2), (8200, 32, 96, 64, "inside", 70, 2), (8200, 48, 64, 128, "ragged", 4, 2)]
 
 
