@@ -416,7 +416,11 @@ __global__ __launch_bounds__(256) void lora_prep_kernel(const uint16_t *__restri
 // rows, but memory holds columns together: a lane loads 8 columns of 8 rows
 // (16 bytes each, 256 contiguous bytes per 16 lanes) and turns the 8 x 8
 // values in registers with 32 byte permutes, so that its q-th fragment holds
-// 8 rows of column n0 + 8 (l % 16) + q: one MFMA per q, no LDS.  The four
+// 8 rows of column n0 + 8 (l % 16) + q: one MFMA per q, no LDS.  Loads are
+// hidden by the other workgroup of the compute unit, so the registers of one
+// step have to let two in: with a second step's rows in flight, ranks above 32
+// left one, and 17776 x (7680 + 1920) took 125 us at rank 64 and 245 at 128,
+// against 97 and 157 (rank 32, two workgroups either way: 72 and 71).  The four
 // waves take every fourth step of the chunk's rows and add up in LDS in wave
 // order; a workgroup writes one partial per request that its chunk meets, at
 // slot chunk + request (unique, both only grow).  Rows of other requests in
@@ -434,12 +438,14 @@ template <int RC, bool WIDE>
 __device__ __forceinline__ void grad_strip(const uint16_t *__restrict__ src, const uint16_t *__restrict__ pk,
                                            const LoraBatch &B, int64_t C, const GradPlan &pl, int strip, int chunk,
                                            int jb, float *__restrict__ out, float *lds) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
     const int64_t n0 = (int64_t)strip * 128;
     const int64_t col = n0 + 8 * c;
     const bool in_col = col < C;
     const int j0 = jb * 16 * RC;
+    // the lane's place in a step: its first row and column (C <= 2^26: below 2^32 bytes)
+    const uint32_t at = 2 * ((uint32_t)(8 * q) * (uint32_t)C + 8 * c);
     const int r0 = chunk * pl.chunk, r1 = r0 + pl.chunk < B.M ? r0 + pl.chunk : B.M;
     for (int s = 0; s < B.S; s++) {
         int lo = seg_clamp(B.seg_start[s], B.M), hi = seg_clamp(B.seg_start[s + 1], B.M);
@@ -451,14 +457,15 @@ __device__ __forceinline__ void grad_strip(const uint16_t *__restrict__ src, con
         for (int i = 0; i < 8; i++)
 #pragma unroll
             for (int k = 0; k < RC; k++) acc[i][k] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-        v4i wa[8], wb[8], pf[RC][3];
-        auto load = [&](v4i(&w)[8], int m0) {
+        v4i w[8], pf[RC][3];
+        auto load = [&](int m0) {
             const int m = m0 + 8 * q;  // the lane's 8 rows
             const bool edge = m0 < lo || m0 + 32 > hi;  // wave-uniform
 #pragma unroll
             for (int r = 0; r < 8; r++) {
                 const bool ok = in_col && (!edge || (m + r >= lo && m + r < hi));
-                w[r] = ok ? ld16(src + (int64_t)(m + r) * C + col) : (v4i){0, 0, 0, 0};
+                const char *row = reinterpret_cast<const char *>(src + (int64_t)(m0 + r) * C + n0);  // wave-uniform
+                w[r] = ok ? ld16(row + at) : (v4i){0, 0, 0, 0};
             }
         };
         auto parts = [&](int m0) {
@@ -466,9 +473,9 @@ __device__ __forceinline__ void grad_strip(const uint16_t *__restrict__ src, con
             for (int k = 0; k < RC; k++)
 #pragma unroll
                 for (int p = 0; p < 3; p++)
-                    pf[k][p] = ld16(pk + packed_at(m0 + 8 * q, p, (j0 + 16 * k < B.R ? j0 + 16 * k : 0) + c, B.R));
+                    pf[k][p] = ld16(pk + packed_at(m0, p, j0 + 16 * k < B.R ? j0 + 16 * k : 0, B.R) + 8 * lane);
         };
-        auto mul = [&](v4i(&w)[8], int m0) {
+        auto mul = [&](int m0) {
             const int m = m0 + 8 * q;
             if (m0 < lo || m0 + 32 > hi) {  // wave-uniform
 #pragma unroll
@@ -504,17 +511,17 @@ __device__ __forceinline__ void grad_strip(const uint16_t *__restrict__ src, con
                     }
             }
         };
-        // the next step's rows go out before this step's products
+        // the next step's operands go out once this step's products have taken theirs
         const int first = (lo & ~31) + 32 * wave;
-        if (first < hi) load(wa, first);
-        for (int m0 = first; m0 < hi; m0 += 256) {
-            parts(m0);
-            if (m0 + 128 < hi) load(wb, m0 + 128);
-            mul(wa, m0);
+        if (first < hi) {
+            parts(first);
+            load(first);
+        }
+        for (int m0 = first; m0 < hi; m0 += 128) {
+            mul(m0);
             if (m0 + 128 < hi) {
                 parts(m0 + 128);
-                if (m0 + 256 < hi) load(wa, m0 + 256);
-                mul(wb, m0 + 128);
+                load(m0 + 128);
             }
         }
         // waves 1..3 add to wave 0 in order, 8 * RC pieces of 64 x 16 bytes
@@ -565,7 +572,7 @@ __device__ __forceinline__ void grad_strip(const uint16_t *__restrict__ src, con
 }
 
 template <int RC>
-__global__ __launch_bounds__(256, RC < 4 ? 2 : 1) void lora_grad_kernel(const uint16_t *__restrict__ dy,
+__global__ __launch_bounds__(256, 2) void lora_grad_kernel(const uint16_t *__restrict__ dy,
                                                         const uint16_t *__restrict__ x,
                                                         const uint16_t *__restrict__ tp,
                                                         const uint16_t *__restrict__ up, LoraBatch B, int64_t N,
@@ -613,12 +620,13 @@ __global__ __launch_bounds__(256) void lora_grad_sum_kernel(const float *__restr
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-// Rows of a chunk, a multiple of kGradRows: strips x chunks up to 1024
-// workgroups (two rounds of the two that a compute unit holds), not more,
-// since each writes a partial that is read again.
-int grad_chunk(int64_t M, int64_t N, int64_t K) {
-    const int64_t strips = (N + 127) / 128 + (K + 127) / 128;
-    int64_t chunks = 1024 / (strips > 0 ? strips : 1);
+// Rows of a chunk, a multiple of kGradRows: up to 512 workgroups (the two that
+// each compute unit holds), counting the two for ranks above 64.  More write
+// more partials that are read again (8000 x 1920 + 1920, rank 128, the whole
+// backward pass: 121 us with 512, 147 with twice as many).
+int grad_chunk(int64_t M, int64_t N, int64_t K, int64_t R) {
+    const int64_t strips = ((N + 127) / 128 + (K + 127) / 128) * ((R + 63) / 64);
+    int64_t chunks = 512 / (strips > 0 ? strips : 1);
     if (chunks < 1) chunks = 1;
     return (int)round_up(M > 0 ? (M + chunks - 1) / chunks : 1, kGradRows);
 }
@@ -630,7 +638,7 @@ struct BackwardLayout {
 
 BackwardLayout backward_layout(int64_t M, int64_t N, int64_t K, int64_t R, int64_t S, int64_t nA) {
     BackwardLayout L;
-    L.chunk = grad_chunk(M, N, K);
+    L.chunk = grad_chunk(M, N, K, R);
     L.slots = (int)((M + L.chunk - 1) / L.chunk + S);
     const size_t packed = 2 * 3 * (size_t)R * round_up(M, 32);
     size_t o = 0;
