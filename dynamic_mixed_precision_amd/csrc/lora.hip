@@ -358,22 +358,34 @@ __global__ __launch_bounds__(256) void lora_prep_kernel(const uint16_t *__restri
                                                         const float *__restrict__ t, LoraBatch B, int64_t N, int64_t K,
                                                         PrepPlan pl, uint16_t *__restrict__ at,
                                                         uint16_t *__restrict__ bt, uint16_t *__restrict__ tp) {
-    __shared__ uint16_t tile[64 * (kMaxLoraRank + 2)];
+    __shared__ __attribute__((aligned(16))) uint16_t tile[64 * (kMaxLoraRank + 2)];
     int blk = blockIdx.x;
     const int tid = threadIdx.x, R = B.R;
+    const int pieces = R / 8;
+    // 8 values of 8 different rows of the tile, packed as one piece
+    auto column = [&](int r, int j) {
+        v4i o;
+#pragma unroll
+        for (int d = 0; d < 4; d++)
+            o[d] = tile[(r + 2 * d) * (R + 2) + j] | (uint32_t)tile[(r + 2 * d + 1) * (R + 2) + j] << 16;
+        return o;
+    };
     if (blk < pl.nb * B.nA) {
         const int i = blk / pl.nb, rank = adapter_rank(B, i);
         const int64_t n0 = (int64_t)(blk % pl.nb) * 64;
         const uint16_t *src = b + (int64_t)i * N * R;
-        for (int e = tid; e < 64 * R; e += 256) {
-            const int r = e / R, j = e % R;
-            tile[r * (R + 2) + j] = n0 + r < N && j < rank ? src[(n0 + r) * R + j] : (uint16_t)0;
+        for (int e = tid; e < 64 * pieces; e += 256) {
+            const int r = e / pieces, j = e % pieces * 8;
+            v4i v = {0, 0, 0, 0};
+            if (n0 + r < N) v = keep8(ld16(src + (n0 + r) * R + j), rank - j);
+#pragma unroll
+            for (int d = 0; d < 4; d++) *reinterpret_cast<int *>(tile + r * (R + 2) + j + 2 * d) = v[d];
         }
         __syncthreads();
         uint16_t *dst = bt + (int64_t)i * R * N;
-        for (int e = tid; e < 64 * R; e += 256) {
-            const int r = e & 63, j = e >> 6;
-            if (n0 + r < N) dst[(int64_t)j * N + n0 + r] = tile[r * (R + 2) + j];
+        for (int e = tid; e < 8 * R; e += 256) {
+            const int r = (e & 7) * 8, j = e >> 3;
+            if (n0 + r < N) *reinterpret_cast<v4i *>(dst + (int64_t)j * N + n0 + r) = column(r, j);
         }
         return;
     }
@@ -382,15 +394,24 @@ __global__ __launch_bounds__(256) void lora_prep_kernel(const uint16_t *__restri
         const int i = blk / pl.na, rank = adapter_rank(B, i);
         const int64_t k0 = (int64_t)(blk % pl.na) * 64;
         const uint16_t *src = a + (int64_t)i * R * K;
-        for (int e = tid; e < 64 * R; e += 256) {
-            const int r = e & 63, j = e >> 6;
-            tile[r * (R + 2) + j] = k0 + r < K && j < rank ? src[(int64_t)j * K + k0 + r] : (uint16_t)0;
+        for (int e = tid; e < 8 * R; e += 256) {
+            const int r = (e & 7) * 8, j = e >> 3;
+            v4i v = {0, 0, 0, 0};
+            if (k0 + r < K && j < rank) v = ld16(src + (int64_t)j * K + k0 + r);
+#pragma unroll
+            for (int d = 0; d < 4; d++) {
+                tile[(r + 2 * d) * (R + 2) + j] = (uint16_t)v[d];
+                tile[(r + 2 * d + 1) * (R + 2) + j] = (uint16_t)((uint32_t)v[d] >> 16);
+            }
         }
         __syncthreads();
         uint16_t *dst = at + (int64_t)i * K * R;
-        for (int e = tid; e < 64 * R; e += 256) {
-            const int r = e / R, j = e % R;
-            if (k0 + r < K) dst[(k0 + r) * R + j] = tile[r * (R + 2) + j];
+        for (int e = tid; e < 64 * pieces; e += 256) {
+            const int r = e / pieces, j = e % pieces * 8;
+            v4i v;
+#pragma unroll
+            for (int d = 0; d < 4; d++) v[d] = *reinterpret_cast<const int *>(tile + r * (R + 2) + j + 2 * d);
+            if (k0 + r < K) *reinterpret_cast<v4i *>(dst + (k0 + r) * R + j) = v;
         }
         return;
     }
