@@ -784,13 +784,24 @@ hipError_t launch_lora_backward(hipStream_t s, const uint16_t *dy, const uint16_
         if (e != hipSuccess) return e;
         GradPlan gp{L.chunk, (int)((N + 127) / 128), (int)((K + 127) / 128)};
         const unsigned strips = (unsigned)(gp.strips_n + gp.strips_k), chunks = (unsigned)((B.M + L.chunk - 1) / L.chunk);
-        if (B.R <= 16)
-            hipLaunchKernelGGL(lora_grad_kernel<1>, dim3(strips, chunks, 1), dim3(256), 0, s, dy, x, tp, up, B, N, K, gp, pb, pa);
+        // 16 ranks a workgroup while the chunks are short (a wave takes at most two
+        // steps of one) and all workgroups fit on the chip at once, four to a
+        // compute unit: then a workgroup's latency is the time.  The whole backward
+        // pass at 1920 + 1920 with 16 ranks a workgroup and with all of them (at
+        // most 64): 903 rows, rank 64: 36 and 43 us; 300 rows, rank 128: 42 and 53;
+        // 2000 rows, rank 32, chunks of 128: 34 and 37; 4000, of 256: 40.1 and 41.2;
+        // 6000, of 384: 50.8 and 49.5; 10000, of 640: 73 and 69, since dy and x are
+        // read once more.
+#define DMPQ_GRAD(RC_) \
+    hipLaunchKernelGGL(lora_grad_kernel<RC_>, dim3(strips, chunks, (B.R + 16 * RC_ - 1) / (16 * RC_)), dim3(256), 0, s, dy, \
+                       x, tp, up, B, N, K, gp, pb, pa)
+        if (B.R <= 16 || (L.chunk <= 256 && (int64_t)strips * chunks * (B.R / 16) <= 1024))
+            DMPQ_GRAD(1);
         else if (B.R <= 32)
-            hipLaunchKernelGGL(lora_grad_kernel<2>, dim3(strips, chunks, 1), dim3(256), 0, s, dy, x, tp, up, B, N, K, gp, pb, pa);
+            DMPQ_GRAD(2);
         else
-            hipLaunchKernelGGL(lora_grad_kernel<4>, dim3(strips, chunks, (B.R + 63) / 64), dim3(256), 0, s, dy, x, tp, up, B, N, K,
-                               gp, pb, pa);
+            DMPQ_GRAD(4);
+#undef DMPQ_GRAD
         e = hipGetLastError();
         if (e != hipSuccess) return e;
         LoraBatch one = B;  // u already carries the scales, at the ranks' zeros
