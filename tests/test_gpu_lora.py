@@ -320,6 +320,21 @@ def test_backward(M, K, N, R, kind, S, n):
     assert none["dx"] is None and torch.equal(none["da"], out["da"]) and torch.equal(none["db"], out["db"])
 
 
+# long chunks of rows: a workgroup of the gradients then takes up to 64 ranks at
+# once, with ranks, columns and requests that end inside its tiles
+@pytest.mark.parametrize("M,K,N,R,kind,S,n", [
+    (8300, 1008, 1008, 32, "ragged", 7, 3), (8300, 1008, 1040, 48, "inside", 9, 3), (8447, 912, 1104, 64, "outside", 6, 2),
+    (4300, 1008, 1008, 112, "ragged", 5, 3), (8705, 1024, 1024, 16, "ragged", 40, 4)])
+def test_backward_of_long_chunks(M, K, N, R, kind, S, n):
+    require_gpu()
+    say(f"lora_backward {M} {K} {N} {R} {kind} {S}")
+    g = Grads(Batch(M, K, N, R, kind, S, n, seed=M + K + N + R))
+    out = g.run()
+    g.check(out)
+    again = g.run()
+    assert all(torch.equal(out[k].view(torch.uint8), again[k].view(torch.uint8)) for k in out)
+
+
 def test_backward_of_no_rows_is_zero():
     require_gpu()
     q = Batch(0, 32, 48, 16, "ragged", 2, 2, seed=1)
