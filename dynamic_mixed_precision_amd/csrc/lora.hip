@@ -441,7 +441,7 @@ __global__ __launch_bounds__(256) void lora_prep_kernel(const uint16_t *__restri
 // hidden by the other workgroup of the compute unit, so the registers of one
 // step have to let two in: with a second step's rows in flight, ranks above 32
 // left one, and 17776 x (7680 + 1920) took 125 us at rank 64 and 245 at 128,
-// against 97 and 157 (rank 32, two workgroups either way: 72 and 71).  The four
+// against 90 and 157 (rank 32, two workgroups either way: 72 and 71).  The four
 // waves take every fourth step of the chunk's rows and add up in LDS in wave
 // order; a workgroup writes one partial per request that its chunk meets, at
 // slot chunk + request (unique, both only grow).  Rows of other requests in
