@@ -350,7 +350,7 @@ __device__ __forceinline__ void lora_epilogue(AccV (&acc)[4][4], Scale &sc, uint
                     sc((float)acc[i][j][4 * g + 2], j, g, 2), sc((float)acc[i][j][4 * g + 3], j, g, 3));
         LoraRows<AHEAD> next;
         if (i < 3) T.load_t(lora, i + 1, next);
-        lora_band_add<ES == 2 ? 2 : 3, AHEAD>(lora, T, i, n0, N, lds, t);
+        lora_band_add<AHEAD>(lora, T, i, n0, N, lds, t);
         if (i < 3) t = next;
         amax = fmaxf(amax, epi_band_to_global<ES, EPI, 32, true>(band, y, M, N, m0 + wm * 128 + i * 32,
                                                                  n0 + wn * 128, lane, vec));
@@ -410,7 +410,7 @@ __device__ __forceinline__ void split_fixup_epilogue(const uint32_t *part, Scale
         for (int j = 0; j < 4; j++)
 #pragma unroll
             for (int r = 0; r < 16; r++) add[j][r] = 0.0f;
-        lora_slice<ES == 2 ? 2 : 3>(lora, m0 + wm * 128 + i * 32 + lm, n0 + wn * 128, N, lane, add);
+        lora_slice(lora, m0 + wm * 128 + i * 32 + lm, n0 + wn * 128, N, lane, add);
     }
 #pragma unroll
     for (int j = 0; j < 4; j++) {

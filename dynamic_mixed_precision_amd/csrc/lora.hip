@@ -8,9 +8,9 @@
 //
 // Every product has one dimension of at most 128, so all of them are bound by
 // the one pass over their widest tensor.  MFMA does the products: x, dy, a and
-// b are bf16 and exact in it; t and u are fp32 and enter as 2 bf16 parts where
-// the result is rounded to bf16 anyway and as 3 where it stays fp32 (split8).
-// Sums are fp32 in a fixed order: no atomics, the same bits on every call.
+// b are bf16 and exact in it; t and u are fp32 and enter as 3 bf16 parts that
+// hold all their bits (split8).  Sums are fp32 in a fixed order: no atomics, the
+// same bits on every call.
 #include "device.hpp"
 #include "gemm_common.hpp"
 #include "gemm_dma.hpp"
@@ -169,12 +169,11 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(const uint16_t 
 // four blocks a workgroup, at 17776 x 12288 bf16).  Neighbouring workgroups
 // take neighbouring columns (rows first: 4.5 TB/s).  The block's b, one
 // contiguous piece of memory, goes through registers into LDS, entries past
-// the rank as zeros.  t, as 2 bf16 parts for a bf16 y and 3 for fp32, is the
-// 32x32x16 MFMA's first operand, so a lane's 16 accumulators are 16 rows of
-// one column; the second operand of MFMA p holds b's rows n0 + 4 i + p for
-// lanes i, so the four MFMAs leave every lane four consecutive columns of
-// those rows, and base and y move in 8- or 16-byte pieces, 32 lanes a row,
-// straight between memory and registers.
+// the rank as zeros.  t, in bf16 parts, is the 32x32x16 MFMA's first operand,
+// so a lane's 16 accumulators are 16 rows of one column; the second operand of
+// MFMA p holds b's rows n0 + 4 i + p for lanes i, so the four MFMAs leave every
+// lane four consecutive columns of those rows, and base and y move in 8- or
+// 16-byte pieces, 32 lanes a row, straight between memory and registers.
 // ---------------------------------------------------------------------------
 constexpr int kExpandRows = 128, kExpandCols = 128, kExpandWaves = 4;
 
@@ -242,7 +241,6 @@ __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const
                                                                            const void *base,
                                                                            const uint16_t *__restrict__ b, LoraBatch B,
                                                                            int64_t N, unsigned cols, void *y) {
-    constexpr int NS = ES == 2 ? 2 : 3;
     // b's row 4 i + p of the block lies at LDS row 32 p + i; 16 bytes of
     // padding spread the lanes' 16-byte reads over the banks
     constexpr int ROW = 32 * RC + 16;
@@ -320,13 +318,13 @@ __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const
             const v4f a0 = *reinterpret_cast<const v4f *>(tw + li * TROW + 32 * lh);
             const v4f a1 = *reinterpret_cast<const v4f *>(tw + li * TROW + 32 * lh + 16);
             const float v[8] = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
-            v4i tf[NS], bf[4];
-            split8<NS>(v, tf);
+            v4i tf[kParts], bf[4];
+            split8(v, tf);
 #pragma unroll
             for (int p = 0; p < 4; p++)
                 bf[p] = *reinterpret_cast<const v4i *>(lds + (32 * p + li) * ROW + 32 * c + 16 * lh);
 #pragma unroll
-            for (int s = NS - 1; s >= 0; s--)
+            for (int s = kParts - 1; s >= 0; s--)
 #pragma unroll
                 for (int p = 0; p < 4; p++) acc[p] = mfma32(tf[s], bf[p], acc[p]);
         }
@@ -424,8 +422,8 @@ __global__ __launch_bounds__(256) void lora_prep_kernel(const uint16_t *__restri
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) v[i] = m0 + i < B.M ? t[(m0 + i) * R + j] : 0.0f;
-    v4i p[3];
-    split8<3>(v, p);
+    v4i p[kParts];
+    split8(v, p);
 #pragma unroll
     for (int i = 0; i < 3; i++) *reinterpret_cast<v4i *>(tp + packed_at((int)m0, i, j, R)) = p[i];
 }

@@ -93,23 +93,26 @@ __device__ __forceinline__ int adapter_rank(const LoraBatch &B, int a) {
 }
 
 // ---- fp32 as a sum of bf16 values -------------------------------------------
-// The bf16 MFMA multiplies an fp32 operand as NS bf16 parts, each the nearest
-// to what the parts before it leave: 2 parts keep 16 bits and more of it
-// (error at most 2^-18 of the value), 3 parts all 24.  bf16 has fp32's
-// exponents, so nothing overflows but values within half a bf16 step of
-// FLT_MAX; an infinite or NaN value is its own first part, the others 0.
-template <int NS>
-__device__ __forceinline__ void split8(const float v[8], v4i (&out)[NS]) {
+// The bf16 MFMA multiplies an fp32 operand as 3 bf16 parts, each the nearest to
+// what the parts before it leave: together all its 24 bits.  Results that are
+// rounded to bf16 take 3 parts too: where the adapter term cancels against what
+// it is added to, the 2^-18 of it that 2 parts lose is many bf16 steps of the
+// result.  bf16 has fp32's exponents, so nothing overflows but values within
+// half a bf16 step of FLT_MAX; an infinite or NaN value is its own first part,
+// the others 0.
+constexpr int kParts = 3;
+
+__device__ __forceinline__ void split8(const float v[8], v4i (&out)[kParts]) {
     float r[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) r[i] = v[i];
 #pragma unroll
-    for (int p = 0; p < NS; p++) {
+    for (int p = 0; p < kParts; p++) {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             const uint32_t w = cvt_pk_bf16(r[2 * i], r[2 * i + 1]);
             out[p][i] = (int)w;
-            if (p + 1 < NS) {
+            if (p + 1 < kParts) {
                 const float lo = bf16_lo(w), hi = bf16_hi(w);
                 r[2 * i] = __builtin_isfinite(lo) ? r[2 * i] - lo : 0.0f;
                 r[2 * i + 1] = __builtin_isfinite(hi) ? r[2 * i + 1] - hi : 0.0f;
@@ -141,19 +144,17 @@ __device__ __forceinline__ v4f mfma16(const v4i &a, const v4i &b, const v4f &c) 
 // v += scale * t b^T for 32 rows x 128 columns in the GEMMs' accumulator
 // layout: lane l holds row l % 32 (`row`; past M: nothing is added) and, in
 // v[j][4g + e], column n0 + 32 j + 8 g + 4 (l / 32) + e.  b's rows are the
-// MFMA's first operand, scale * t in NS bf16 parts (split8) the second.  Where
+// MFMA's first operand, scale * t in bf16 parts (split8) the second.  Where
 // all rows share an adapter the products accumulate straight onto v.  Rows of
 // several adapters take one product per adapter over all 32 rows, added where
 // it belongs and never multiplied by zero elsewhere: one adapter's infinity
 // must not reach another request's rows.
-template <int NS>
-__device__ __forceinline__ void lora_t_frag(const float *tr, float sc, v4i (&tf)[NS]) {
+__device__ __forceinline__ void lora_t_frag(const float *tr, float sc, v4i (&tf)[kParts]) {
     const v4f a0 = *reinterpret_cast<const v4f *>(tr), a1 = *reinterpret_cast<const v4f *>(tr + 4);
     const float v[8] = {sc * a0[0], sc * a0[1], sc * a0[2], sc * a0[3], sc * a1[0], sc * a1[1], sc * a1[2], sc * a1[3]};
-    split8<NS>(v, tf);
+    split8(v, tf);
 }
 
-template <int NS>
 __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_t n0, int64_t N, int lane,
                                            v16f (&v)[4]) {
     const LoraBatch &B = L.batch;
@@ -177,14 +178,14 @@ __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_
         const int64_t off = (int64_t)a * N * B.R;
         if (own == in_m) {
             for (int c = 0; c < rank; c += 16) {
-                v4i tf[NS];
-                lora_t_frag<NS>(tr + c, sc, tf);
+                v4i tf[kParts];
+                lora_t_frag(tr + c, sc, tf);
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     v4i bf = *reinterpret_cast<const v4i *>(bl[j] + off + c);
                     if (c + 16 > rank) bf = keep8(bf, rank - c - 8 * lh);
 #pragma unroll
-                    for (int p = NS - 1; p >= 0; p--) v[j] = mfma32(bf, tf[p], v[j]);
+                    for (int p = kParts - 1; p >= 0; p--) v[j] = mfma32(bf, tf[p], v[j]);
                 }
             }
         } else {
@@ -194,12 +195,12 @@ __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_
 #pragma unroll
                 for (int e = 0; e < 16; e++) d[e] = 0.0f;
                 for (int c = 0; c < rank; c += 16) {
-                    v4i tf[NS];
-                    lora_t_frag<NS>(tr + c, sc, tf);
+                    v4i tf[kParts];
+                    lora_t_frag(tr + c, sc, tf);
                     v4i bf = *reinterpret_cast<const v4i *>(bl[j] + off + c);
                     if (c + 16 > rank) bf = keep8(bf, rank - c - 8 * lh);
 #pragma unroll
-                    for (int p = NS - 1; p >= 0; p--) d = mfma32(bf, tf[p], d);
+                    for (int p = kParts - 1; p >= 0; p--) d = mfma32(bf, tf[p], d);
                 }
 #pragma unroll
                 for (int e = 0; e < 16; e++) v[j][e] = mine == a ? v[j][e] + d[e] : v[j][e];
@@ -354,7 +355,7 @@ __device__ __forceinline__ LoraTile lora_tile_begin(const LoraEpi &L, int64_t m0
 
 // Slice i of every wave.  Called by all four waves after they wrote their
 // bands (lds + wave * kLoraBandBytes); returns with the wave's own band ready.
-template <int NS, int AHEAD>
+template <int AHEAD>
 __device__ __forceinline__ void lora_band_add(const LoraEpi &L, LoraTile &T, int i, int64_t n0, int64_t N,
                                               uint8_t *lds, const LoraRows<AHEAD> &t) {
     const LoraBatch &B = L.batch;
@@ -387,13 +388,13 @@ __device__ __forceinline__ void lora_band_add(const LoraEpi &L, LoraTile &T, int
             auto piece = [&](int c, const v4f &a0, const v4f &a1) {
                 const float v[8] = {T.sc * a0[0], T.sc * a0[1], T.sc * a0[2], T.sc * a0[3],
                                     T.sc * a1[0], T.sc * a1[1], T.sc * a1[2], T.sc * a1[3]};
-                v4i tf[NS], bf[4];
-                split8<NS>(v, tf);
+                v4i tf[kParts], bf[4];
+                split8(v, tf);
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                     bf[j] = *reinterpret_cast<const v4i *>(bs + (wn * 128 + 32 * j + lm) * brow + 2 * c + 16 * lh);
 #pragma unroll
-                for (int p = NS - 1; p >= 0; p--)
+                for (int p = kParts - 1; p >= 0; p--)
 #pragma unroll
                     for (int j = 0; j < 4; j++) d[j] = mfma32(bf[j], tf[p], d[j]);
             };

@@ -432,9 +432,9 @@ dmpq_status dmpq_selftest_codec(hipStream_t stream, int codec, uint32_t lo, uint
  *   if they do not ascend the results are unspecified, and no access is out
  *   of bounds.
  * Sums are fp32 in a fixed order (the same bits on every call).  t is fp32;
- * where it enters a product it is split into bf16 parts that keep 16 bits of
- * it for a bf16 result and all 24 for an fp32 one.  A value that is not finite
- * stays within its own row (forward) or its own adapter (gradients).
+ * where it enters a product it is split into bf16 parts that keep all its
+ * bits.  A value that is not finite stays within its own row (forward) or its
+ * own adapter (gradients).
  * ========================================================================= */
 
 /* t [M x R] fp32 = x a^T, each row through its own adapter's a; zeros past the
