@@ -11,6 +11,8 @@
 // b are bf16 and exact in it; t and u are fp32 and enter as 3 bf16 parts that
 // hold all their bits (split8).  Sums are fp32 in a fixed order: no atomics, the
 // same bits on every call.
+#include <type_traits>
+
 #include "device.hpp"
 #include "gemm_common.hpp"
 #include "gemm_dma.hpp"
@@ -148,13 +150,11 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(const uint16_t 
         }
         t[(int64_t)(st.row0 + r) * B.R + j0 + j] = v;
         if constexpr (UP) {
-            float rest = v;
+            float rest = v;  // as split8
 #pragma unroll
-            for (int p = 0; p < 3; p++) {
-                const uint32_t h = f32_to_bf16(rest);
-                packed[packed_at(st.row0 + r, p, j0 + j, B.R)] = (uint16_t)h;
-                const float f = bf16_lo(h);
-                rest = __builtin_isfinite(f) ? rest - f : 0.0f;
+            for (int p = 0; p < kParts; p++) {
+                packed[packed_at(st.row0 + r, p, j0 + j, B.R)] = (uint16_t)(__float_as_uint(rest) >> 16);
+                rest = split_rest(p == 0 ? split_finite(rest) : rest);
             }
         }
     }
@@ -247,6 +247,7 @@ __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const
     __shared__ __attribute__((aligned(16))) uint8_t lds[kExpandCols * ROW];
     constexpr int TROW = 16 * 4 + 16;  // 16 ranks of a row of t and padding
     __shared__ __attribute__((aligned(16))) uint8_t tlds[kExpandWaves][32 * TROW];
+    __shared__ int odd_b[kExpandWaves];  // whether the b that a wave copied holds an infinity or NaN
     typedef Quad<ES> Q;
     const unsigned tile = blockIdx.x / cols, cb = blockIdx.x - tile * cols;
     SegTile st;
@@ -298,12 +299,25 @@ __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const
         const int rank = adapter_rank(B, st.adapter);
         if (B.scale) sc = B.scale[st.adapter];
         const int per_row = B.R / 8;  // 16-byte pieces of a row of b
+        u16x2 top = {0, 0};
 #pragma unroll
         for (int k = 0; k < RC; k++) {
             const int e = tid + 256 * k, n = e / per_row, c = e - n * per_row;
-            if (n < kExpandCols)
-                *reinterpret_cast<v4i *>(lds + (32 * (n & 3) + (n >> 2)) * ROW + 16 * c) = keep8(piece[k], rank - 8 * c);
+            piece[k] = keep8(piece[k], rank - 8 * c);
+            if (n < kExpandCols) {
+                *reinterpret_cast<v4i *>(lds + (32 * (n & 3) + (n >> 2)) * ROW + 16 * c) = piece[k];
+                magnitudes8(piece[k], top);
+            }
         }
+        const uint64_t any = __ballot(nonfinite_in(top));
+        if (lane == 0) odd_b[wave] = any != 0;
+        if (__builtin_expect(any != 0, 0))
+#pragma unroll
+            for (int k = 0; k < RC; k++) {
+                const int e = tid + 256 * k, n = e / per_row, c = e - n * per_row;
+                if (n < kExpandCols)
+                    *reinterpret_cast<v4i *>(lds + (32 * (n & 3) + (n >> 2)) * ROW + 16 * c) = ones8(piece[k]);
+            }
         __syncthreads();
         if (wrows <= 0) return;
 #pragma unroll
@@ -327,6 +341,22 @@ __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const
             for (int s = kParts - 1; s >= 0; s--)
 #pragma unroll
                 for (int p = 0; p < 4; p++) acc[p] = mfma32(tf[s], bf[p], acc[p]);
+        }
+        if (__builtin_expect(__builtin_amdgcn_readfirstlane(odd_b[0] | odd_b[1] | odd_b[2] | odd_b[3]), 0)) {
+            // b's infinities and NaN, from memory
+            const float *tr = t + (int64_t)(row0 + (li < wrows ? li : wrows - 1)) * B.R + 8 * lh;
+            const int64_t n = (int64_t)cb * kExpandCols + 4 * li;
+#pragma unroll 1
+            for (int c = 0; c < rank; c += 16) {
+                const v4f a0 = *reinterpret_cast<const v4f *>(tr + c), a1 = *reinterpret_cast<const v4f *>(tr + c + 4);
+                const float v[8] = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
+                const v4i sf = sign8(v);
+#pragma unroll
+                for (int p = 0; p < 4; p++) {
+                    const v4i f = ld16(bw + (n + p < N ? n + p : N - 1) * B.R + c + 8 * lh);
+                    acc[p] = mfma32(sf, odd8(keep8(f, rank - c - 8 * lh)), acc[p]);
+                }
+            }
         }
     }
 #pragma unroll
@@ -443,7 +473,9 @@ __global__ __launch_bounds__(256) void lora_prep_kernel(const uint16_t *__restri
 // waves take every fourth step of the chunk's rows and add up in LDS in wave
 // order; a workgroup writes one partial per request that its chunk meets, at
 // slot chunk + request (unique, both only grow).  Rows of other requests in
-// the same step are read as zeros in both operands.
+// the same step are read as zeros in both operands.  Where a wave's sums come out
+// not finite, it takes its rows again with dy's or x's infinities kept from the
+// later parts of p (split8): looking for them beforehand would cost every call.
 // WIDE (da): G is stored [j][c], else (db) [c][j].
 // ---------------------------------------------------------------------------
 constexpr int kGradRows = 128;  // rows of a chunk: a multiple of 4 waves x 32
@@ -472,10 +504,6 @@ __device__ __forceinline__ void grad_strip(const uint16_t *__restrict__ src, con
         hi = hi < r1 ? hi : r1;
         if (lo >= hi || seg_adapter_of(B, s) < 0) continue;  // workgroup-uniform
         v4f acc[8][RC];
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-#pragma unroll
-            for (int k = 0; k < RC; k++) acc[i][k] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
         v4i w[8], pf[RC][3];
         auto load = [&](int m0) {
             const int m = m0 + 8 * q;  // the lane's 8 rows
@@ -494,7 +522,8 @@ __device__ __forceinline__ void grad_strip(const uint16_t *__restrict__ src, con
                 for (int p = 0; p < 3; p++)
                     pf[k][p] = ld16(pk + packed_at(m0, p, j0 + 16 * k < B.R ? j0 + 16 * k : 0, B.R) + 8 * lane);
         };
-        auto mul = [&](int m0) {
+        // apart: infinities of src kept from the later parts of p
+        auto mul = [&](int m0, auto apart) {
             const int m = m0 + 8 * q;
             if (m0 < lo || m0 + 32 > hi) {  // wave-uniform
 #pragma unroll
@@ -511,36 +540,70 @@ __device__ __forceinline__ void grad_strip(const uint16_t *__restrict__ src, con
 #pragma unroll
             for (int d = 0; d < 4; d++) {
                 v4i f0, f1;  // columns 2d and 2d + 1: 8 rows each
+                auto turn = [&]() {
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    f0[r] = (int)__builtin_amdgcn_perm((uint32_t)w[2 * r + 1][d], (uint32_t)w[2 * r][d], 0x05040100u);
-                    f1[r] = (int)__builtin_amdgcn_perm((uint32_t)w[2 * r + 1][d], (uint32_t)w[2 * r][d], 0x07060302u);
-                }
-#pragma unroll
-                for (int k = 0; k < RC; k++)
-#pragma unroll
-                    for (int p = 2; p >= 0; p--) {  // the small parts first
-                        if constexpr (WIDE) {
-                            acc[2 * d][k] = mfma16(f0, pf[k][p], acc[2 * d][k]);
-                            acc[2 * d + 1][k] = mfma16(f1, pf[k][p], acc[2 * d + 1][k]);
-                        } else {
-                            acc[2 * d][k] = mfma16(pf[k][p], f0, acc[2 * d][k]);
-                            acc[2 * d + 1][k] = mfma16(pf[k][p], f1, acc[2 * d + 1][k]);
-                        }
+                    for (int r = 0; r < 4; r++) {
+                        f0[r] = (int)__builtin_amdgcn_perm((uint32_t)w[2 * r + 1][d], (uint32_t)w[2 * r][d], 0x05040100u);
+                        f1[r] = (int)__builtin_amdgcn_perm((uint32_t)w[2 * r + 1][d], (uint32_t)w[2 * r][d], 0x07060302u);
                     }
+                };
+                auto part = [&](int k, int p) {
+                    if constexpr (WIDE) {
+                        acc[2 * d][k] = mfma16(f0, pf[k][p], acc[2 * d][k]);
+                        acc[2 * d + 1][k] = mfma16(f1, pf[k][p], acc[2 * d + 1][k]);
+                    } else {
+                        acc[2 * d][k] = mfma16(pf[k][p], f0, acc[2 * d][k]);
+                        acc[2 * d + 1][k] = mfma16(pf[k][p], f1, acc[2 * d + 1][k]);
+                    }
+                };
+                turn();
+                if constexpr (apart) f0 = finite8(f0), f1 = finite8(f1);
+#pragma unroll
+                for (int k = 0; k < RC; k++) {
+                    part(k, 2), part(k, 1);  // the small parts first
+                    if constexpr (!apart) part(k, 0);
+                }
+                if constexpr (apart) {
+                    turn();
+#pragma unroll
+                    for (int k = 0; k < RC; k++) part(k, 0);
+                }
             }
         };
         // the next step's operands go out once this step's products have taken theirs
         const int first = (lo & ~31) + 32 * wave;
+        auto clear = [&]() {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+#pragma unroll
+                for (int k = 0; k < RC; k++) acc[i][k] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+        };
+        clear();
         if (first < hi) {
             parts(first);
             load(first);
         }
         for (int m0 = first; m0 < hi; m0 += 128) {
-            mul(m0);
+            mul(m0, std::false_type());
             if (m0 + 128 < hi) {
                 parts(m0 + 128);
                 load(m0 + 128);
+            }
+        }
+        float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // NaN after a value that is not finite
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int k = 0; k < RC; k++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) zero[r] = __builtin_fmaf(acc[i][k][r], 0.0f, zero[r]);
+        const bool odd = !((zero[0] + zero[1]) + (zero[2] + zero[3]) == 0.0f);
+        if (__builtin_expect(__ballot(odd) != 0, 0)) {
+            clear();
+            for (int m0 = first; m0 < hi; m0 += 128) {
+                parts(m0);
+                load(m0);
+                mul(m0, std::true_type());
             }
         }
         // waves 1..3 add to wave 0 in order, 8 * RC pieces of 64 x 16 bytes

@@ -93,14 +93,31 @@ __device__ __forceinline__ int adapter_rank(const LoraBatch &B, int a) {
 }
 
 // ---- fp32 as a sum of bf16 values -------------------------------------------
-// The bf16 MFMA multiplies an fp32 operand as 3 bf16 parts, each the nearest to
-// what the parts before it leave: together all its 24 bits.  Results that are
-// rounded to bf16 take 3 parts too: where the adapter term cancels against what
-// it is added to, the 2^-18 of it that 2 parts lose is many bf16 steps of the
-// result.  bf16 has fp32's exponents, so nothing overflows but values within
-// half a bf16 step of FLT_MAX; an infinite or NaN value is its own first part,
-// the others 0.
+// The bf16 MFMA multiplies an fp32 operand as 3 bf16 parts, each the leading 8
+// bits of what the parts before it leave: together all its 24 bits.  Results
+// that are rounded to bf16 take 3 parts too: where the adapter term cancels
+// against what it is added to, what 2 parts lose is many bf16 steps of the
+// result.  Cut off and not rounded, no part exceeds the value, so the largest
+// fp32 numbers do not become infinite.  An infinite or NaN value is its own
+// first part (a quiet NaN, as arithmetic gives, has its mark in the upper
+// half); the later parts are then some finite values, which change neither.
+//
+// The other factor's infinities and NaN may meet the first part only: the
+// later ones may be 0, and 0 * inf is not what the whole value gives.  Where
+// that factor is at hand as fragments, the later parts multiply finite8() of
+// it.  Where it lies in LDS it does so as ones8(), and a product that is taken
+// only if such a value was seen adds odd8() of it times the value's sign
+// (sign8): a branch in every product instead cost the INT8 GEMM 10% at rank 64.
+// Either way inf * value is infinite with the right sign and inf * 0 NaN; with
+// finite8() a value below bf16's range (2^-133) counts as 0 there.
 constexpr int kParts = 3;
+
+__device__ __forceinline__ float split_rest(float v) {  // v without its first part
+    return v - __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+}
+__device__ __forceinline__ float split_finite(float v) {
+    return __builtin_amdgcn_fmed3f(v, -3.402823466e38f, 3.402823466e38f);
+}
 
 __device__ __forceinline__ void split8(const float v[8], v4i (&out)[kParts]) {
     float r[8];
@@ -109,16 +126,66 @@ __device__ __forceinline__ void split8(const float v[8], v4i (&out)[kParts]) {
 #pragma unroll
     for (int p = 0; p < kParts; p++) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint32_t w = cvt_pk_bf16(r[2 * i], r[2 * i + 1]);
-            out[p][i] = (int)w;
-            if (p + 1 < kParts) {
-                const float lo = bf16_lo(w), hi = bf16_hi(w);
-                r[2 * i] = __builtin_isfinite(lo) ? r[2 * i] - lo : 0.0f;
-                r[2 * i + 1] = __builtin_isfinite(hi) ? r[2 * i + 1] - hi : 0.0f;
-            }
-        }
+        for (int i = 0; i < 4; i++)
+            out[p][i] = (int)__builtin_amdgcn_perm(__float_as_uint(r[2 * i + 1]), __float_as_uint(r[2 * i]), 0x07060302u);
+        if (p + 1 < kParts)
+#pragma unroll
+            for (int i = 0; i < 8; i++) r[i] = split_rest(p == 0 ? split_finite(r[i]) : r[i]);
     }
+}
+
+// Bits 15 and 31 of a word: its two bf16 values are infinite or NaN (all ones
+// in the exponent, which adding one carries out of).
+__device__ __forceinline__ uint32_t nonfinite2(int w) { return (((uint32_t)w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+// The same question for many words at once: magnitudes8() takes the largest
+// of each half's bits without the sign, which is 0x7F80 or more after such a
+// value (two operations a word).
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void magnitudes8(const v4i &v, u16x2 &top) {
+#pragma unroll
+    for (int d = 0; d < 4; d++) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, v[d] & 0x7FFF7FFF));
+}
+__device__ __forceinline__ bool nonfinite_in(u16x2 top) { return top[0] >= 0x7F80 || top[1] >= 0x7F80; }
+
+// All ones in the halves of a word that nonfinite2 found.
+__device__ __forceinline__ uint32_t halves(uint32_t found) { return (found >> 15) * 0xFFFFu; }
+
+// 8 bf16 values with 0 in place of infinities and NaN;
+__device__ __forceinline__ v4i finite8(v4i v) {
+#pragma unroll
+    for (int d = 0; d < 4; d++) v[d] &= (int)~halves(nonfinite2(v[d]));
+    return v;
+}
+
+// with 1 of their sign in their place;
+__device__ __forceinline__ v4i ones8(v4i v) {
+#pragma unroll
+    for (int d = 0; d < 4; d++) {
+        const uint32_t h = halves(nonfinite2(v[d]));
+        v[d] = (int)(((uint32_t)v[d] & (~h | 0x80008000u)) | (h & 0x3F803F80u));
+    }
+    return v;
+}
+
+// and only infinities and NaN, 0 in place of the others.
+__device__ __forceinline__ v4i odd8(v4i v) {
+#pragma unroll
+    for (int d = 0; d < 4; d++) v[d] &= (int)halves(nonfinite2(v[d]));
+    return v;
+}
+
+// The signs of 8 fp32 values as bf16 1, -1 and 0 (of a NaN: 1 or -1; the
+// products with ones8() are NaN by then).
+__device__ __forceinline__ v4i sign8(const float v[8]) {
+    v4i o;
+#pragma unroll
+    for (int d = 0; d < 4; d++) {
+        const uint32_t lo = v[2 * d] == 0.0f ? 0u : (__float_as_uint(v[2 * d]) >> 16 & 0x8000u) | 0x3F80u;
+        const uint32_t hi = v[2 * d + 1] == 0.0f ? 0u : (__float_as_uint(v[2 * d + 1]) >> 16 & 0x8000u) | 0x3F80u;
+        o[d] = (int)(lo | hi << 16);
+    }
+    return o;
 }
 
 // The first n of 8 bf16 values, zeros in place of the others.
@@ -184,8 +251,9 @@ __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_
                 for (int j = 0; j < 4; j++) {
                     v4i bf = *reinterpret_cast<const v4i *>(bl[j] + off + c);
                     if (c + 16 > rank) bf = keep8(bf, rank - c - 8 * lh);
+                    const v4i fin = finite8(bf);
 #pragma unroll
-                    for (int p = kParts - 1; p >= 0; p--) v[j] = mfma32(bf, tf[p], v[j]);
+                    for (int p = kParts - 1; p >= 0; p--) v[j] = mfma32(p > 0 ? fin : bf, tf[p], v[j]);
                 }
             }
         } else {
@@ -199,8 +267,9 @@ __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_
                     lora_t_frag(tr + c, sc, tf);
                     v4i bf = *reinterpret_cast<const v4i *>(bl[j] + off + c);
                     if (c + 16 > rank) bf = keep8(bf, rank - c - 8 * lh);
+                    const v4i fin = finite8(bf);
 #pragma unroll
-                    for (int p = kParts - 1; p >= 0; p--) d = mfma32(bf, tf[p], d);
+                    for (int p = kParts - 1; p >= 0; p--) d = mfma32(p > 0 ? fin : bf, tf[p], d);
                 }
 #pragma unroll
                 for (int e = 0; e < 16; e++) v[j][e] = mine == a ? v[j][e] + d[e] : v[j][e];
@@ -267,7 +336,10 @@ struct LoraWords {
 // are loaded as they are used.  4 (a rank of 64) in the fp32-accumulator
 // GEMMs.  The INT8 GEMM's registers hold no more than 1: with 4 its kernel
 // spills 34 and takes 302 us without any adapter where it takes 252 with 1.
-static_assert(kLoraBOff + 256 * (2 * kMaxLoraRank + 16) <= kLoraLds, "bands and b fit");
+// the last words of the area: for each wave, whether the b it copied holds an
+// infinity or NaN
+constexpr int kLoraOddOff = kLoraLds - 16;
+static_assert(kLoraBOff + 256 * (2 * kMaxLoraRank + 16) <= kLoraOddOff && kLoraOddOff % 16 == 0, "bands and b fit");
 
 template <int AHEAD>
 struct LoraRows {
@@ -276,11 +348,11 @@ struct LoraRows {
 
 // What a workgroup keeps over the slices of its tile: the tile's rows, the
 // first request that may have some, and the request whose b is in LDS with
-// its rows of the tile, rank and scale.
+// its rows of the tile, rank and scale, and whether that b is all finite.
 struct LoraTile {
     LoraWords words;
     int r0, r1, s0, staged;
-    int lo, hi, rank;
+    int lo, hi, rank, odd;
     float sc;
 
     // request s's rows of the tile; false if there are none or no adapter
@@ -291,7 +363,8 @@ struct LoraTile {
         h = end < r1 ? end : r1;
         return l < h && a >= 0;
     }
-    // its b into LDS; the barriers around the copy are the caller's
+    // its b into LDS; the barriers around the copy are the caller's, who then
+    // calls read_odd
     __device__ __forceinline__ void stage_b(const LoraEpi &L, int s, int l, int h, int a, int64_t n0, int64_t N,
                                             uint8_t *lds) {
         const LoraBatch &B = L.batch;
@@ -300,13 +373,31 @@ struct LoraTile {
         staged = s, lo = l, hi = h;
         rank = words.rank(B, a);
         sc = words.scale(B, a);
+        u16x2 top = {0, 0};
+        auto at = [&](int e, int &n, int &c) {  // piece e: its row and place in it, its values
+            n = e / per_row, c = e - n * per_row;
+            const int64_t g = n0 + n < N ? n0 + n : N - 1;
+            return keep8(*reinterpret_cast<const v4i *>(bw + g * B.R + 8 * c), rank - 8 * c);
+        };
+        int n, c;
 #pragma unroll 4
         for (int e = threadIdx.x; e < 256 * per_row; e += 256) {
-            const int n = e / per_row, c = e - n * per_row;
-            const int64_t g = n0 + n < N ? n0 + n : N - 1;
-            const v4i f = *reinterpret_cast<const v4i *>(bw + g * B.R + 8 * c);
-            *reinterpret_cast<v4i *>(lds + kLoraBOff + n * brow + 16 * c) = keep8(f, rank - 8 * c);
+            const v4i f = at(e, n, c);
+            *reinterpret_cast<v4i *>(lds + kLoraBOff + n * brow + 16 * c) = f;
+            magnitudes8(f, top);
         }
+        const uint64_t any = __ballot(nonfinite_in(top));
+        if ((threadIdx.x & 63) == 0) reinterpret_cast<int *>(lds + kLoraOddOff)[threadIdx.x >> 6] = any != 0;
+        if (__builtin_expect(any != 0, 0))
+#pragma unroll 1
+            for (int e = threadIdx.x; e < 256 * per_row; e += 256) {
+                const v4i f = at(e, n, c);
+                *reinterpret_cast<v4i *>(lds + kLoraBOff + n * brow + 16 * c) = ones8(f);
+            }
+    }
+    __device__ __forceinline__ void read_odd(const uint8_t *lds) {
+        const v4i w = *reinterpret_cast<const v4i *>(lds + kLoraOddOff);
+        odd = __builtin_amdgcn_readfirstlane(w[0] | w[1] | w[2] | w[3]);
     }
     // the lane's row of t in slice i of its wave
     __device__ __forceinline__ const float *row(const LoraEpi &L, int i) const {
@@ -336,7 +427,7 @@ __device__ __forceinline__ LoraTile lora_tile_begin(const LoraEpi &L, int64_t m0
     T.r1 = m0 + 256 < B.M ? (int)m0 + 256 : B.M;
     T.s0 = 0;
     T.staged = -1;
-    T.lo = T.hi = T.rank = 0;
+    T.lo = T.hi = T.rank = T.odd = 0;
     T.sc = 0.0f;
     T.load_t(L, 0, t);
     for (int c = 0; c <= B.S; c += 64) {  // the last request that starts at or before the tile
@@ -350,6 +441,7 @@ __device__ __forceinline__ LoraTile lora_tile_begin(const LoraEpi &L, int64_t m0
     int l, h, a;
     if (T.s0 < B.S && T.rows_of(B, T.s0, l, h, a)) T.stage_b(L, T.s0, l, h, a, n0, N, lds);
     __syncthreads();
+    if (T.staged >= 0) T.read_odd(lds);
     return T;
 }
 
@@ -376,6 +468,7 @@ __device__ __forceinline__ void lora_band_add(const LoraEpi &L, LoraTile &T, int
                 __syncthreads();  // every wave is done with the last request's b
                 T.stage_b(L, s, l, h, a, n0, N, lds);
                 __syncthreads();
+                T.read_odd(lds);
             }
         }
         const bool last = T.hi >= T.r1;
@@ -405,6 +498,23 @@ __device__ __forceinline__ void lora_band_add(const LoraEpi &L, LoraTile &T, int
                 const float *p = T.row(L, i);
                 for (int c = 16 * AHEAD; c < T.rank; c += 16)
                     piece(c, *reinterpret_cast<const v4f *>(p + c), *reinterpret_cast<const v4f *>(p + c + 4));
+            }
+            if (__builtin_expect(T.odd, 0)) {  // b's infinities and NaN, from memory
+                const float *p = T.row(L, i);
+                const uint16_t *bw = L.b + (int64_t)T.words.adapter(B, s) * N * B.R + 8 * lh;
+#pragma unroll 1
+                for (int c = 0; c < T.rank; c += 16) {
+                    const v4f a0 = *reinterpret_cast<const v4f *>(p + c), a1 = *reinterpret_cast<const v4f *>(p + c + 4);
+                    const float v[8] = {T.sc * a0[0], T.sc * a0[1], T.sc * a0[2], T.sc * a0[3],
+                                        T.sc * a1[0], T.sc * a1[1], T.sc * a1[2], T.sc * a1[3]};
+                    const v4i sf = sign8(v);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int64_t n = n0 + wn * 128 + 32 * j + lm;
+                        const v4i f = *reinterpret_cast<const v4i *>(bw + (n < N ? n : N - 1) * B.R + c);
+                        d[j] = mfma32(odd8(keep8(f, T.rank - c - 8 * lh)), sf, d[j]);
+                    }
+                }
             }
             const bool own = mine0 + lm >= T.lo && mine0 + lm < T.hi;
 #pragma unroll

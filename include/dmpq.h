@@ -434,7 +434,9 @@ dmpq_status dmpq_selftest_codec(hipStream_t stream, int codec, uint32_t lo, uint
  * Sums are fp32 in a fixed order (the same bits on every call).  t is fp32;
  * where it enters a product it is split into bf16 parts that keep all its
  * bits.  A value that is not finite stays within its own row (forward) or its
- * own adapter (gradients).
+ * own adapter (gradients), and products with it are as in fp32: an infinity
+ * times a number is infinite with its sign, times 0 NaN (a t or u below 2^-133
+ * may count as 0 there).
  * ========================================================================= */
 
 /* t [M x R] fp32 = x a^T, each row through its own adapter's a; zeros past the

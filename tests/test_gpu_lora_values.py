@@ -1,6 +1,8 @@
-"""GPU: the adapter operators at values where their bf16 parts could show.  Every
-form that has the product is run: lora_forward, the three GEMM epilogues (whole
-tiles and the split tail) and dx."""
+"""GPU: the adapter operators at values where their bf16 parts could show: the
+largest fp32 values, infinities and NaN in a factor, and a term that cancels
+against what it is added to.  Every form that has the product is run:
+lora_forward, the three GEMM epilogues (whole tiles and the split tail), dx, da
+and db."""
 import numpy as np
 import pytest
 import torch
@@ -13,6 +15,7 @@ pytestmark = pytest.mark.gpu
 
 HALF_BF16 = 2.0 ** -8
 HALF_F32 = 2.0 ** -24
+FLT_MAX = np.float32(3.4028234663852886e38)
 
 
 def parts(v):
@@ -159,6 +162,143 @@ def rounded(tol, want, f32):
     """The tolerance of the fp32 result and the rounding to the output's type."""
     with np.errstate(invalid="ignore"):
         return tol + np.abs(want) * 2 * HALF_F32 if f32 else tol * (1 + HALF_BF16) + (np.abs(want) + tol) * HALF_BF16
+
+
+# ---- the largest values -------------------------------------------------------
+
+
+@both
+def test_largest_values(form, f32):
+    """t = FLT_MAX is an fp32 number like any other: t * 2^-60 is finite."""
+    require_gpu()
+    say(f"largest values {form} {f32}")
+    t = np.zeros((40, 16), np.float32)
+    t[:, 3] = FLT_MAX
+    t[1::2, 3] = -FLT_MAX
+    b = np.zeros((1, 48, 16), np.float32)
+    b[:, :, 3] = 2.0 ** -60
+    q = Pool(t, b)
+    want, mag = q.term()
+    same(FORMS[form](q, 0, f32), want, rounded(mag * 4 * HALF_F32, want, f32))
+
+
+def gradients(t, dy, x, a, b, rank, start, ad):
+    """da and db of given arrays (u = dy b, scale 1)."""
+    n, R, K = a.shape
+    N, M = b.shape[1], len(dy)
+    da, db = torch.full((n, R, K), float("nan"), device="cuda"), torch.full((n, N, R), float("nan"), device="cuda")
+    ws = dm.new_lora_workspace(M, N, K, R, len(ad), n)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    dm.lora_backward(bf(dy).cuda(), bf(x).cuda(), torch.from_numpy(np.float32(t)).cuda(), bf(a).cuda(), bf(b).cuda(),
+                     i32(rank), torch.ones(n, device="cuda"), i32(start), i32(ad), None, None, da, db, ws)
+    torch.cuda.synchronize()
+    return da, db
+
+
+def test_largest_values_in_the_gradients():
+    require_gpu()
+    say("largest values da db")
+    M, R = 33, 16
+    u = np.zeros((M, R), np.float32)
+    u[7, 2], u[20, 5] = FLT_MAX, -FLT_MAX
+    dy, b = spread(u, R)
+    x = np.full((M, 32), 2.0 ** -60, np.float32)
+    da, _ = gradients(np.zeros((M, R)), dy, x, np.zeros((1, R, 32)), b.T[None], [R], [0, M], [0])
+    want = u.astype(np.float64).T @ x
+    same(da[0], want, np.abs(want) * 4 * HALF_F32)
+    dy2 = np.full((M, 48), 2.0 ** -60, np.float32)
+    _, db = gradients(u, dy2, x, np.zeros((1, R, 32)), np.zeros((1, 48, R)), [R], [0, M], [0])
+    want = dy2.astype(np.float64).T @ u
+    same(db[0], want, np.abs(want) * 4 * HALF_F32)
+
+
+# ---- infinities and NaN ---------------------------------------------------------
+
+
+def infinite_pool(seed, M=150, N=176, R=48):
+    """Three requests of three adapters; the middle one's b holds infinities of either
+    sign, both in one row, and a NaN; t has zeros; entries past a rank are infinite too."""
+    rng = np.random.default_rng(seed)
+    t = rng.standard_normal((M, R)).astype(np.float32)
+    t[::3, 4] = 0.0
+    b = bf(rng.standard_normal((3, N, R)) * 0.1).float().numpy()
+    rank = [R, 37, 21]
+    b[1, 5, 3], b[1, 9, 4], b[1, 33, 2] = np.inf, -np.inf, np.nan
+    b[1, 17, 0], b[1, 17, 1] = np.inf, -np.inf
+    b[1, 130, 36] = np.inf
+    b[1, 40, 37:], b[2, :, 21:] = np.inf, -np.inf
+    start = [0, 21, 101, M]
+    for i, r in enumerate(rank):  # what is past the rank is zero in t, as lora_shrink leaves it
+        t[start[i]:start[i + 1], r:] = 0.0
+    return Pool(t, b, rank, None, start, [0, 1, 2])
+
+
+@both
+def test_infinite_factors(form, f32):
+    """t b^T with infinities in b is infinite where one product is, of its sign, and NaN
+    where the definition is (0 * inf, inf - inf): nothing else changes."""
+    require_gpu()
+    say(f"infinite b {form} {f32}")
+    q = infinite_pool(3)
+    want, mag = q.term()
+    tol = np.where(np.isfinite(mag), mag, 0) * (q.R + 8) * 2 * HALF_F32
+    assert np.isinf(want).sum() > 200 and np.isnan(want).sum() > 50
+    same(FORMS[form](q, 0, f32), want, rounded(tol, want, f32))
+
+
+@both
+def test_infinite_rows(form, f32):
+    """The same of the other factor: infinities and NaN in t (the GEMMs take it as it is)."""
+    require_gpu()
+    if form in ("forward", "dx"):
+        pytest.skip("t is computed there, from finite factors")
+    say(f"infinite t {form} {f32}")
+    q = infinite_pool(4)
+    q.b = np.where(np.isfinite(q.b), q.b, 0.25).astype(np.float32)
+    q.b[:, 7, 6] = 0.0
+    q.t[30, 6], q.t[31, 6], q.t[120, 0] = np.inf, -np.inf, np.nan
+    q.t[32, 2], q.t[32, 3] = np.inf, -np.inf
+    want, mag = q.term()
+    tol = np.where(np.isfinite(mag), mag, 0) * (q.R + 8) * 2 * HALF_F32
+    same(FORMS[form](q, 0, f32), want, rounded(tol, want, f32))
+
+
+@pytest.mark.parametrize("M,R", [(150, 16), (150, 96), (8300, 48)])
+def test_infinite_factors_in_the_gradients(M, R):
+    """db with infinite dy and da with infinite x: summed over the rows, of each term's sign."""
+    require_gpu()
+    say(f"infinite dy and x {M} {R}")
+    rng = np.random.default_rng(M + R)
+    N, K, n = 64, 48, 2
+    t = rng.standard_normal((M, R)).astype(np.float32)
+    t[::5, 1] = 0.0
+    start, ad, rank = [0, 37, M], [1, 0], [R, R - 5]
+    t[:37, R - 5:] = 0.0
+    dy = bf(rng.standard_normal((M, N)) * 0.1).float().numpy()
+    dy[50, 3], dy[90, 7], dy[91, 7], dy[140, 20], dy[11, 30] = np.inf, -np.inf, np.inf, np.nan, -np.inf
+    x, a = np.zeros((M, K), np.float32), np.zeros((n, R, K), np.float32)
+    b = bf(rng.standard_normal((n, N, R)) * 0.1).float().numpy()
+    _, db = gradients(t, dy, x, a, b, rank, start, ad)
+
+    def check(got, left, right, rank_last):
+        """got[i] = left^T right over the rows of adapter i, up to its rank in the axis of ranks."""
+        for s in range(2):
+            i, rows = ad[s], slice(start[s], start[s + 1])
+            l, r = left[rows].astype(np.float64), right[rows].astype(np.float64)
+            with np.errstate(invalid="ignore"):
+                want = np.stack([(l * r[:, j:j + 1]).sum(0) for j in range(R)], -1)  # [columns, R]
+                mag = np.nan_to_num(np.stack([np.abs(l * r[:, j:j + 1]).sum(0) for j in range(R)], -1), posinf=0.0)
+            want[:, rank[i]:] = 0.0
+            tol = mag * (l.shape[0] + N + 16) * 2 * HALF_F32
+            same(got[i], want if rank_last else want.T, tol if rank_last else tol.T)
+
+    check(db, dy, t, True)
+    u, ones = spread(t, R)
+    if u.shape[1] % 16 == 0:  # dy carries t's parts, b adds them up: u = t exactly
+        x = bf(rng.standard_normal((M, K)) * 0.1).float().numpy()
+        x[60, 2], x[100, 9], x[103, 9], x[149, 30], x[12, 40] = np.inf, np.inf, -np.inf, np.nan, -np.inf
+        da, _ = gradients(np.zeros((M, R)), u, x, a, np.repeat(ones.T[None], n, 0), rank, start, ad)
+        check(da, x, t, False)
 
 
 # ---- a term that cancels ------------------------------------------------------------
