@@ -272,13 +272,15 @@ __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const
         if (base && m < rows && left > 0)
             bv[r] = left >= 4 ? Q::load(bp + m * ld + lane_off) : Q::load_some(bp + m * ld + lane_off, left);
     }
+    // an adapter of rank 0 adds nothing, whatever its scale (alpha / rank: infinite)
+    const int rank = st.adapter < 0 ? 0 : adapter_rank(B, st.adapter);
     v16f acc[4];
     float sc = 1.0f;
 #pragma unroll
     for (int p = 0; p < 4; p++)
 #pragma unroll
-        for (int e = 0; e < 16; e++) acc[p][e] = st.adapter < 0 ? -0.0f : 0.0f;  // base + -0 is base bit for bit
-    if (st.adapter >= 0) {
+        for (int e = 0; e < 16; e++) acc[p][e] = 0.0f;
+    if (rank > 0) {
         const int64_t bn = N * B.R;  // values of one adapter's b
         const uint16_t *bw = b + st.adapter * bn;
         v4i piece[RC];
@@ -296,7 +298,6 @@ __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const
 #pragma unroll
             for (int c = 0; c < RC; c++) tv[c][h] = *reinterpret_cast<const v4f *>(tr + (16 * c < B.R ? 16 * c : 0));
         }
-        const int rank = adapter_rank(B, st.adapter);
         if (B.scale) sc = B.scale[st.adapter];
         const int per_row = B.R / 8;  // 16-byte pieces of a row of b
         u16x2 top = {0, 0};
@@ -363,7 +364,8 @@ __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const
     for (int r = 0; r < 16; r++) {
         const int m = 8 * (r >> 2) + (r & 3);
         if (m >= rows || left <= 0) continue;
-        const Q o = bv[r].plus(sc, acc[0][r], acc[1][r], acc[2][r], acc[3][r]);
+        // (base alone is copied, not added to: all bits of a NaN or -0 stay)
+        const Q o = rank > 0 ? bv[r].plus(sc, acc[0][r], acc[1][r], acc[2][r], acc[3][r]) : bv[r];
         if (left >= 4)
             o.store(yp + m * ld + lane_off);
         else

@@ -447,7 +447,8 @@ dmpq_status dmpq_lora_shrink(hipStream_t stream, const uint16_t *x, const uint16
                              int64_t n_adapters, float *t);
 /* t as above, and y [M x N] = base + scale * t b^T (out_dtype F32 or BF16, of
  * base and y both).  base may be y (in place) or NULL (zeros); rows without
- * adapter are base bit for bit.  N >= 0 is any. */
+ * adapter, or whose adapter has rank 0 (whatever its scale), are base bit for
+ * bit.  N >= 0 is any. */
 dmpq_status dmpq_lora_forward(hipStream_t stream, const uint16_t *x, const void *base,
                               const uint16_t *a, const uint16_t *b, const int32_t *rank,
                               const float *scale, const int32_t *seg_start,

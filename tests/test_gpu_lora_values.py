@@ -1,6 +1,6 @@
 """GPU: the adapter operators at values where their bf16 parts could show: the
-largest fp32 values, infinities and NaN in a factor, and a term that cancels
-against what it is added to.  Every form that has the product is run:
+largest fp32 values, infinities and NaN in a factor, a term that cancels against
+what it is added to, and rank 0.  Every form that has the product is run:
 lora_forward, the three GEMM epilogues (whole tiles and the split tail), dx, da
 and db."""
 import numpy as np
@@ -323,3 +323,68 @@ def test_a_term_that_cancels(form, f32):
     q = Pool(t, b, [6])
     want = 1.0 + np.repeat(t.astype(np.float64).sum(1)[:, None], N, 1)
     same(FORMS[form](q, 1, f32), want, rounded(12 * HALF_F32, want, f32))
+
+
+# ---- rank 0 and no adapter ---------------------------------------------------------
+
+
+@pytest.mark.parametrize("f32", [False, True], ids=["bf16", "f32"])
+def test_rank_zero_adds_nothing(f32):
+    """An adapter of rank 0 (scale alpha / rank: infinite) leaves its rows as rows without
+    an adapter: base bit for bit, -0 and every NaN pattern among them."""
+    require_gpu()
+    say(f"rank 0 {f32}")
+    rng = np.random.default_rng(2)
+    M, N, R = 200, 136, 16
+    t = rng.standard_normal((M, R)).astype(np.float32)
+    t[:130] = 0.0
+    b = bf(rng.standard_normal((3, N, R))).float().numpy()
+    q = Pool(t, b, [0, 0, 16], [np.inf, 2.0, 1.0], [0, 60, 90, 130, M], [0, 1, -1, 2])
+    if f32:
+        base = torch.from_numpy(rng.integers(0, 1 << 32, (M, N), dtype=np.uint64).astype(np.uint32).view(np.float32)).cuda()
+    else:
+        base = torch.from_numpy(rng.integers(0, 1 << 16, (M, N)).astype(np.uint16).view(np.int16)).cuda().view(BF)
+    base[::7] = -0.0
+    bits = torch.int32 if f32 else torch.int16
+    y = forward(q, base, f32)
+    assert torch.equal(y[:130].view(bits), base[:130].view(bits))
+    inplace = base.clone()
+    x, a = spread(q.t, R)
+    dm.lora_forward(bf(x).cuda(), inplace, bf(np.repeat(a[None], 3, 0)).cuda(), bf(b).cuda(), *q.batch(),
+                    torch.empty(M, R, device="cuda"), inplace, dm.OUT_F32 if f32 else dm.OUT_BF16)
+    torch.cuda.synchronize()
+    assert torch.equal(inplace.view(bits), y.view(bits))
+
+
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("route", list(GEMMS))
+def test_rank_zero_adds_nothing_to_the_gemms(route, split):
+    require_gpu()
+    say(f"rank 0 {route} {split}")
+    rng = np.random.default_rng(2)
+    M, N = 200, 136
+    q = Pool(np.zeros((M, 16)), rng.standard_normal((2, N, 16)), [0, 0], [np.inf, 3.0], [0, 90, M], [0, 1])
+    K = {"bf16": 2048, "int8": 4096, "nvfp4": 2048}[route] if split else 256
+    act, wt = constant_operand(route, M, K, 1), constant_operand(route, N, K, 1)
+    ws = dm.new_workspace(dm.OP_GEMM, "cuda", M, N) if split else None
+    y, z = torch.empty(M, N, dtype=BF, device="cuda"), torch.empty(M, N, dtype=BF, device="cuda")
+    GEMMS[route][0](*act, *wt, torch.from_numpy(q.t).cuda(), bf(q.b).cuda(), *q.batch(), y, 0, ws)
+    GEMMS[route][1](*act, *wt, z, 0, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(y.view(torch.int16), z.view(torch.int16))
+
+
+def test_rank_zero_has_no_gradient():
+    require_gpu()
+    say("rank 0 backward")
+    rng = np.random.default_rng(5)
+    M, N, K, R = 100, 48, 80, 16
+    dy, x = bf(rng.standard_normal((M, N))).cuda(), bf(rng.standard_normal((M, K))).cuda()
+    a, b = bf(rng.standard_normal((2, R, K))).cuda(), bf(rng.standard_normal((2, N, R))).cuda()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    base = torch.from_numpy(rng.integers(0, 1 << 16, (M, K)).astype(np.uint16).view(np.int16)).cuda().view(BF)
+    dx, da, db = torch.empty_like(base), torch.full((2, R, K), 7.0, device="cuda"), torch.full((2, N, R), 7.0, device="cuda")
+    dm.lora_backward(dy, x, torch.zeros(M, R, device="cuda"), a, b, i32([0, 0]), torch.tensor([np.inf, 1.0], device="cuda").float(),
+                     i32([0, 40, M]), i32([0, 1]), base, dx, da, db, dm.new_lora_workspace(M, N, K, R, 2, 2))
+    torch.cuda.synchronize()
+    assert torch.equal(dx.view(torch.int16), base.view(torch.int16)) and not da.any() and not db.any()
