@@ -405,13 +405,7 @@ __device__ __forceinline__ void split_fixup_epilogue(const uint32_t *part, Scale
     const bool vec = ((N * ES) & 15) == 0;
     sc.row(m0 + wm * 128 + i * 32 + lm);
     v16f add[4];
-    if constexpr (LORA) {
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-#pragma unroll
-            for (int r = 0; r < 16; r++) add[j][r] = 0.0f;
-        lora_slice(lora, m0 + wm * 128 + i * 32 + lm, n0 + wn * 128, N, lane, add);
-    }
+    if constexpr (LORA) lora_slice(lora, m0 + wm * 128 + i * 32 + lm, n0 + wn * 128, N, lane, add);
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         uint4 v[S][4];

@@ -207,18 +207,22 @@ __device__ __forceinline__ v4f mfma16(const v4i &a, const v4i &b, const v4f &c) 
 }
 
 // ---- the adapter term of a GEMM's epilogue -----------------------------------
+// y = projection + scale * (t b^T) by request: the scale multiplies the sum of
+// the products, as in the expand kernel, so that the two agree for every scale.
+//
 // Of one 32-row slice, run by one wave on its own (the fixup of split tiles):
-// v += scale * t b^T for 32 rows x 128 columns in the GEMMs' accumulator
-// layout: lane l holds row l % 32 (`row`; past M: nothing is added) and, in
-// v[j][4g + e], column n0 + 32 j + 8 g + 4 (l / 32) + e.  b's rows are the
-// MFMA's first operand, scale * t in bf16 parts (split8) the second.  Where
-// all rows share an adapter the products accumulate straight onto v.  Rows of
-// several adapters take one product per adapter over all 32 rows, added where
-// it belongs and never multiplied by zero elsewhere: one adapter's infinity
-// must not reach another request's rows.
-__device__ __forceinline__ void lora_t_frag(const float *tr, float sc, v4i (&tf)[kParts]) {
+// v = scale * (t b^T) for 32 rows x 128 columns in the GEMMs' accumulator
+// layout: lane l holds row l % 32 (`row`; past M: unspecified) and, in
+// v[j][4g + e], column n0 + 32 j + 8 g + 4 (l / 32) + e.  Rows without adapter or
+// of rank 0 get -0, which adds nothing to any number.  b's rows are the MFMA's
+// first operand, t in bf16 parts (split8) the second.  Where all rows share an
+// adapter the products accumulate straight onto v.  Rows of several adapters
+// take one product per adapter over all 32 rows, kept where it belongs and never
+// multiplied by zero elsewhere: one adapter's infinity must not reach another
+// request's rows.
+__device__ __forceinline__ void lora_t_frag(const float *tr, v4i (&tf)[kParts]) {
     const v4f a0 = *reinterpret_cast<const v4f *>(tr), a1 = *reinterpret_cast<const v4f *>(tr + 4);
-    const float v[8] = {sc * a0[0], sc * a0[1], sc * a0[2], sc * a0[3], sc * a1[0], sc * a1[1], sc * a1[2], sc * a1[3]};
+    const float v[8] = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
     split8(v, tf);
 }
 
@@ -234,6 +238,10 @@ __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_
         const int64_t n = n0 + 32 * j + lm;
         bl[j] = L.b + (n < N ? n : N - 1) * B.R + 8 * lh;
     }
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) v[j][e] = -0.0f;
     uint64_t todo = __ballot(mine >= 0);
     const uint64_t in_m = __ballot(row < B.M);
     while (todo) {
@@ -241,12 +249,13 @@ __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_
         const uint64_t own = __ballot(mine == a);
         todo &= ~own;
         const int rank = adapter_rank(B, a);
+        if (rank == 0) continue;
         const float sc = B.scale[a];
         const int64_t off = (int64_t)a * N * B.R;
         if (own == in_m) {
             for (int c = 0; c < rank; c += 16) {
                 v4i tf[kParts];
-                lora_t_frag(tr + c, sc, tf);
+                lora_t_frag(tr + c, tf);
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     v4i bf = *reinterpret_cast<const v4i *>(bl[j] + off + c);
@@ -256,6 +265,10 @@ __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_
                     for (int p = kParts - 1; p >= 0; p--) v[j] = mfma32(p > 0 ? fin : bf, tf[p], v[j]);
                 }
             }
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int e = 0; e < 16; e++) v[j][e] *= sc;
         } else {
 #pragma unroll
             for (int j = 0; j < 4; j++) {
@@ -264,7 +277,7 @@ __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_
                 for (int e = 0; e < 16; e++) d[e] = 0.0f;
                 for (int c = 0; c < rank; c += 16) {
                     v4i tf[kParts];
-                    lora_t_frag(tr + c, sc, tf);
+                    lora_t_frag(tr + c, tf);
                     v4i bf = *reinterpret_cast<const v4i *>(bl[j] + off + c);
                     if (c + 16 > rank) bf = keep8(bf, rank - c - 8 * lh);
                     const v4i fin = finite8(bf);
@@ -272,7 +285,7 @@ __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_
                     for (int p = kParts - 1; p >= 0; p--) d = mfma32(p > 0 ? fin : bf, tf[p], d);
                 }
 #pragma unroll
-                for (int e = 0; e < 16; e++) v[j][e] = mine == a ? v[j][e] + d[e] : v[j][e];
+                for (int e = 0; e < 16; e++) v[j][e] = mine == a ? sc * d[e] : v[j][e];
             }
         }
     }
@@ -479,8 +492,7 @@ __device__ __forceinline__ void lora_band_add(const LoraEpi &L, LoraTile &T, int
 #pragma unroll
                 for (int e = 0; e < 16; e++) d[j][e] = 0.0f;
             auto piece = [&](int c, const v4f &a0, const v4f &a1) {
-                const float v[8] = {T.sc * a0[0], T.sc * a0[1], T.sc * a0[2], T.sc * a0[3],
-                                    T.sc * a1[0], T.sc * a1[1], T.sc * a1[2], T.sc * a1[3]};
+                const float v[8] = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
                 v4i tf[kParts], bf[4];
                 split8(v, tf);
 #pragma unroll
@@ -505,8 +517,7 @@ __device__ __forceinline__ void lora_band_add(const LoraEpi &L, LoraTile &T, int
 #pragma unroll 1
                 for (int c = 0; c < T.rank; c += 16) {
                     const v4f a0 = *reinterpret_cast<const v4f *>(p + c), a1 = *reinterpret_cast<const v4f *>(p + c + 4);
-                    const float v[8] = {T.sc * a0[0], T.sc * a0[1], T.sc * a0[2], T.sc * a0[3],
-                                        T.sc * a1[0], T.sc * a1[1], T.sc * a1[2], T.sc * a1[3]};
+                    const float v[8] = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
                     const v4i sf = sign8(v);
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
@@ -524,7 +535,8 @@ __device__ __forceinline__ void lora_band_add(const LoraEpi &L, LoraTile &T, int
                     float4 *p = reinterpret_cast<float4 *>(band + lm * kLoraBandStride + (32 * j + 8 * g + 4 * lh) * 4);
                     float4 o = *p;
                     if (own) {
-                        o.x += d[j][4 * g], o.y += d[j][4 * g + 1], o.z += d[j][4 * g + 2], o.w += d[j][4 * g + 3];
+                        o.x = __builtin_fmaf(T.sc, d[j][4 * g], o.x), o.y = __builtin_fmaf(T.sc, d[j][4 * g + 1], o.y);
+                        o.z = __builtin_fmaf(T.sc, d[j][4 * g + 2], o.z), o.w = __builtin_fmaf(T.sc, d[j][4 * g + 3], o.w);
                         *p = o;
                     }
                 }

@@ -1,8 +1,8 @@
 """GPU: the adapter operators at values where their bf16 parts could show: the
 largest fp32 values, infinities and NaN in a factor, a term that cancels against
-what it is added to, and rank 0.  Every form that has the product is run:
-lora_forward, the three GEMM epilogues (whole tiles and the split tail), dx, da
-and db."""
+what it is added to, rank 0 and large scales.  Every form that has the product
+is run: lora_forward, the three GEMM epilogues (whole tiles and the split tail), dx,
+da and db."""
 import numpy as np
 import pytest
 import torch
@@ -388,3 +388,25 @@ def test_rank_zero_has_no_gradient():
                      i32([0, 40, M]), i32([0, 1]), base, dx, da, db, dm.new_lora_workspace(M, N, K, R, 2, 2))
     torch.cuda.synchronize()
     assert torch.equal(dx.view(torch.int16), base.view(torch.int16)) and not da.any() and not db.any()
+
+
+@both
+@pytest.mark.parametrize("scale", [np.inf, 2.0 ** 120])
+def test_the_scale_multiplies_the_sum(form, f32, scale):
+    """y = base + scale * (t b^T): a scale that would overflow t alone, or is infinite, meets
+    the sum of the products (terms of both signs), not each of them."""
+    require_gpu()
+    if form == "dx":
+        pytest.skip("u = scale * dy b carries the scale there")
+    say(f"scale {scale} {form} {f32}")
+    rng = np.random.default_rng(6)
+    M, N, R = 90, 80, 16
+    t = (rng.uniform(0.5, 1.0, (M, R)) * rng.choice([-1, 1], (M, R)) * 2.0 ** 20).astype(np.float32)
+    b = bf(rng.uniform(0.5, 1.0, (2, N, R)) * rng.choice([-1, 1], (2, N, R)) * 2.0 ** -30).float().numpy()
+    q = Pool(t, b, None, [scale, 1.0], [0, 50, M], [0, 1])
+    want, mag = q.term()
+    # a sum within its own error of zero may have either sign: none is here
+    s, m = Pool(t, b, None, None, q.start, q.ad).term()
+    assert np.all(np.abs(s) > m * (R + 8) * 2 * HALF_F32)
+    tol = np.where(np.isfinite(mag), mag, 0) * (R + 8) * 2 * HALF_F32
+    same(FORMS[form](q, 0, f32), want, rounded(tol, want, f32))
