@@ -208,12 +208,13 @@ __device__ __forceinline__ void adamw_block(const AdamwTensor &t, const AdamwHyp
 
 // One workgroup to a chunk of 1024 values, a block to each wave: a wave's
 // loads all go out at once and nothing waits for its stores.  The chunks go
-// from the last to the first: the norm read the gradients' end last, so part
+// from `last` down to the first: the norm read the gradients' end last, so part
 // of it is still in the Infinity Cache (82.6 M fp32 parameters with their norm:
 // 520 us, 539 from the first on).
 template <int PT, int GT, int BITS>
-__global__ __launch_bounds__(256) void adamw_kernel(AdamwTable T, AdamwHyper h, const double *__restrict__ norm) {
-    const unsigned chunk = gridDim.x - 1 - blockIdx.x;
+__global__ __launch_bounds__(256) void adamw_kernel(AdamwTable T, AdamwHyper h, const double *__restrict__ norm,
+                                                    unsigned last) {
+    const unsigned chunk = last - blockIdx.x;
     const AdamwTensor t = T.tensors[T.chunk_tensor[chunk]];
     float clip = 1.0f;
     if (norm) {
@@ -288,11 +289,14 @@ __global__ __launch_bounds__(256) void grad_norm_kernel(const double *__restrict
 
 template <int PT, int GT>
 void step(hipStream_t s, const AdamwTable &t, const AdamwHyper &h, const double *norm) {
-    const dim3 grid((unsigned)t.chunks), block(256);
-    if (t.state_bits == 8)
-        hipLaunchKernelGGL((adamw_kernel<PT, GT, 8>), grid, block, 0, s, t, h, norm);
-    else
-        hipLaunchKernelGGL((adamw_kernel<PT, GT, 32>), grid, block, 0, s, t, h, norm);
+    for (int64_t end = t.chunks; end > 0; end -= kMaxGroups) {  // once, below 8.6e9 values
+        const dim3 grid((unsigned)(end < kMaxGroups ? end : kMaxGroups)), block(256);
+        const unsigned last = (unsigned)(end - 1);
+        if (t.state_bits == 8)
+            hipLaunchKernelGGL((adamw_kernel<PT, GT, 8>), grid, block, 0, s, t, h, norm, last);
+        else
+            hipLaunchKernelGGL((adamw_kernel<PT, GT, 32>), grid, block, 0, s, t, h, norm, last);
+    }
 }
 
 }  // namespace

@@ -152,6 +152,10 @@ hipError_t launch_lora_backward(hipStream_t s, const uint16_t *dy, const uint16_
                                 const uint16_t *a, const uint16_t *b, const LoraBatch &B, int64_t N, int64_t K,
                                 const uint16_t *dx_base, uint16_t *dx, float *da, float *db, void *ws);
 
+// Workgroups of 256 threads in one launch: a grid counts its threads in 32 bits,
+// so calls that need more (2^31 threads) take several launches.
+constexpr int64_t kMaxGroups = int64_t(1) << 23;
+
 // ---- AdamW over many tensors -------------------------------------------------
 // A device table: the tensors, then the tensor of each chunk of kAdamwChunk
 // values (chunks are numbered tensor by tensor).
