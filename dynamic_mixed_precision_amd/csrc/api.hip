@@ -698,6 +698,7 @@ dmpq_status dmpq_lora_backward(hipStream_t stream, const uint16_t *dy, const uin
     if (ws_bytes < need)
         return fail(DMPQ_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", __func__, ws_bytes, need);
     if (n_adapters > 65535) return fail(DMPQ_ERR_UNSUPPORTED, "%s: more than 65535 adapters", __func__);
+    if (n_adapters * (N + K) > INT32_MAX) return fail(DMPQ_ERR_UNSUPPORTED, "%s: n_adapters * (N + K) exceeds 2^31", __func__);
     return hip_status(launch_lora_backward(stream, dy, x, t, a, b, B, N, K, dx_base, dx, da, db, ws), __func__);
 }
 

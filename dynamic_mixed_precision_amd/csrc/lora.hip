@@ -49,14 +49,15 @@ __device__ __forceinline__ v4i ld16(const void *p) { return *reinterpret_cast<co
 template <int RT, int RC, int WAVES, bool UP>
 __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(const uint16_t *__restrict__ x,
                                                                  const uint16_t *__restrict__ a, LoraBatch B,
-                                                                 int64_t K, int tile, float *__restrict__ t,
+                                                                 int64_t K, int tile, unsigned first,
+                                                                 float *__restrict__ t,
                                                                  uint16_t *__restrict__ packed) {
     constexpr int TM = 16 * RT, TJ = 16 * RC, ROWS = TM + TJ, LOADS = ROWS / 8;
     constexpr int STRIDE = TJ + 4;  // of the sums
     constexpr int STAGE = ROWS * 128, SUMS = TM * STRIDE * 4;
     __shared__ __attribute__((aligned(16))) uint8_t lds[WAVES * (STAGE > SUMS ? STAGE : SUMS)];
     SegTile st;
-    if (!seg_tile(B, blockIdx.x, tile, st)) return;
+    if (!seg_tile(B, (int)(first + blockIdx.x), tile, st)) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j0 = blockIdx.y * TJ;
     const int rank = st.adapter < 0 ? 0 : adapter_rank(B, st.adapter);
@@ -240,7 +241,8 @@ template <int ES, int RC>
 __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const float *__restrict__ t,
                                                                            const void *base,
                                                                            const uint16_t *__restrict__ b, LoraBatch B,
-                                                                           int64_t N, unsigned cols, void *y) {
+                                                                           int64_t N, unsigned cols, unsigned first,
+                                                                           void *y) {
     // b's row 4 i + p of the block lies at LDS row 32 p + i; 16 bytes of
     // padding spread the lanes' 16-byte reads over the banks
     constexpr int ROW = 32 * RC + 16;
@@ -249,9 +251,9 @@ __global__ __launch_bounds__(64 * kExpandWaves, 2) void lora_expand_kernel(const
     __shared__ __attribute__((aligned(16))) uint8_t tlds[kExpandWaves][32 * TROW];
     __shared__ int odd_b[kExpandWaves];  // whether the b that a wave copied holds an infinity or NaN
     typedef Quad<ES> Q;
-    const unsigned tile = blockIdx.x / cols, cb = blockIdx.x - tile * cols;
+    const unsigned down = blockIdx.x / cols, cb = blockIdx.x - down * cols;
     SegTile st;
-    if (!seg_tile(B, (int)tile, kExpandRows, st)) return;
+    if (!seg_tile(B, (int)(first + down), kExpandRows, st)) return;
     if (st.adapter < 0 && base == y) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 31, lh = lane >> 5;
@@ -386,10 +388,10 @@ struct PrepPlan {
 
 __global__ __launch_bounds__(256) void lora_prep_kernel(const uint16_t *__restrict__ a, const uint16_t *__restrict__ b,
                                                         const float *__restrict__ t, LoraBatch B, int64_t N, int64_t K,
-                                                        PrepPlan pl, uint16_t *__restrict__ at,
+                                                        PrepPlan pl, unsigned first, uint16_t *__restrict__ at,
                                                         uint16_t *__restrict__ bt, uint16_t *__restrict__ tp) {
     __shared__ __attribute__((aligned(16))) uint16_t tile[64 * (kMaxLoraRank + 2)];
-    int blk = blockIdx.x;
+    int blk = (int)(first + blockIdx.x);
     const int tid = threadIdx.x, R = B.R;
     const int pieces = R / 8;
     // 8 values of 8 different rows of the tile, packed as one piece
@@ -674,11 +676,11 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(const uint16_t *__res
 // rank and for adapters without rows.  4 values per thread.
 __global__ __launch_bounds__(256) void lora_grad_sum_kernel(const float *__restrict__ pb,
                                                             const float *__restrict__ pa, LoraBatch B, int64_t N,
-                                                            int64_t K, int chunk, float *__restrict__ da,
-                                                            float *__restrict__ db) {
+                                                            int64_t K, int chunk, unsigned first,
+                                                            float *__restrict__ da, float *__restrict__ db) {
     const int i = blockIdx.y, rank = adapter_rank(B, i);
     const int64_t nb = N * B.R, na = K * B.R;
-    int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    int64_t e = (((int64_t)first + blockIdx.x) * 256 + threadIdx.x) * 4;
     const bool is_b = e < nb;
     if (!is_b) e -= nb;
     if (!is_b && e >= na) return;
@@ -749,6 +751,18 @@ unsigned seg_tiles(const LoraBatch &B, int TM) {
     return (unsigned)(n < B.M ? n : B.M);
 }
 
+// launch(first, n) for `count` units in runs of at most `most` (units of one
+// workgroup of 256 threads: what a grid holds).
+template <class Launch>
+hipError_t in_launches(int64_t count, Launch launch, int64_t most = kMaxGroups) {
+    for (int64_t first = 0; first < count; first += most) {
+        launch((unsigned)first, (unsigned)(count - first < most ? count - first : most));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // From 8192 rows on, one tile of 48 to 80 rows to each compute unit, or to
 // each of a multiple of them (M / 256 rows: with 64 each, 17776 rows made 278
 // tiles, and the 22 units with two set the time: 75 us where 16384 rows took
@@ -765,50 +779,55 @@ hipError_t shrink(hipStream_t st, const uint16_t *x, const uint16_t *a, const Lo
         const int pieces = (B.M + 15) / 16 * (B.R / 16);
         if (pieces < 256)
             hipLaunchKernelGGL((lora_shrink_kernel<1, 1, 16, UP>), dim3(seg_tiles(B, 16), B.R / 16), dim3(1024), 0, st,
-                               x, a, B, K, 16, t, packed);
+                               x, a, B, K, 16, 0u, t, packed);
         else if (pieces < 1024)
             hipLaunchKernelGGL((lora_shrink_kernel<1, 2, 8, UP>), dim3(seg_tiles(B, 16), (B.R + 31) / 32), dim3(512), 0,
-                               st, x, a, B, K, 16, t, packed);
+                               st, x, a, B, K, 16, 0u, t, packed);
         else
             hipLaunchKernelGGL((lora_shrink_kernel<2, 4, 8, UP>), dim3(seg_tiles(B, 32), (B.R + 63) / 64), dim3(512), 0,
-                               st, x, a, B, K, 32, t, packed);
+                               st, x, a, B, K, 32, 0u, t, packed);
         return hipGetLastError();
     }
     const int64_t rounds = ((int64_t)B.M + 256 * 80 - 1) / (256 * 80);
     const int64_t ragged = B.S < 64 ? B.S : 64;  // a request may end in a short tile
     int64_t tile = (B.M + 256 * rounds - ragged - 1) / (256 * rounds - ragged);
     if (tile > 80) tile = 80;
-    const dim3 grid(seg_tiles(B, (int)tile), (B.R + 63) / 64);
-#define DMPQ_SHRINK(RC_) \
-    hipLaunchKernelGGL((lora_shrink_kernel<5, RC_, 4, UP>), grid, dim3(256), 0, st, x, a, B, K, (int)tile, t, packed)
-    if (B.R <= 16)
-        DMPQ_SHRINK(1);
-    else if (B.R <= 32)
-        DMPQ_SHRINK(2);
-    else
-        DMPQ_SHRINK(4);
+    return in_launches(seg_tiles(B, (int)tile), [&](unsigned first, unsigned n) {
+        const dim3 grid(n, (B.R + 63) / 64);
+#define DMPQ_SHRINK(RC_)                                                                                         \
+    hipLaunchKernelGGL((lora_shrink_kernel<5, RC_, 4, UP>), grid, dim3(256), 0, st, x, a, B, K, (int)tile, first, t, \
+                       packed)
+        if (B.R <= 16)
+            DMPQ_SHRINK(1);
+        else if (B.R <= 32)
+            DMPQ_SHRINK(2);
+        else
+            DMPQ_SHRINK(4);
 #undef DMPQ_SHRINK
-    return hipGetLastError();
+    });
 }
 
 template <int ES>
 hipError_t expand(hipStream_t st, const float *t, const void *base, const uint16_t *b, const LoraBatch &B, int64_t N,
                   void *y) {
-    const int64_t cols = (N + kExpandCols - 1) / kExpandCols, grid = seg_tiles(B, kExpandRows) * cols;
-    if (grid > INT32_MAX) return hipErrorInvalidValue;
-#define DMPQ_EXPAND(RC_) \
-    hipLaunchKernelGGL((lora_expand_kernel<ES, RC_>), dim3((unsigned)grid), dim3(64 * kExpandWaves), 0, st, t, base, b, \
-                       B, N, (unsigned)cols, y)
-    if (B.R <= 16)
-        DMPQ_EXPAND(1);
-    else if (B.R <= 32)
-        DMPQ_EXPAND(2);
-    else if (B.R <= 64)
-        DMPQ_EXPAND(4);
-    else
-        DMPQ_EXPAND(8);
+    const unsigned cols = (unsigned)((N + kExpandCols - 1) / kExpandCols);  // <= 2^19
+    return in_launches(
+        seg_tiles(B, kExpandRows),
+        [&](unsigned first, unsigned n) {
+#define DMPQ_EXPAND(RC_)                                                                                           \
+    hipLaunchKernelGGL((lora_expand_kernel<ES, RC_>), dim3(n * cols), dim3(64 * kExpandWaves), 0, st, t, base, b, B, N, \
+                       cols, first, y)
+            if (B.R <= 16)
+                DMPQ_EXPAND(1);
+            else if (B.R <= 32)
+                DMPQ_EXPAND(2);
+            else if (B.R <= 64)
+                DMPQ_EXPAND(4);
+            else
+                DMPQ_EXPAND(8);
 #undef DMPQ_EXPAND
-    return hipGetLastError();
+        },
+        kMaxGroups / cols);
 }
 
 }  // namespace
@@ -840,9 +859,9 @@ hipError_t launch_lora_backward(hipStream_t s, const uint16_t *dy, const uint16_
     if (B.M > 0) {
         PrepPlan pp{(int)((N + 63) / 64), (int)((K + 63) / 64)};
         const int64_t pack = ((int64_t)(B.M + 7) / 8 * B.R + 255) / 256;
-        hipLaunchKernelGGL(lora_prep_kernel, dim3((unsigned)((int64_t)(pp.nb + pp.na) * B.nA + pack)), dim3(256), 0, s, a,
-                           b, t, B, N, K, pp, at, bt, tp);
-        hipError_t e = hipGetLastError();
+        hipError_t e = in_launches((int64_t)(pp.nb + pp.na) * B.nA + pack, [&](unsigned first, unsigned n) {
+            hipLaunchKernelGGL(lora_prep_kernel, dim3(n), dim3(256), 0, s, a, b, t, B, N, K, pp, first, at, bt, tp);
+        });
         if (e == hipSuccess) e = shrink<true>(s, dy, bt, B, N, u, up);
         if (e != hipSuccess) return e;
         GradPlan gp{L.chunk, (int)((N + 127) / 128), (int)((K + 127) / 128)};
@@ -876,9 +895,10 @@ hipError_t launch_lora_backward(hipStream_t s, const uint16_t *dy, const uint16_
     }
     if (B.nA == 0) return hipSuccess;
     const int64_t vals = (N + K) * B.R;
-    hipLaunchKernelGGL(lora_grad_sum_kernel, dim3((unsigned)((vals / 4 + 255) / 256), (unsigned)B.nA), dim3(256), 0, s, pb,
-                       pa, B, N, K, L.chunk, da, db);
-    return hipGetLastError();
+    return in_launches((vals / 4 + 255) / 256, [&](unsigned first, unsigned n) {
+        hipLaunchKernelGGL(lora_grad_sum_kernel, dim3(n, (unsigned)B.nA), dim3(256), 0, s, pb, pa, B, N, K, L.chunk, first,
+                           da, db);
+    });
 }
 
 }  // namespace dmpq

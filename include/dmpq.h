@@ -484,7 +484,8 @@ dmpq_status dmpq_qgemm_nvfp4_lora(hipStream_t stream, const uint8_t *ca, const u
  *   da = sum of u^T x          [n x R x K] fp32, over all rows of each adapter
  *   db = sum of scale * dy^T t [n x N x R] fp32
  * da and db are written whole: zeros past a rank and for adapters without
- * rows.  N must be a multiple of 16 (it is summed over).  ws:
+ * rows.  N must be a multiple of 16 (it is summed over).  At most 65535
+ * adapters, and n_adapters * (N + K) at most 2^31.  ws:
  * dmpq_lora_backward_bytes() bytes. */
 size_t dmpq_lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t S,
                                 int64_t n_adapters);
