@@ -669,7 +669,8 @@ size_t dmpq_lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int6
     if (M < 0 || N < 0 || K < 0 || R < 0 || S < 0 || n_adapters < 0 || M > most || N > kMaxLoraWidth ||
         K > kMaxLoraWidth || R > kMaxLoraRank || S > most / 2 || n_adapters > most)
         return 0;
-    return lora_backward_bytes(M, N, K, R, S, n_adapters);
+    const size_t bytes = lora_backward_bytes(M, N, K, R, S, n_adapters);
+    return bytes == SIZE_MAX ? 0 : bytes;
 }
 
 dmpq_status dmpq_lora_backward(hipStream_t stream, const uint16_t *dy, const uint16_t *x,
@@ -692,7 +693,8 @@ dmpq_status dmpq_lora_backward(hipStream_t stream, const uint16_t *dy, const uin
     REQUIRE_PTR_N(dx, 0);
     REQUIRE_PTR_N(da, n_adapters);
     REQUIRE_PTR_N(db, n_adapters);
-    const size_t need = dmpq_lora_backward_bytes(M, N, K, R, S, n_adapters);
+    const size_t need = lora_backward_bytes(M, N, K, R, S, n_adapters);
+    if (need == SIZE_MAX) return fail(DMPQ_ERR_UNSUPPORTED, "%s: the workspace passes 64 bits", __func__);
     if (need > 0 && !ws) return fail(DMPQ_ERR_WORKSPACE, "%s: workspace is NULL", __func__);
     if (ws && !aligned16(ws)) return fail(DMPQ_ERR_MISALIGNED, "%s: workspace is not 16-byte aligned", __func__);
     if (ws_bytes < need)

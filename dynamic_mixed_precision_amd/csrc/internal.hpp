@@ -147,6 +147,7 @@ hipError_t launch_lora_shrink(hipStream_t s, const uint16_t *x, const uint16_t *
 // y = base + scale * t b^T by request; base NULL reads as 0; base may be y
 hipError_t launch_lora_expand(hipStream_t s, const float *t, const void *base, const uint16_t *b,
                               const LoraBatch &B, int64_t N, int out_dtype, void *y);
+// the workspace of launch_lora_backward; SIZE_MAX: more than 4e18 bytes
 size_t lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t S, int64_t nA);
 hipError_t launch_lora_backward(hipStream_t s, const uint16_t *dy, const uint16_t *x, const float *t,
                                 const uint16_t *a, const uint16_t *b, const LoraBatch &B, int64_t N, int64_t K,

@@ -844,6 +844,10 @@ hipError_t launch_lora_expand(hipStream_t s, const float *t, const void *base, c
 }
 
 size_t lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t S, int64_t nA) {
+    // backward_layout's sizes without their rounding, in fp64: they can pass 64 bits
+    const double slots = (double)M / kGradRows + 1 + (double)S;
+    const double bytes = (double)(N + K) * R * (2.0 * nA + 4.0 * slots) + 16.0 * (double)R * (M + 32.0);
+    if (bytes > 4e18) return SIZE_MAX;
     return backward_layout(M, N, K, R, S, nA).total;
 }
 

@@ -486,7 +486,9 @@ dmpq_status dmpq_qgemm_nvfp4_lora(hipStream_t stream, const uint8_t *ca, const u
  * da and db are written whole: zeros past a rank and for adapters without
  * rows.  N must be a multiple of 16 (it is summed over).  At most 65535
  * adapters, and n_adapters * (N + K) at most 2^31.  ws:
- * dmpq_lora_backward_bytes() bytes. */
+ * dmpq_lora_backward_bytes() bytes (0: out of range, or past 4e18 bytes).  They
+ * grow with the number of requests, used or empty: each may need a partial sum
+ * of its own, (N + K) * R fp32 values, beside those of the chunks of rows. */
 size_t dmpq_lora_backward_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t S,
                                 int64_t n_adapters);
 dmpq_status dmpq_lora_backward(hipStream_t stream, const uint16_t *dy, const uint16_t *x,

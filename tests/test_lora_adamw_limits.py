@@ -9,3 +9,22 @@ def test_backward_of_a_pool_too_large():
     big = dict(N=1 << 16, K=1 << 16, n=65535, bytes=1 << 62)
     refused(4, "dmpq_lora_backward", *backward_args(**big))
     assert "2^31" in dm.last_error()
+
+
+def test_a_workspace_past_64_bits():
+    """(chunks + requests) partials of (N + K) * R values: with 2^28 requests at the widest
+    linear 2^64 bytes and a little more, of which only the little came back."""
+    size = dm.lib().dmpq_lora_backward_bytes
+    W = 1 << 26
+    assert size(1, W, W, 128, 1 << 20, 1) > 1 << 56
+    for S in ((1 << 28) - 1, 1 << 28, (1 << 28) + 77, (1 << 29) - 1):
+        assert size(1, W, W, 128, S, 1) == 0
+        refused(4, "dmpq_lora_backward", *backward_args(M=1, N=W, K=W, R=128, S=S, n=1, bytes=1 << 62))
+    assert size(1 << 29, W, W, 128, 1 << 28, 1) == 0
+    assert size(0, W, W, 128, 0, (1 << 30) - 1) == 0  # the transposed pools alone
+    # exact below the limit: what the parts add up to, each rounded up to 256 bytes
+    up = lambda v: -(-v // 256) * 256  # noqa: E731
+    M, N, K, R, S, n = 100, 48, 80, 16, 3, 2
+    slots = 1 + S
+    want = up(2 * n * R * K) + up(2 * n * R * N) + 2 * up(2 * 3 * R * 128) + up(4 * M * R) + up(4 * slots * N * R) + up(4 * slots * K * R)
+    assert size(M, N, K, R, S, n) == want
