@@ -586,8 +586,9 @@ def lora_backward(dy, x, t, a, b, rank, scale, seg_start, seg_adapter, dx_base, 
 # ---- AdamW over many tensors ----------------------------------------------------
 
 class AdamwTable:
-    """The places of the tensors that one adamw_step call updates.  Holds
-    references to them: their memory must not move while the table is used."""
+    """The places of the tensors that one adamw_step call updates.  Holds the
+    tensors themselves, whatever becomes of the lists they came in: their memory
+    must not move while the table is used."""
 
     def __init__(self, table, n: int, chunks: int, p_dtype: int, g_dtype: int, bits: int, keep):
         self.table, self.n, self.chunks = table, n, chunks
@@ -631,7 +632,7 @@ def adamw_table(params, grads, m, v, m_scales=None, v_scales=None, copies=None) 
     _check(lib().dmpq_adamw_table(rows, k, p_dtype, g_dtype, bits, host.data_ptr(), nbytes,
                                   C.byref(chunks)), "dmpq_adamw_table")
     device = params[0].device if k else "cuda"
-    return AdamwTable(host.to(device), k, chunks.value, p_dtype, g_dtype, bits, lists)
+    return AdamwTable(host.to(device), k, chunks.value, p_dtype, g_dtype, bits, [tuple(x) for x in lists])
 
 
 def _one_size(ts, name: str) -> int:

@@ -1,5 +1,10 @@
-"""CPU: limits of the adapter entry points that only very large sizes meet.  Nothing
-here is launched."""
+"""CPU: limits of the adapter entry points that only very large sizes meet, and what
+the table of an AdamW step keeps.  Nothing here is launched."""
+import gc
+import weakref
+
+import torch
+
 import dynamic_mixed_precision_amd as dm
 from test_lora_adamw_abi import backward_args, refused
 
@@ -28,3 +33,23 @@ def test_a_workspace_past_64_bits():
     slots = 1 + S
     want = up(2 * n * R * K) + up(2 * n * R * N) + 2 * up(2 * 3 * R * 128) + up(4 * M * R) + up(4 * slots * N * R) + up(4 * slots * K * R)
     assert size(M, N, K, R, S, n) == want
+
+
+def test_the_table_keeps_its_tensors(monkeypatch):
+    """The table writes to the tensors' memory, so they live as long as it does, also where
+    the caller's lists are emptied or their entries replaced."""
+    monkeypatch.setattr(dm, "_ptr", lambda t: None if t is None else t.data_ptr())
+    new = lambda: [torch.zeros(64) for _ in range(3)]  # noqa: E731
+    lists = [new() for _ in range(4)]
+    alive = [weakref.ref(t) for ts in lists for t in ts]
+    table = dm.adamw_table(*lists)
+    for i, ts in enumerate(lists):
+        if i % 2:
+            ts.clear()
+        else:
+            ts[:] = [None] * 3
+    gc.collect()
+    assert all(r() is not None for r in alive)
+    del table
+    gc.collect()
+    assert all(r() is None for r in alive)
