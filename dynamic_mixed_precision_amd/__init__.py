@@ -470,26 +470,58 @@ def selftest_codec(codec: int, lo: int, hi: int, stats, stream=None) -> None:
 
 # ---- low-rank adapters beside a linear ----------------------------------------
 
+_types = None
+
+
+def _load_types():
+    """Per kind of operand the tensor types that hold it: bf16 also as its bits,
+    8-bit codes also as bytes."""
+    global _types
+    import torch
+    _types = {"fp32": frozenset((torch.float32,)), "int32": frozenset((torch.int32,)),
+              "bf16": frozenset((torch.bfloat16, torch.int16, torch.uint16)),
+              "E4M3": frozenset((torch.float8_e4m3fn, torch.uint8, torch.int8))}
+    return _types
+
+
+def _need_type(t, name: str, nbytes: int, kind: str) -> None:
+    """As _need, and by type instead of element size: fp16 has bf16's size, and
+    fp32 has int32's."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    if t.dtype not in (_types or _load_types())[kind]:
+        raise ValueError(f"{name} is {t.dtype}, needs {kind}")
+    have = t.nbytes
+    if have < nbytes:
+        raise ValueError(f"{name} holds {have} bytes, needs {nbytes}")
+
+
+def _need_lora_out(y, name: str, M: int, N: int, out_dtype: int) -> None:
+    if out_dtype == OUT_BF16:
+        _need_type(y, name, 2 * M * N, "bf16")
+    elif out_dtype == OUT_F32:  # any other type is the library's error to report
+        _need_type(y, name, 4 * M * N, "fp32")
+
 def _need_lora(x_rows: int, a, b, rank, scale, seg_start, seg_adapter, t, K=None, N=None):
     """The pool and batch that every adapter call shares; returns (R, S, n)."""
     n, R = _pool_shape(a if a is not None else b, a is not None)
     if a is not None:
         if a.shape != (n, R, K):
             raise ValueError(f"a has shape {tuple(a.shape)}, needs {(n, R, K)}")
-        _need(a, "a", 2 * n * R * K, 2)
+        _need_type(a, "a", 2 * n * R * K, "bf16")
     if b is not None:
         if b.shape != (n, N, R):
             raise ValueError(f"b has shape {tuple(b.shape)}, needs {(n, N, R)}")
-        _need(b, "b", 2 * n * N * R, 2)
-    _need(rank, "rank", 4 * n, 4)
+        _need_type(b, "b", 2 * n * N * R, "bf16")
+    _need_type(rank, "rank", 4 * n, "int32")
     if scale is not None:
-        _need(scale, "scale", 4 * n, 4)
+        _need_type(scale, "scale", 4 * n, "fp32")
     S = seg_start.numel() - 1
     if S < 0:
         raise ValueError("seg_start needs at least one entry")
-    _need(seg_start, "seg_start", 4 * (S + 1), 4)
-    _need(seg_adapter, "seg_adapter", 4 * S, 4)
-    _need(t, "t", 4 * x_rows * R, 4)
+    _need_type(seg_start, "seg_start", 4 * (S + 1), "int32")
+    _need_type(seg_adapter, "seg_adapter", 4 * S, "int32")
+    _need_type(t, "t", 4 * x_rows * R, "fp32")
     return R, S, n
 
 
@@ -510,7 +542,7 @@ def new_lora_workspace(M: int, N: int, K: int, R: int, S: int, n_adapters: int, 
 def lora_shrink(x, a, rank, seg_start, seg_adapter, t, stream=None) -> None:
     """t [M, R] fp32 = x a^T, each row through the adapter of its request."""
     M, K = x.shape
-    _need(x, "x", 2 * M * K, 2)
+    _need_type(x, "x", 2 * M * K, "bf16")
     R, S, n = _need_lora(M, a, None, rank, None, seg_start, seg_adapter, t, K=K)
     _check(lib().dmpq_lora_shrink(_stream(stream), _ptr(x), _ptr(a), _ptr(rank), _ptr(seg_start),
                                   _ptr(seg_adapter), M, K, R, S, n, _ptr(t)), "dmpq_lora_shrink")
@@ -521,11 +553,11 @@ def lora_forward(x, base, a, b, rank, scale, seg_start, seg_adapter, t, y, out_d
     """t as lora_shrink, and y = base + scale * t b^T (base may be y, or None for zeros)."""
     M, K = x.shape
     N = b.shape[1]
-    _need(x, "x", 2 * M * K, 2)
+    _need_type(x, "x", 2 * M * K, "bf16")
     R, S, n = _need_lora(M, a, b, rank, scale, seg_start, seg_adapter, t, K=K, N=N)
-    _need_out(y, M, N, out_dtype)
+    _need_lora_out(y, "y", M, N, out_dtype)
     if base is not None:
-        _need_out(base, M, N, out_dtype)
+        _need_lora_out(base, "base", M, N, out_dtype)
     _check(lib().dmpq_lora_forward(_stream(stream), _ptr(x), _ptr(base), _ptr(a), _ptr(b), _ptr(rank),
                                    _ptr(scale), _ptr(seg_start), _ptr(seg_adapter), M, N, K, R, S, n,
                                    out_dtype, _ptr(t), _ptr(y)), "dmpq_lora_forward")
@@ -535,6 +567,9 @@ def gemm_bf16_lora(x, w, t, b, rank, scale, seg_start, seg_adapter, y, epilogue:
                    out_dtype: int = OUT_BF16, stream=None) -> None:
     """gemm_bf16_ex with the adapters' scale * t b^T added in its epilogue."""
     M, N, K = _need_bf16_gemm(x, w, y, out_dtype)
+    _need_type(x, "x", 0, "bf16")
+    _need_type(w, "w", 0, "bf16")
+    _need_lora_out(y, "y", M, N, out_dtype)
     R, S, n = _need_lora(M, None, b, rank, scale, seg_start, seg_adapter, t, N=N)
     _check(lib().dmpq_gemm_bf16_lora(_stream(stream), _ptr(x), _ptr(w), _ptr(t), _ptr(b), _ptr(rank),
                                      _ptr(scale), _ptr(seg_start), _ptr(seg_adapter), M, N, K, R, S, n,
@@ -545,6 +580,7 @@ def qgemm_int8_lora(qa, sa, qw, sw, t, b, rank, scale, seg_start, seg_adapter, y
                     ws=None, out_dtype: int = OUT_BF16, stream=None) -> None:
     """qgemm_int8_ex with the adapters' scale * t b^T added in its epilogue."""
     M, N, K = _need_int8_gemm(qa, sa, qw, sw, y, out_dtype)
+    _need_lora_out(y, "y", M, N, out_dtype)
     R, S, n = _need_lora(M, None, b, rank, scale, seg_start, seg_adapter, t, N=N)
     _check(lib().dmpq_qgemm_int8_lora(_stream(stream), _ptr(qa), _ptr(sa), _ptr(qw), _ptr(sw), _ptr(t),
                                       _ptr(b), _ptr(rank), _ptr(scale), _ptr(seg_start), _ptr(seg_adapter),
@@ -556,6 +592,7 @@ def qgemm_nvfp4_lora(ca, sa, ga, cw, sw, gw, t, b, rank, scale, seg_start, seg_a
                      epilogue: int = 0, ws=None, out_dtype: int = OUT_BF16, stream=None) -> None:
     """qgemm_nvfp4_ex with the adapters' scale * t b^T added in its epilogue."""
     M, N, K = _need_nvfp4_gemm(ca, sa, ga, cw, sw, gw, y, out_dtype)
+    _need_lora_out(y, "y", M, N, out_dtype)
     R, S, n = _need_lora(M, None, b, rank, scale, seg_start, seg_adapter, t, N=N)
     _check(lib().dmpq_qgemm_nvfp4_lora(_stream(stream), _ptr(ca), _ptr(sa), _ptr(ga), _ptr(cw), _ptr(sw),
                                        _ptr(gw), _ptr(t), _ptr(b), _ptr(rank), _ptr(scale),
@@ -569,14 +606,14 @@ def lora_backward(dy, x, t, a, b, rank, scale, seg_start, seg_adapter, dx_base, 
     may be dx, or None for zeros; dx None: not computed)."""
     M, K = x.shape
     N = b.shape[1]
-    _need(x, "x", 2 * M * K, 2)
-    _need(dy, "dy", 2 * M * N, 2)
+    _need_type(x, "x", 2 * M * K, "bf16")
+    _need_type(dy, "dy", 2 * M * N, "bf16")
     R, S, n = _need_lora(M, a, b, rank, scale, seg_start, seg_adapter, t, K=K, N=N)
     for g, name in ((dx_base, "dx_base"), (dx, "dx")):
         if g is not None:
-            _need(g, name, 2 * M * K, 2)
-    _need(da, "da", 4 * n * R * K, 4)
-    _need(db, "db", 4 * n * N * R, 4)
+            _need_type(g, name, 2 * M * K, "bf16")
+    _need_type(da, "da", 4 * n * R * K, "fp32")
+    _need_type(db, "db", 4 * n * N * R, "fp32")
     _check(lib().dmpq_lora_backward(_stream(stream), _ptr(dy), _ptr(x), _ptr(t), _ptr(a), _ptr(b),
                                     _ptr(rank), _ptr(scale), _ptr(seg_start), _ptr(seg_adapter),
                                     _ptr(dx_base), M, N, K, R, S, n, _ptr(dx), _ptr(da), _ptr(db),
@@ -608,20 +645,19 @@ def adamw_table(params, grads, m, v, m_scales=None, v_scales=None, copies=None) 
              copies if copies is not None else [None] * k]
     if any(x is None or len(x) != k for x in lists):
         raise ValueError("adamw_table needs lists of the same length")
-    p_dtype = OUT_BF16 if _one_size(params, "params") == 2 else OUT_F32
-    g_dtype = OUT_BF16 if _one_size(grads, "grads") == 2 else OUT_F32
+    p_dtype, g_dtype = _one_type(params, "params"), _one_type(grads, "grads")
     rows = (AdamwTensor * max(1, k))()
     for i, (p, g, mi, vi, ms, vs, c) in enumerate(zip(*lists)):
         n = p.numel()
         blocks = (n + 255) // 256
         _need(g, "grad", n * g.element_size())
         for s, name in ((mi, "m"), (vi, "v")):
-            _need(s, name, n * (1 if eight else 4), 1 if eight else 4)
+            _need_type(s, name, n * (1 if eight else 4), "E4M3" if eight else "fp32")
         if eight:
-            _need(ms, "m_scales", 4 * blocks, 4)
-            _need(vs, "v_scales", 4 * blocks, 4)
+            _need_type(ms, "m_scales", 4 * blocks, "fp32")
+            _need_type(vs, "v_scales", 4 * blocks, "fp32")
         if c is not None:
-            _need(c, "copy", 2 * n, 2)
+            _need_type(c, "copy", 2 * n, "bf16")
         for f, q in (("p", p), ("g", g), ("m", mi), ("v", vi), ("ms", ms), ("vs", vs), ("copy", c)):
             setattr(rows[i], f, _ptr(q))
         rows[i].n = n
@@ -635,11 +671,12 @@ def adamw_table(params, grads, m, v, m_scales=None, v_scales=None, copies=None) 
     return AdamwTable(host.to(device), k, chunks.value, p_dtype, g_dtype, bits, [tuple(x) for x in lists])
 
 
-def _one_size(ts, name: str) -> int:
-    sizes = {t.element_size() for t in ts} or {4}
-    if len(sizes) != 1 or not sizes <= {2, 4}:
-        raise ValueError(f"{name} must all be fp32 or all bf16")
-    return sizes.pop()
+def _one_type(ts, name: str) -> int:
+    kinds = {t.dtype for t in ts}
+    for out, kind in ((OUT_F32, "fp32"), (OUT_BF16, "bf16")):
+        if kinds <= (_types or _load_types())[kind]:
+            return out
+    raise ValueError(f"{name} must all be fp32 or all bf16")
 
 
 def grad_norm(table: AdamwTable, norm, ws, stream=None) -> None:
