@@ -368,7 +368,7 @@ __device__ __forceinline__ void f32_band_epilogue(v16f (&acc)[4][4], uint8_t *ld
                                                   void *y, float *slot, const LoraEpi &lora) {
     if constexpr ((EPI & kEpiLora) != 0) {
         EpiScaleF32 sc{gA, gW};
-        lora_epilogue<OUT, EPI, 4>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot, lora);
+        lora_epilogue<OUT, EPI, 3>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot, lora);
     } else {
         EpiScaleF32 sc{gA, gW};
         band_epilogue<OUT, EPI>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot);

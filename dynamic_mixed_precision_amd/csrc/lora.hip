@@ -7,10 +7,11 @@
 //   backward u = scale dy b, dx = dx_base + u a, da = u^T x, db = scale dy^T t
 //
 // Every product has one dimension of at most 128, so all of them are bound by
-// the one pass over their widest tensor.  MFMA does the products: x, dy, a and
-// b are bf16 and exact in it; t and u are fp32 and enter as 3 bf16 parts that
-// hold all their bits (split8).  Sums are fp32 in a fixed order: no atomics, the
-// same bits on every call.
+// the passes over their widest tensor: one, but two over dy in the backward
+// pass (u needs whole rows of it, db whole columns).  MFMA does the products: x,
+// dy, a and b are bf16 and exact in it; t and u are fp32 and enter as 3 bf16
+// parts that hold all their bits (split8).  Sums are fp32 in a fixed order: no
+// atomics, the same bits on every call.
 #include <type_traits>
 
 #include "device.hpp"

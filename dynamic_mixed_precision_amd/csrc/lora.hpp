@@ -107,7 +107,8 @@ __device__ __forceinline__ int adapter_rank(const LoraBatch &B, int a) {
 // that factor is at hand as fragments, the later parts multiply finite8() of
 // it.  Where it lies in LDS it does so as ones8(), and a product that is taken
 // only if such a value was seen adds odd8() of it times the value's sign
-// (sign8): a branch in every product instead cost the INT8 GEMM 10% at rank 64.
+// (sign8): a branch in every product instead cost the INT8 GEMM 6% at rank 64,
+// this way 3%.
 // Either way inf * value is infinite with the right sign and inf * 0 NaN; with
 // finite8() a value below bf16's range (2^-133) counts as 0 there.
 constexpr int kParts = 3;
@@ -293,10 +294,11 @@ __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_
 
 // Of a 256 x 256 tile of 2 x 2 waves, slice by slice: the epilogue writes 32
 // rows of every wave's scaled fp32 values to LDS bands, and lora_band_add adds
-// the adapters' products to the bands.  (Onto the accumulators themselves the
-// products need no LDS traffic, but whatever stood between the main loop and
-// them made the compiler spill accumulators: 26 to 130 us more on a GEMM of
-// 237 us even without any adapter.)
+// the adapters' products to the bands.  (Onto the scaled values in registers
+// the products need no LDS traffic, but the code between the main loop and the
+// stores then spills: the INT8 GEMM of 17776 x 1920 x 5760, 211 us without the
+// term, took 269 without a single adapter and 303 at rank 16; 253 and 284 with
+// the bands.)
 //
 // The workgroup copies b's 256 rows of one request into LDS (entries past the
 // rank as zeros); a tile that belongs to one request does so once.  A lane
@@ -345,15 +347,17 @@ struct LoraWords {
     }
 };
 
-// AHEAD: the 16-rank pieces of t that a lane holds a slice ahead; the others
-// are loaded as they are used.  4 (a rank of 64) in the fp32-accumulator
-// GEMMs.  The INT8 GEMM's registers hold no more than 1: with 4 its kernel
-// spills 34 and takes 302 us without any adapter where it takes 252 with 1.
 // the last words of the area: for each wave, whether the b it copied holds an
 // infinity or NaN
 constexpr int kLoraOddOff = kLoraLds - 16;
 static_assert(kLoraBOff + 256 * (2 * kMaxLoraRank + 16) <= kLoraOddOff && kLoraOddOff % 16 == 0, "bands and b fit");
 
+// AHEAD: the 16-rank pieces of t that a lane holds a slice ahead; the others
+// are loaded as they are used.  3 (a rank of 48) in the fp32-accumulator GEMMs:
+// with 4 the NVFP4 kernels spill up to 25 registers (17776 x 1920 x 5760, rank
+// 16: 434 us against 427; x 3072 x 9216, rank 64: 914 and 911; with 2: 423 and
+// 919).  The INT8 GEMM's registers hold no more than 1: with 4 it takes 277 us
+// without any adapter where it takes 253 with 1.
 template <int AHEAD>
 struct LoraRows {
     v4f v[AHEAD][2];
@@ -512,7 +516,13 @@ __device__ __forceinline__ void lora_band_add(const LoraEpi &L, LoraTile &T, int
                     piece(c, *reinterpret_cast<const v4f *>(p + c), *reinterpret_cast<const v4f *>(p + c + 4));
             }
             if (__builtin_expect(T.odd, 0)) {  // b's infinities and NaN, from memory
-                const float *p = T.row(L, i);
+                // (the empty asm keeps this branch's addresses from being computed, and
+                // held in registers, before it)
+                int tid = threadIdx.x;
+                asm volatile("" : "+v"(tid));
+                const int lm = tid & 31, lh = tid >> 5 & 1, wn = tid >> 6 & 1;
+                const int r = T.r0 + (tid >> 7) * 128 + 32 * i + lm;
+                const float *p = L.t + (int64_t)(r < B.M ? r : B.M - 1) * B.R + 8 * lh;
                 const uint16_t *bw = L.b + (int64_t)T.words.adapter(B, s) * N * B.R + 8 * lh;
 #pragma unroll 1
                 for (int c = 0; c < T.rank; c += 16) {
