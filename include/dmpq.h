@@ -513,7 +513,9 @@ dmpq_status dmpq_lora_backward(hipStream_t stream, const uint16_t *dy, const uin
  * v = (E4M3(v code) * vs)^2 with vs = max sqrt(v) / 448; a v that is not zero
  * keeps at least the smallest code.  All zeros is the start of both forms.
  * A gradient that is not finite makes its value (8 bits: an infinity, its
- * block) NaN for good, unless the step is guarded by the norm.
+ * block) NaN for good, unless the step is guarded by the norm.  One whose square
+ * overflows fp32 (above 1.8e19 after clipping) makes v infinite, so that its
+ * parameter no longer moves (8 bits: its block NaN).
  * ========================================================================= */
 typedef struct dmpq_adamw_tensor {
     void *p;
