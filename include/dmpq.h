@@ -515,7 +515,8 @@ dmpq_status dmpq_lora_backward(hipStream_t stream, const uint16_t *dy, const uin
  * A gradient that is not finite makes its value (8 bits: an infinity, its
  * block) NaN for good, unless the step is guarded by the norm.  One whose square
  * overflows fp32 (above 1.8e19 after clipping) makes v infinite, so that its
- * parameter no longer moves (8 bits: its block NaN).
+ * parameter no longer moves but for the decay (8 bits: none of its block does,
+ * and it becomes NaN).
  * ========================================================================= */
 typedef struct dmpq_adamw_tensor {
     void *p;
