@@ -145,7 +145,14 @@ for _r in GEMMS:
     FORMS[_r] = lambda q, base, f32=False, r=_r: projected(q, r, base, f32)
     FORMS[_r + "-split"] = lambda q, base, f32=False, r=_r: projected(q, r, base, f32, True)
 BOTH = [(f, o) for f in FORMS for o in (False, True) if not (f == "dx" and o)]
-both = pytest.mark.parametrize("form,f32", BOTH, ids=[f + ("-f32" if o else "-bf16") for f, o in BOTH])
+
+
+def forms(without=()):
+    some = [(f, o) for f, o in BOTH if f not in without]
+    return pytest.mark.parametrize("form,f32", some, ids=[f + ("-f32" if o else "-bf16") for f, o in some])
+
+
+both = forms()
 
 
 def same(y, want, tol):
@@ -246,12 +253,10 @@ def test_infinite_factors(form, f32):
     same(FORMS[form](q, 0, f32), want, rounded(tol, want, f32))
 
 
-@both
+@forms(without=("forward", "dx"))  # (there t is computed, from finite factors)
 def test_infinite_rows(form, f32):
     """The same of the other factor: infinities and NaN in t (the GEMMs take it as it is)."""
     require_gpu()
-    if form in ("forward", "dx"):
-        pytest.skip("t is computed there, from finite factors")
     say(f"infinite t {form} {f32}")
     q = infinite_pool(4)
     q.b = np.where(np.isfinite(q.b), q.b, 0.25).astype(np.float32)
@@ -390,14 +395,12 @@ def test_rank_zero_has_no_gradient():
     assert torch.equal(dx.view(torch.int16), base.view(torch.int16)) and not da.any() and not db.any()
 
 
-@both
+@forms(without=("dx",))  # (there u = scale * dy b carries the scale)
 @pytest.mark.parametrize("scale", [np.inf, 2.0 ** 120])
 def test_the_scale_multiplies_the_sum(form, f32, scale):
     """y = base + scale * (t b^T): a scale that would overflow t alone, or is infinite, meets
     the sum of the products (terms of both signs), not each of them."""
     require_gpu()
-    if form == "dx":
-        pytest.skip("u = scale * dy b carries the scale there")
     say(f"scale {scale} {form} {f32}")
     rng = np.random.default_rng(6)
     M, N, R = 90, 80, 16
