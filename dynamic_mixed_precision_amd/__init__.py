@@ -30,6 +30,9 @@ FP4_SCALED_MFMA = 1
 OP_GAMMA, OP_QUANT_NVFP4, OP_TDC, OP_PREP_WEIGHT, OP_OUTLIER, OP_GEMM_AMAX, OP_GEMM = 0, 1, 2, 3, 4, 5, 6
 OP_GEMM_W4 = 7
 OP_GRAD_NORM = 8
+ACT_NONE, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+ROPE_PAIRS, ROPE_HALVES = 0, 1
 
 EXPORTS = ("dmpq_last_error", "dmpq_version", "dmpq_workspace_bytes", "dmpq_gamma_sums",
            "dmpq_gate_and_route", "dmpq_hadamard_quant_int8", "dmpq_hadamard_quant_nvfp4",
@@ -41,7 +44,10 @@ EXPORTS = ("dmpq_last_error", "dmpq_version", "dmpq_workspace_bytes", "dmpq_gamm
            "dmpq_hadamard_quant_int8_w8", "dmpq_lora_shrink", "dmpq_lora_forward",
            "dmpq_gemm_bf16_lora", "dmpq_qgemm_int8_lora", "dmpq_qgemm_nvfp4_lora",
            "dmpq_lora_backward_bytes", "dmpq_lora_backward", "dmpq_adamw_table_bytes",
-           "dmpq_adamw_table", "dmpq_grad_norm", "dmpq_adamw_step")
+           "dmpq_adamw_table", "dmpq_grad_norm", "dmpq_adamw_step", "dmpq_gemm_bf16_linear",
+           "dmpq_qgemm_int8_linear", "dmpq_qgemm_nvfp4_linear", "dmpq_linear_backward_bytes",
+           "dmpq_linear_epilogue_backward", "dmpq_rope_table", "dmpq_qk_norm_rope",
+           "dmpq_qk_backward_bytes", "dmpq_qk_norm_rope_backward")
 
 
 class DmpqError(RuntimeError):
@@ -60,6 +66,29 @@ class AdamwTensor(C.Structure):
     """Mirror of dmpq_adamw_tensor."""
     _fields_ = [("p", C.c_void_p), ("g", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
                 ("ms", C.c_void_p), ("vs", C.c_void_p), ("copy", C.c_void_p), ("n", C.c_int64)]
+
+
+class QkHeadsStruct(C.Structure):
+    """Mirror of dmpq_qk_heads."""
+    _fields_ = [("n_q", C.c_int32), ("n_k", C.c_int32), ("dim", C.c_int32), ("norm", C.c_int32),
+                ("layout", C.c_int32), ("w_dtype", C.c_int32), ("rope_pairs", C.c_int32), ("eps", C.c_double),
+                ("wq", C.c_void_p), ("bq", C.c_void_p), ("wk", C.c_void_p), ("bk", C.c_void_p),
+                ("table", C.c_void_p)]
+
+
+class LoraTermStruct(C.Structure):
+    """Mirror of dmpq_lora_term."""
+    _fields_ = [("t", C.c_void_p), ("b", C.c_void_p), ("rank", C.c_void_p), ("scale", C.c_void_p),
+                ("seg_start", C.c_void_p), ("seg_adapter", C.c_void_p), ("R", C.c_int64), ("S", C.c_int64),
+                ("n_adapters", C.c_int64)]
+
+
+class LinearEpilogueStruct(C.Structure):
+    """Mirror of dmpq_linear_epilogue."""
+    _fields_ = [("bias", C.c_void_p), ("gate", C.c_void_p), ("residual", C.c_void_p), ("gate_start", C.c_void_p),
+                ("pre", C.c_void_p), ("gate_rows", C.c_int64), ("bias_dtype", C.c_int32), ("gate_dtype", C.c_int32),
+                ("act", C.c_int32), ("flags", C.c_int32), ("heads", C.POINTER(QkHeadsStruct)),
+                ("lora", C.POINTER(LoraTermStruct))]
 
 
 class TdcParams(C.Structure):
@@ -124,6 +153,17 @@ def _declare(L):
                                    C.POINTER(C.c_int64)]),
         "dmpq_grad_norm": (i32, [vp, vp, i64, i64, i32, vp, vp, C.c_size_t]),
         "dmpq_adamw_step": (i32, [vp, vp, i64, i64, i32, i32, i32, f64, f64, f64, f64, f64, i64, vp, f64]),
+        "dmpq_gemm_bf16_linear": (i32, [vp] * 3 + [i64] * 3 + [i32, vp, vp, vp, C.c_size_t]),
+        "dmpq_qgemm_int8_linear": (i32, [vp] * 5 + [i64] * 3 + [i32, vp, vp, vp, C.c_size_t]),
+        "dmpq_qgemm_nvfp4_linear": (i32, [vp] * 7 + [i64] * 3 + [i32, vp, vp, vp, C.c_size_t]),
+        "dmpq_linear_backward_bytes": (C.c_size_t, [i64] * 3),
+        "dmpq_linear_epilogue_backward": (i32, [vp, vp, vp, i64, i64, i32, i32, vp, i32, vp, i64] + [vp] * 4 +
+                                          [C.c_size_t]),
+        "dmpq_rope_table": (i32, [vp, vp, i32, vp, i64, i32, vp, vp]),
+        "dmpq_qk_norm_rope": (i32, [vp, vp, i64, vp, i64, i64, i32, vp, vp, i64, vp, i64]),
+        "dmpq_qk_backward_bytes": (C.c_size_t, [i32]),
+        "dmpq_qk_norm_rope_backward": (i32, [vp] + [vp, i64] * 4 + [i64, i32, vp] + [vp, i64] * 2 + [vp] * 5 +
+                                       [C.c_size_t]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -697,3 +737,282 @@ def adamw_step(table: AdamwTable, lr: float, beta1: float = 0.9, beta2: float = 
     _check(lib().dmpq_adamw_step(_stream(stream), _ptr(table.table), table.n, table.chunks, table.p_dtype,
                                  table.g_dtype, table.bits, lr, beta1, beta2, eps, weight_decay, int(step),
                                  _ptr(norm), max_norm), "dmpq_adamw_step")
+
+
+# ---- the whole linear -----------------------------------------------------------
+
+def _float_type(t, name: str) -> int:
+    """OUT_F32 or OUT_BF16 of an fp32 or bf16 tensor."""
+    kinds = _types or _load_types()
+    if t.dtype in kinds["fp32"]:
+        return OUT_F32
+    if t.dtype in kinds["bf16"]:
+        return OUT_BF16
+    raise ValueError(f"{name} is {t.dtype}, needs fp32 or bf16")
+
+
+_KIND = {OUT_F32: ("fp32", 4), OUT_BF16: ("bf16", 2)}
+
+
+class QkHeads:
+    """The heads of q and k (qk_heads).  Holds its tensors."""
+
+    def __init__(self, struct, n_q: int, n_k: int, dim: int, norm: int, table, keep):
+        self.struct, self.n_q, self.n_k, self.dim, self.norm, self.table = struct, n_q, n_k, dim, norm, table
+        self._keep = keep
+
+
+def qk_heads(n_q: int, n_k: int, dim: int, norm: int = NORM_NONE, eps: float = 1e-6, wq=None, bq=None, wk=None,
+             bk=None, table=None, layout: int = ROPE_PAIRS) -> QkHeads:
+    """n_q heads of q and n_k of k of `dim` values: their norm with weights w and
+    b [dim] (fp32 or bf16, one type; None: 1 and 0) and, with the `table`
+    [rows, pairs, 2] of rope_table, the rotation.  The object can be kept: it
+    holds the tensors, which must not move."""
+    keep = (wq, bq, wk, bk, table)
+    kinds = set()
+    for w, name in ((wq, "wq"), (bq, "bq"), (wk, "wk"), (bk, "bk")):
+        if w is not None:
+            kinds.add(_float_type(w, name))
+            _need(w, name, dim * w.element_size())
+    if len(kinds) > 1:
+        raise ValueError("wq, bq, wk and bk must all be fp32 or all bf16")
+    pairs = 0
+    if table is not None:
+        if table.dim() != 3 or table.shape[2] != 2:
+            raise ValueError(f"table has shape {tuple(table.shape)}, needs (rows, pairs, 2)")
+        _need_type(table, "table", 0, "fp32")
+        pairs = table.shape[1]
+    st = QkHeadsStruct(n_q, n_k, dim, norm, layout, kinds.pop() if kinds else OUT_F32, pairs, eps, _ptr(wq),
+                       _ptr(bq), _ptr(wk), _ptr(bk), _ptr(table))
+    return QkHeads(st, n_q, n_k, dim, norm, table, keep)
+
+
+def _need_table(heads: QkHeads, M: int) -> None:
+    if heads.table is not None and heads.table.shape[0] < M:
+        raise ValueError(f"table has {heads.table.shape[0]} rows, needs {M}")
+
+
+class LinearEpilogue:
+    """What follows the product of a *_linear GEMM (linear_epilogue).  Holds its
+    tensors."""
+
+    def __init__(self, struct, bias, gate, gate_start, residual, pre, heads, adapters, keep):
+        self.struct, self.bias, self.gate, self.gate_start = struct, bias, gate, gate_start
+        self.residual, self.pre, self.heads, self.adapters = residual, pre, heads, adapters
+        self._keep = keep
+        self._checked = None
+
+
+def linear_epilogue(bias=None, act: int = ACT_NONE, gate=None, gate_start=None, residual=None, pre=None, heads=None,
+                    adapters=None, amax: bool = False) -> LinearEpilogue:
+    """y = residual + gate[request of the row] * act(x w^T + adapters + bias).
+
+    bias [N] and gate [S, N]: fp32 or bf16; gate_start int32 [S + 1]: the rows'
+    requests (None: the gate's one row is for all); residual and pre [M, N] of
+    y's type, pre receiving the value before heads and act; heads: a QkHeads,
+    for a QKV linear; adapters: (t, b, rank, scale, seg_start, seg_adapter) as
+    the *_lora GEMMs take them; amax: leave the NVFP4 amax of y in the workspace
+    (EPI_NVFP4_AMAX).  The object can be kept for further calls of the same
+    shapes: it holds the tensors, which must not move."""
+    rows = 0
+    bias_type = OUT_F32 if bias is None else _float_type(bias, "bias")
+    gate_type = OUT_F32 if gate is None else _float_type(gate, "gate")
+    if gate is not None:
+        if gate.dim() != 2:
+            raise ValueError(f"gate has shape {tuple(gate.shape)}, needs (requests, N)")
+        rows = gate.shape[0]
+        if gate_start is not None:
+            _need_type(gate_start, "gate_start", 4 * (rows + 1), "int32")
+    elif gate_start is not None:
+        raise ValueError("gate is missing")
+    lora = None
+    if adapters is not None:
+        t, b, rank, scale, seg_start, seg_adapter = adapters
+        R, S, n = _need_lora(0, None, b, rank, scale, seg_start, seg_adapter, t, N=_pool_n(b))
+        lora = LoraTermStruct(_ptr(t), _ptr(b), _ptr(rank), _ptr(scale), _ptr(seg_start), _ptr(seg_adapter), R, S, n)
+    st = LinearEpilogueStruct(
+        _ptr(bias), _ptr(gate), _ptr(residual), _ptr(gate_start), _ptr(pre), rows, bias_type, gate_type, act,
+        EPI_NVFP4_AMAX if amax else 0, None if heads is None else C.pointer(heads.struct),
+        None if lora is None else C.pointer(lora))
+    return LinearEpilogue(st, bias, gate, gate_start, residual, pre, heads, adapters, lora)
+
+
+def _pool_n(b) -> int:
+    if b.dim() != 3:
+        raise ValueError(f"the adapter pool has shape {tuple(b.shape)}, needs 3 dimensions")
+    return b.shape[1]
+
+
+def _need_linear(epi: LinearEpilogue, y, M: int, N: int, out_dtype: int):
+    _need_lora_out(y, "y", M, N, out_dtype)
+    if epi._checked != (M, N, out_dtype):  # an epilogue that is kept is looked over once per shape
+        if epi.bias is not None:
+            _need(epi.bias, "bias", N * epi.bias.element_size())
+        if epi.gate is not None and epi.gate.shape[1] != N:
+            raise ValueError(f"gate has shape {tuple(epi.gate.shape)}, needs {N} columns")
+        for t, name in ((epi.residual, "residual"), (epi.pre, "pre")):
+            if t is not None:
+                _need_lora_out(t, name, M, N, out_dtype)
+        if epi.heads is not None:
+            _need_table(epi.heads, M)
+        if epi.adapters is not None:
+            t, b, rank, scale, seg_start, seg_adapter = epi.adapters
+            _need_lora(M, None, b, rank, scale, seg_start, seg_adapter, t, N=N)
+        epi._checked = (M, N, out_dtype)
+    return C.addressof(epi.struct)
+
+
+def gemm_bf16_linear(x, w, y, epilogue: LinearEpilogue, ws=None, out_dtype: int = OUT_BF16, stream=None) -> None:
+    """The BF16 linear x w^T with the whole epilogue; ws: an OP_GEMM workspace
+    (None: no tail split; needed for amax)."""
+    M, N, K = _need_bf16_gemm(x, w, y, out_dtype)
+    _need_type(x, "x", 0, "bf16")
+    _need_type(w, "w", 0, "bf16")
+    e = _need_linear(epilogue, y, M, N, out_dtype)
+    _check(lib().dmpq_gemm_bf16_linear(_stream(stream), _ptr(x), _ptr(w), M, N, K, out_dtype, _ptr(y), e, *_ws(ws)),
+           "dmpq_gemm_bf16_linear")
+
+
+def qgemm_int8_linear(qa, sa, qw, sw, y, epilogue: LinearEpilogue, ws=None, out_dtype: int = OUT_BF16,
+                      stream=None) -> None:
+    """The INT8 linear with the whole epilogue."""
+    M, N, K = _need_int8_gemm(qa, sa, qw, sw, y, out_dtype)
+    e = _need_linear(epilogue, y, M, N, out_dtype)
+    _check(lib().dmpq_qgemm_int8_linear(_stream(stream), _ptr(qa), _ptr(sa), _ptr(qw), _ptr(sw), M, N, K, out_dtype,
+                                        _ptr(y), e, *_ws(ws)), "dmpq_qgemm_int8_linear")
+
+
+def qgemm_nvfp4_linear(ca, sa, ga, cw, sw, gw, y, epilogue: LinearEpilogue, ws=None, out_dtype: int = OUT_BF16,
+                       stream=None) -> None:
+    """The NVFP4 linear with the whole epilogue."""
+    M, N, K = _need_nvfp4_gemm(ca, sa, ga, cw, sw, gw, y, out_dtype)
+    e = _need_linear(epilogue, y, M, N, out_dtype)
+    _check(lib().dmpq_qgemm_nvfp4_linear(_stream(stream), _ptr(ca), _ptr(sa), _ptr(ga), _ptr(cw), _ptr(sw), _ptr(gw),
+                                         M, N, K, out_dtype, _ptr(y), e, *_ws(ws)), "dmpq_qgemm_nvfp4_linear")
+
+
+def new_linear_backward_workspace(M: int, N: int, gate_rows: int = 0, device="cuda"):
+    """Workspace tensor for linear_epilogue_backward."""
+    import torch
+    return torch.empty(int(lib().dmpq_linear_backward_bytes(M, N, gate_rows)), dtype=torch.uint8, device=device)
+
+
+def linear_epilogue_backward(dy, pre, du, ws=None, act: int = ACT_NONE, gate=None, gate_start=None, dgate=None,
+                             dbias=None, stream=None) -> None:
+    """Gradients of y = residual + gate * act(pre) from dy [M, N]: du of pre
+    (may be dy or pre, or None), dgate [S, N] and dbias [N] fp32 (None: not
+    computed).  pre may be None where act is ACT_NONE and dgate None."""
+    M, N = dy.shape
+    dtype = _float_type(dy, "dy")
+    kind, size = _KIND[dtype]
+    for t, name in ((pre, "pre"), (du, "du")):
+        if t is not None:
+            _need_type(t, name, size * M * N, kind)
+    rows = 0
+    if gate is not None:
+        if gate.dim() != 2 or gate.shape[1] != N:
+            raise ValueError(f"gate has shape {tuple(gate.shape)}, needs (requests, {N})")
+        rows = gate.shape[0]
+        if gate_start is not None:
+            _need_type(gate_start, "gate_start", 4 * (rows + 1), "int32")
+        if dgate is not None:
+            _need_type(dgate, "dgate", 4 * rows * N, "fp32")
+    elif gate_start is not None or dgate is not None:
+        raise ValueError("gate is missing")
+    if dbias is not None:
+        _need_type(dbias, "dbias", 4 * N, "fp32")
+    _check(lib().dmpq_linear_epilogue_backward(
+        _stream(stream), _ptr(dy), _ptr(pre), M, N, dtype, act, _ptr(gate),
+        0 if gate is None else _float_type(gate, "gate"), _ptr(gate_start), rows, _ptr(du), _ptr(dgate), _ptr(dbias),
+        *_ws(ws)), "dmpq_linear_epilogue_backward")
+
+
+# ---- the heads of q and k ---------------------------------------------------------
+
+def rope_table(pos, freqs, axis_pairs, table, stream=None) -> None:
+    """table [M, P, 2] fp32 = (cos, sin) of pos[m, axis] * freqs[p]: pos [M, axes]
+    int32 or fp32, freqs [P] fp64 (radians per position), axis_pairs: how many of
+    the P pairs turn with each axis, in their order."""
+    if pos.dim() != 2 or pos.shape[1] != len(axis_pairs):
+        raise ValueError(f"pos has shape {tuple(pos.shape)}, needs (rows, {len(axis_pairs)})")
+    M, P = pos.shape[0], sum(axis_pairs)
+    kinds = _types or _load_types()
+    kind = OUT_F32 if pos.dtype in kinds["fp32"] else OUT_I32 if pos.dtype in kinds["int32"] else None
+    if kind is None:
+        raise ValueError(f"pos is {pos.dtype}, needs int32 or fp32")
+    if str(freqs.dtype) != "torch.float64":
+        raise ValueError(f"freqs is {freqs.dtype}, needs fp64")
+    _need(freqs, "freqs", 8 * P)
+    _need_type(table, "table", 8 * M * P, "fp32")
+    pairs = (C.c_int32 * len(axis_pairs))(*axis_pairs)
+    _check(lib().dmpq_rope_table(_stream(stream), _ptr(pos), kind, _ptr(freqs), M, len(axis_pairs), pairs,
+                                 _ptr(table)), "dmpq_rope_table")
+
+
+def _rows(t, name: str, M: int, n: int, dim: int, kind: str):
+    """(pointer, row stride) of [M, n, dim] heads whose rows may lie apart."""
+    if t is None:
+        if n * M > 0:
+            raise ValueError(f"{name} is missing")
+        return None, n * dim
+    if tuple(t.shape) != (M, n, dim):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {(M, n, dim)}")
+    if t.dtype not in (_types or _load_types())[kind]:
+        raise ValueError(f"{name} is {t.dtype}, needs {kind}")
+    if not t.is_cuda:
+        raise ValueError("libdmpq device arguments must be GPU tensors")
+    st = t.stride()
+    if (dim > 1 and st[2] != 1) or (n > 1 and st[1] != dim):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    return (t.data_ptr() if t.numel() else None), (st[0] if M > 1 else n * dim)
+
+
+def _qk_shape(q, k, heads: QkHeads):
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("q and k are missing")
+    M = some.shape[0]
+    _need_table(heads, M)
+    dtype = _float_type(some, "q")
+    return M, dtype, _KIND[dtype][0]
+
+
+def qk_norm_rope(q, k, heads: QkHeads, q_out, k_out, stream=None) -> None:
+    """q_out, k_out = the heads of q [M, n_q, dim] and k [M, n_k, dim] normed and
+    rotated (fp32 or bf16; may be q and k).  Rows may lie apart: q and k can be
+    views into the rows of QKV.  q and q_out (k and k_out) are None for 0 heads."""
+    M, dtype, kind = _qk_shape(q, k, heads)
+    args = []
+    for t, name, n in ((q, "q", heads.n_q), (k, "k", heads.n_k), (q_out, "q_out", heads.n_q),
+                       (k_out, "k_out", heads.n_k)):
+        args.append(_rows(t, name, M, n, heads.dim, kind))
+    (pq, lq), (pk, lk), (po, lo), (pko, lko) = args
+    _check(lib().dmpq_qk_norm_rope(_stream(stream), pq, lq, pk, lk, M, dtype, C.addressof(heads.struct), po, lo, pko,
+                                   lko), "dmpq_qk_norm_rope")
+
+
+def new_qk_backward_workspace(M: int, heads: QkHeads, device="cuda"):
+    """Workspace tensor for qk_norm_rope_backward (the same for every M)."""
+    import torch
+    return torch.empty(int(lib().dmpq_qk_backward_bytes(heads.dim)), dtype=torch.uint8, device=device)
+
+
+def qk_norm_rope_backward(dq, dk, q, k, heads: QkHeads, dxq, dxk, dwq=None, dbq=None, dwk=None, dbk=None, ws=None,
+                          stream=None) -> None:
+    """Gradients of qk_norm_rope: dxq, dxk of its inputs q and k from dq, dk of its
+    outputs (may be the same), and dw*, db* [dim] fp32 (None: not computed).
+    Without a norm q and k may be None."""
+    M, dtype, kind = _qk_shape(dq, dk, heads)
+    args = []
+    for t, name, n in ((dq, "dq", heads.n_q), (dk, "dk", heads.n_k), (q, "q", heads.n_q), (k, "k", heads.n_k),
+                       (dxq, "dxq", heads.n_q), (dxk, "dxk", heads.n_k)):
+        if t is None and heads.norm == NORM_NONE and name in ("q", "k"):
+            args += [None, n * heads.dim]
+        else:
+            args += _rows(t, name, M, n, heads.dim, kind)
+    for t, name in ((dwq, "dwq"), (dbq, "dbq"), (dwk, "dwk"), (dbk, "dbk")):
+        if t is not None:
+            _need_type(t, name, 4 * heads.dim, "fp32")
+    _check(lib().dmpq_qk_norm_rope_backward(
+        _stream(stream), *args[:8], M, dtype, C.addressof(heads.struct), *args[8:], _ptr(dwq), _ptr(dbq), _ptr(dwk),
+        _ptr(dbk), *_ws(ws)), "dmpq_qk_norm_rope_backward")

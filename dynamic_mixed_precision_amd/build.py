@@ -18,7 +18,9 @@ LIB_PATH = os.path.join(PKG, "libdmpq.so")
 BUILD_DIR = os.path.join(ROOT, "_build", "dmpq")
 
 SOURCES = ["api.hip", "quant.hip", "reduce.hip", "gemm_int8.hip", "gemm_nvfp4.hip", "gemm_bf16.hip",
-           "lora.hip", "adamw.hip", "selftest.hip", "noalloc.hip"]
+           "gemm_int8_linear.hip", "gemm_nvfp4_linear.hip", "gemm_bf16_linear.hip", "linear.hip", "qk.hip",
+           "lora.hip", "adamw.hip", "selftest.hip",
+           "noalloc.hip"]
 ARCH = "gfx950"
 
 # -ffp-contract=off: every fp32 expression is a sequence of single IEEE RNE

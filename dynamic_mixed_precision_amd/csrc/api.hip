@@ -704,6 +704,292 @@ dmpq_status dmpq_lora_backward(hipStream_t stream, const uint16_t *dy, const uin
     return hip_status(launch_lora_backward(stream, dy, x, t, a, b, B, N, K, dx_base, dx, da, db, ws), __func__);
 }
 
+// ---- the whole linear -------------------------------------------------------
+
+static bool float_type(int t) { return t == DMPQ_OUT_F32 || t == DMPQ_OUT_BF16; }
+
+// The heads' shape and parameters; M rows use the table.
+static dmpq_status check_heads(const char *fn, const dmpq_qk_heads *h, int64_t M, QkHeads *out) {
+    if (h->n_q < 0 || h->n_k < 0 || h->n_q > (1 << 20) || h->n_k > (1 << 20))
+        return fail(DMPQ_ERR_BAD_SHAPE, "%s: n_q = %d, n_k = %d must be 0 .. 2^20", fn, h->n_q, h->n_k);
+    if (h->dim <= 0 || h->dim % 8 != 0)
+        return fail(DMPQ_ERR_BAD_SHAPE, "%s: dim = %d must be a positive multiple of 8", fn, h->dim);
+    if (h->dim > kMaxHeadDim) return fail(DMPQ_ERR_UNSUPPORTED, "%s: dim = %d exceeds %d", fn, h->dim, kMaxHeadDim);
+    if (h->norm < DMPQ_NORM_NONE || h->norm > DMPQ_NORM_LAYER)
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: unknown norm %d", fn, h->norm);
+    if (h->layout != DMPQ_ROPE_PAIRS && h->layout != DMPQ_ROPE_HALVES)
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: unknown layout %d", fn, h->layout);
+    if (!float_type(h->w_dtype)) return fail(DMPQ_ERR_INVALID_ARG, "%s: w_dtype %d is not F32 or BF16", fn, h->w_dtype);
+    if (h->rope_pairs < 0 || 2 * (int64_t)h->rope_pairs > h->dim)
+        return fail(DMPQ_ERR_BAD_SHAPE, "%s: rope_pairs = %d must be 0 .. dim / 2", fn, h->rope_pairs);
+    if (h->layout == DMPQ_ROPE_HALVES && h->rope_pairs % 4 != 0)
+        return fail(DMPQ_ERR_UNSUPPORTED, "%s: rope_pairs = %d of halves must be a multiple of 4", fn, h->rope_pairs);
+    if (h->norm == DMPQ_NORM_NONE && (h->wq || h->bq || h->wk || h->bk))
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: weights without a norm", fn);
+    if (h->norm != DMPQ_NORM_NONE && !(h->eps >= 0.0 && h->eps <= 3.0e38))
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: eps = %g", fn, h->eps);
+    REQUIRE_PTR_NF(fn, h->wq, 0);
+    REQUIRE_PTR_NF(fn, h->bq, 0);
+    REQUIRE_PTR_NF(fn, h->wk, 0);
+    REQUIRE_PTR_NF(fn, h->bk, 0);
+    REQUIRE_PTR_NF(fn, h->table, M * h->rope_pairs);
+    *out = QkHeads{h->wq, h->bq, h->wk, h->bk, h->table, h->n_q, h->n_k, h->dim, h->rope_pairs,
+                   h->norm, h->layout, h->w_dtype == DMPQ_OUT_BF16, (float)h->eps};
+    return DMPQ_OK;
+}
+
+// The epilogue of a *_linear GEMM, after check_gemm.
+static dmpq_status check_linear(const char *fn, const dmpq_linear_epilogue *e, int64_t M, int64_t N, int64_t K,
+                                const void *y, int out_dtype, const void *ws, size_t ws_bytes, LinearEpi *out) {
+    if (!e) return fail(DMPQ_ERR_INVALID_ARG, "%s: epilogue is NULL", fn);
+    if (!float_type(out_dtype)) return fail(DMPQ_ERR_INVALID_ARG, "%s: out_dtype %d is not F32 or BF16", fn, out_dtype);
+    if (e->act < DMPQ_ACT_NONE || e->act > DMPQ_ACT_SILU)
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: unknown activation %d", fn, e->act);
+    if ((e->bias && !float_type(e->bias_dtype)) || (e->gate && !float_type(e->gate_dtype)))
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: bias_dtype %d or gate_dtype %d is not F32 or BF16", fn, e->bias_dtype,
+                    e->gate_dtype);
+    if (e->gate_rows < 0) return fail(DMPQ_ERR_BAD_SHAPE, "%s: gate_rows = %lld < 0", fn, (long long)e->gate_rows);
+    if (e->gate_rows > 0 && !e->gate) return fail(DMPQ_ERR_INVALID_ARG, "%s: gate is NULL", fn);
+    if (e->gate && !e->gate_start && e->gate_rows != 1)
+        return fail(DMPQ_ERR_BAD_SHAPE, "%s: a gate of %lld rows needs gate_start", fn, (long long)e->gate_rows);
+    if (M > INT32_MAX / 2 || e->gate_rows > INT32_MAX / 4)
+        return fail(DMPQ_ERR_UNSUPPORTED, "%s: M or gate_rows too large", fn);
+    if (e->flags & ~DMPQ_EPI_NVFP4_AMAX) return fail(DMPQ_ERR_INVALID_ARG, "%s: unknown flags %d", fn, e->flags);
+    REQUIRE_PTR_NF(fn, y, M * N);
+    REQUIRE_PTR_NF(fn, e->bias, 0);
+    REQUIRE_PTR_NF(fn, e->gate, 0);
+    REQUIRE_PTR_NF(fn, e->gate_start, 0);
+    REQUIRE_PTR_NF(fn, e->residual, 0);
+    REQUIRE_PTR_NF(fn, e->pre, 0);
+    *out = LinearEpi{};
+    out->bias = e->bias, out->gate = e->gate, out->residual = e->residual, out->gate_start = e->gate_start;
+    out->pre = e->pre, out->S = (int)e->gate_rows, out->act = e->act;
+    out->bias_bf16 = e->bias_dtype == DMPQ_OUT_BF16, out->gate_bf16 = e->gate_dtype == DMPQ_OUT_BF16;
+    if (e->heads) {
+        const dmpq_qk_heads *h = e->heads;
+        if (dmpq_status s = check_heads(fn, h, M, &out->qk)) return s;
+        if (h->dim != 32 && h->dim != 64 && h->dim != 128)
+            return fail(DMPQ_ERR_UNSUPPORTED, "%s: heads of %d (32, 64 and 128 have an epilogue)", fn, h->dim);
+        if (h->layout == DMPQ_ROPE_HALVES && h->rope_pairs % 8 != 0)
+            return fail(DMPQ_ERR_UNSUPPORTED, "%s: rope_pairs = %d of halves must be a multiple of 8", fn, h->rope_pairs);
+        if (((int64_t)h->n_q + h->n_k) * h->dim > N)
+            return fail(DMPQ_ERR_BAD_SHAPE, "%s: %d + %d heads of %d exceed N = %lld", fn, h->n_q, h->n_k, h->dim,
+                        (long long)N);
+        if (out_dtype != DMPQ_OUT_BF16 || e->act != DMPQ_ACT_NONE || e->gate || e->residual || e->flags)
+            return fail(DMPQ_ERR_UNSUPPORTED, "%s: heads go with DMPQ_OUT_BF16, bias, pre and adapters only", fn);
+    }
+    if (e->lora) {
+        const dmpq_lora_term *l = e->lora;
+        if (dmpq_status s = check_lora(fn, M, N, K, l->R, l->S, l->n_adapters, l->rank, l->scale, true, l->seg_start,
+                                       l->seg_adapter, &out->lora.batch))
+            return s;
+        REQUIRE_PTR_NF(fn, l->t, 1);
+        REQUIRE_PTR_NF(fn, l->b, l->n_adapters * N);
+        out->lora.t = l->t, out->lora.b = l->b;
+    }
+    return check_epilogue(fn, M, N, out_dtype, 3, e->flags, ws, ws_bytes);
+}
+
+// Few rows take the kernels that read each weight once, in any type: unless
+// the tiles' maxima are asked for, which those of 256 x 256 tiles leave.
+static bool few_rows(const dmpq_linear_epilogue *e, int64_t M, int64_t N) {
+    return M <= kFewRows && N <= kMaxFewWidth && !e->flags;
+}
+
+dmpq_status dmpq_gemm_bf16_linear(hipStream_t stream, const uint16_t *x, const uint16_t *w, int64_t M, int64_t N,
+                                  int64_t K, int out_dtype, void *y, const dmpq_linear_epilogue *h_epilogue, void *ws,
+                                  size_t ws_bytes) {
+    LinearEpi lin;
+    if (dmpq_status s = check_gemm(__func__, M, N, K)) return s;
+    if (dmpq_status s = check_linear(__func__, h_epilogue, M, N, K, y, out_dtype, ws, ws_bytes, &lin)) return s;
+    REQUIRE_PTR_N(x, M);
+    REQUIRE_PTR_N(w, N);
+    if (M == 0 || N == 0) return ok();
+    return hip_status(few_rows(h_epilogue, M, N)
+                          ? launch_few_bf16(stream, x, w, M, N, K, out_dtype, y, lin)
+                          : launch_gemm_bf16_linear(stream, x, w, M, N, K, out_dtype, y, h_epilogue->flags != 0,
+                                                    static_cast<float *>(ws), split_area(ws, ws_bytes, M, N), lin),
+                      __func__);
+}
+
+dmpq_status dmpq_qgemm_int8_linear(hipStream_t stream, const int8_t *qa, const float *sa, const int8_t *qw,
+                                   const float *sw, int64_t M, int64_t N, int64_t K, int out_dtype, void *y,
+                                   const dmpq_linear_epilogue *h_epilogue, void *ws, size_t ws_bytes) {
+    LinearEpi lin;
+    if (dmpq_status s = check_gemm(__func__, M, N, K)) return s;
+    if (dmpq_status s = check_linear(__func__, h_epilogue, M, N, K, y, out_dtype, ws, ws_bytes, &lin)) return s;
+    REQUIRE_PTR_N(qa, M);
+    REQUIRE_PTR_N(sa, M);
+    REQUIRE_PTR_N(qw, N);
+    REQUIRE_PTR_N(sw, N);
+    if (M == 0 || N == 0) return ok();
+    return hip_status(few_rows(h_epilogue, M, N)
+                          ? launch_few_int8(stream, qa, sa, qw, sw, M, N, K, out_dtype, y, lin)
+                          : launch_gemm_int8_linear(stream, qa, sa, qw, sw, M, N, K, out_dtype, y, h_epilogue->flags != 0,
+                                                    static_cast<float *>(ws), split_area(ws, ws_bytes, M, N), lin),
+                      __func__);
+}
+
+dmpq_status dmpq_qgemm_nvfp4_linear(hipStream_t stream, const uint8_t *ca, const uint8_t *sa, const float *d_ga,
+                                    const uint8_t *cw, const uint8_t *sw, const float *d_gw, int64_t M, int64_t N,
+                                    int64_t K, int out_dtype, void *y, const dmpq_linear_epilogue *h_epilogue, void *ws,
+                                    size_t ws_bytes) {
+    LinearEpi lin;
+    if (dmpq_status s = check_gemm(__func__, M, N, K)) return s;
+    if (dmpq_status s = check_linear(__func__, h_epilogue, M, N, K, y, out_dtype, ws, ws_bytes, &lin)) return s;
+    REQUIRE_PTR_N(ca, M);
+    REQUIRE_PTR_N(sa, M);
+    REQUIRE_PTR_N(d_ga, M * N);
+    REQUIRE_PTR_N(cw, N);
+    REQUIRE_PTR_N(sw, N);
+    REQUIRE_PTR_N(d_gw, M * N);
+    if (M == 0 || N == 0) return ok();
+    return hip_status(few_rows(h_epilogue, M, N)
+                          ? launch_few_nvfp4(stream, ca, sa, d_ga, cw, sw, d_gw, M, N, K, out_dtype, y, lin)
+                          : launch_gemm_nvfp4_linear(stream, ca, sa, d_ga, cw, sw, d_gw, M, N, K, out_dtype, y,
+                                                     h_epilogue->flags != 0, static_cast<float *>(ws),
+                                                     split_area(ws, ws_bytes, M, N), lin),
+                      __func__);
+}
+
+size_t dmpq_linear_backward_bytes(int64_t M, int64_t N, int64_t gate_rows) {
+    if (M < 0 || N < 0 || gate_rows < 0 || M > INT32_MAX / 2 || N > kMaxFewWidth || gate_rows > INT32_MAX / 4) return 0;
+    const size_t bytes = linear_grad_bytes(M, N, gate_rows);
+    return bytes == SIZE_MAX ? 0 : bytes;
+}
+
+dmpq_status dmpq_linear_epilogue_backward(hipStream_t stream, const void *dy, const void *pre, int64_t M, int64_t N,
+                                          int dtype, int act, const void *gate, int gate_dtype,
+                                          const int32_t *gate_start, int64_t gate_rows, void *du, float *dgate,
+                                          float *dbias, void *ws, size_t ws_bytes) {
+    if (M < 0 || N < 0 || gate_rows < 0)
+        return fail(DMPQ_ERR_BAD_SHAPE, "%s: M = %lld, N = %lld, gate_rows = %lld must be >= 0", __func__, (long long)M,
+                    (long long)N, (long long)gate_rows);
+    if (M > INT32_MAX / 2 || N > kMaxFewWidth || gate_rows > INT32_MAX / 4)
+        return fail(DMPQ_ERR_UNSUPPORTED, "%s: M, N or gate_rows too large", __func__);
+    if (!float_type(dtype)) return fail(DMPQ_ERR_INVALID_ARG, "%s: dtype %d is not F32 or BF16", __func__, dtype);
+    if (act < DMPQ_ACT_NONE || act > DMPQ_ACT_SILU)
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: unknown activation %d", __func__, act);
+    if (gate && !float_type(gate_dtype))
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: gate_dtype %d is not F32 or BF16", __func__, gate_dtype);
+    if ((gate_rows > 0 || dgate) && !gate) return fail(DMPQ_ERR_INVALID_ARG, "%s: gate is NULL", __func__);
+    if (gate && !gate_start && gate_rows != 1)
+        return fail(DMPQ_ERR_BAD_SHAPE, "%s: a gate of %lld rows needs gate_start", __func__, (long long)gate_rows);
+    REQUIRE_PTR_N(dy, M * N);
+    REQUIRE_PTR_N(pre, act != DMPQ_ACT_NONE || dgate ? M * N : 0);
+    REQUIRE_PTR_N(gate, 0);
+    REQUIRE_PTR_N(gate_start, 0);
+    REQUIRE_PTR_N(du, 0);
+    REQUIRE_PTR_N(dgate, 0);
+    REQUIRE_PTR_N(dbias, 0);
+    if (dgate || dbias) {
+        const size_t need = linear_grad_bytes(M, N, gate_rows);
+        if (need == SIZE_MAX) return fail(DMPQ_ERR_UNSUPPORTED, "%s: the workspace passes 64 bits", __func__);
+        if (need > 0 && !ws) return fail(DMPQ_ERR_WORKSPACE, "%s: workspace is NULL", __func__);
+        if (ws && !aligned16(ws)) return fail(DMPQ_ERR_MISALIGNED, "%s: workspace is not 16-byte aligned", __func__);
+        if (ws_bytes < need)
+            return fail(DMPQ_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", __func__, ws_bytes, need);
+    }
+    const LinearGrad G{dy, pre, gate, gate ? gate_start : nullptr, du, dgate, dbias, (int)gate_rows, act,
+                       gate_dtype == DMPQ_OUT_BF16};
+    return hip_status(launch_linear_grad(stream, G, M, N, dtype, ws), __func__);
+}
+
+// ---- the heads of q and k ---------------------------------------------------
+
+dmpq_status dmpq_rope_table(hipStream_t stream, const void *pos, int pos_dtype, const double *freq, int64_t M,
+                            int n_axes, const int32_t *h_axis_pairs, float *table) {
+    if (M < 0) return fail(DMPQ_ERR_BAD_SHAPE, "%s: M = %lld < 0", __func__, (long long)M);
+    if (n_axes < 1 || n_axes > kMaxRopeAxes)
+        return fail(DMPQ_ERR_BAD_SHAPE, "%s: n_axes = %d must be 1 .. %d", __func__, n_axes, kMaxRopeAxes);
+    if (pos_dtype != DMPQ_OUT_F32 && pos_dtype != DMPQ_OUT_I32)
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: pos_dtype %d is not F32 or I32", __func__, pos_dtype);
+    REQUIRE_HOST(h_axis_pairs);
+    RopeAxes ax{n_axes, {}};
+    int64_t P = 0;
+    for (int i = 0; i < n_axes; i++) {
+        if (h_axis_pairs[i] < 0)
+            return fail(DMPQ_ERR_BAD_SHAPE, "%s: axis %d has %d pairs", __func__, i, h_axis_pairs[i]);
+        P += h_axis_pairs[i];
+        if (P > kMaxHeadDim / 2)
+            return fail(DMPQ_ERR_UNSUPPORTED, "%s: more than %d pairs", __func__, kMaxHeadDim / 2);
+        ax.end[i] = (int)P;
+    }
+    if (M > (int64_t(1) << 50)) return fail(DMPQ_ERR_UNSUPPORTED, "%s: M too large", __func__);
+    REQUIRE_PTR_N(pos, M * P);
+    REQUIRE_PTR_N(freq, M * P);
+    REQUIRE_PTR_N(table, M * P);
+    return hip_status(launch_rope_table(stream, pos, pos_dtype == DMPQ_OUT_F32, ax, freq, M, table), __func__);
+}
+
+// A [M x n x D] tensor of rows `ld` elements apart: rows do not overlap and
+// stay 16-byte aligned.
+static dmpq_status check_rows(const char *fn, const char *what, const void *p, int64_t ld, int64_t M, int n, int D, int dtype) {
+    if ((int64_t)n * M > 0 && !p) return fail(DMPQ_ERR_INVALID_ARG, "%s: %s is NULL", fn, what);
+    if (p && !aligned16(p)) return fail(DMPQ_ERR_MISALIGNED, "%s: %s is not 16-byte aligned", fn, what);
+    if (n == 0) return DMPQ_OK;
+    if (ld < (int64_t)n * D) return fail(DMPQ_ERR_BAD_SHAPE, "%s: rows of %s are %lld apart, hold %lld", fn, what, (long long)ld,
+                                         (long long)n * D);
+    if (M > 1 && ld % (dtype == DMPQ_OUT_F32 ? 4 : 8) != 0)
+        return fail(DMPQ_ERR_MISALIGNED, "%s: rows of %s, %lld apart, are not 16-byte aligned", fn, what, (long long)ld);
+    return DMPQ_OK;
+}
+
+static dmpq_status check_qk(const char *fn, int64_t M, int dtype, const dmpq_qk_heads *h, QkHeads *out) {
+    if (M < 0) return fail(DMPQ_ERR_BAD_SHAPE, "%s: M = %lld < 0", fn, (long long)M);
+    if (M > (int64_t(1) << 40)) return fail(DMPQ_ERR_UNSUPPORTED, "%s: M too large", fn);
+    if (!float_type(dtype)) return fail(DMPQ_ERR_INVALID_ARG, "%s: dtype %d is not F32 or BF16", fn, dtype);
+    if (!h) return fail(DMPQ_ERR_INVALID_ARG, "%s: h_heads is NULL", fn);
+    return check_heads(fn, h, M, out);
+}
+
+dmpq_status dmpq_qk_norm_rope(hipStream_t stream, const void *q, int64_t ldq, const void *k, int64_t ldk, int64_t M,
+                              int dtype, const dmpq_qk_heads *h_heads, void *q_out, int64_t ldq_out, void *k_out,
+                              int64_t ldk_out) {
+    QkHeads H;
+    if (dmpq_status s = check_qk(__func__, M, dtype, h_heads, &H)) return s;
+    if (dmpq_status s = check_rows(__func__, "q", q, ldq, M, H.nq, H.D, dtype)) return s;
+    if (dmpq_status s = check_rows(__func__, "k", k, ldk, M, H.nk, H.D, dtype)) return s;
+    if (dmpq_status s = check_rows(__func__, "q_out", q_out, ldq_out, M, H.nq, H.D, dtype)) return s;
+    if (dmpq_status s = check_rows(__func__, "k_out", k_out, ldk_out, M, H.nk, H.D, dtype)) return s;
+    QkTensors T{};
+    T.q = q, T.k = k, T.q_out = q_out, T.k_out = k_out;
+    T.ldq = ldq, T.ldk = ldk, T.ldq_out = ldq_out, T.ldk_out = ldk_out;
+    return hip_status(launch_qk(stream, T, H, M, dtype, false, nullptr), __func__);
+}
+
+size_t dmpq_qk_backward_bytes(int dim) { return dim <= 0 || dim > kMaxHeadDim ? 0 : qk_grad_bytes(dim); }
+
+dmpq_status dmpq_qk_norm_rope_backward(hipStream_t stream, const void *dq, int64_t lddq, const void *dk, int64_t lddk,
+                                       const void *q, int64_t ldq, const void *k, int64_t ldk, int64_t M, int dtype,
+                                       const dmpq_qk_heads *h_heads, void *dxq, int64_t lddxq, void *dxk, int64_t lddxk,
+                                       float *dwq, float *dbq, float *dwk, float *dbk, void *ws, size_t ws_bytes) {
+    QkHeads H;
+    if (dmpq_status s = check_qk(__func__, M, dtype, h_heads, &H)) return s;
+    if (dmpq_status s = check_rows(__func__, "dq", dq, lddq, M, H.nq, H.D, dtype)) return s;
+    if (dmpq_status s = check_rows(__func__, "dk", dk, lddk, M, H.nk, H.D, dtype)) return s;
+    if (H.norm != 0) {
+        if (dmpq_status s = check_rows(__func__, "q", q, ldq, M, H.nq, H.D, dtype)) return s;
+        if (dmpq_status s = check_rows(__func__, "k", k, ldk, M, H.nk, H.D, dtype)) return s;
+    }
+    if (dmpq_status s = check_rows(__func__, "dxq", dxq, lddxq, M, H.nq, H.D, dtype)) return s;
+    if (dmpq_status s = check_rows(__func__, "dxk", dxk, lddxk, M, H.nk, H.D, dtype)) return s;
+    REQUIRE_PTR_N(dwq, 0);
+    REQUIRE_PTR_N(dbq, 0);
+    REQUIRE_PTR_N(dwk, 0);
+    REQUIRE_PTR_N(dbk, 0);
+    if (dwq || dbq || dwk || dbk) {
+        if (H.norm == 0) return fail(DMPQ_ERR_INVALID_ARG, "%s: gradients of weights without a norm", __func__);
+        const size_t need = qk_grad_bytes(H.D);
+        if (!ws) return fail(DMPQ_ERR_WORKSPACE, "%s: workspace is NULL", __func__);
+        if (!aligned16(ws)) return fail(DMPQ_ERR_MISALIGNED, "%s: workspace is not 16-byte aligned", __func__);
+        if (ws_bytes < need)
+            return fail(DMPQ_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", __func__, ws_bytes, need);
+    }
+    const QkTensors T{q, k, dxq, dxk, ldq, ldk, lddxq, lddxk, dq, dk, lddq, lddk, dwq, dbq, dwk, dbk};
+    return hip_status(launch_qk(stream, T, H, M, dtype, true, ws), __func__);
+}
+
 // ---- AdamW ------------------------------------------------------------------
 
 static int64_t adamw_chunks(const dmpq_adamw_tensor *t, int64_t n) {

@@ -6,6 +6,7 @@
 
 #include "device.hpp"
 #include "internal.hpp"
+#include "linear.hpp"
 #include "lora.hpp"
 
 namespace dmpq {
@@ -131,32 +132,57 @@ struct EpiBand {
 // layer's NVFP4 tensor-amax term, with the same fp32 butterfly order as the
 // quantizer -- is written to the tile's entry of the maxima.  kEpiLora: the
 // adapter term of the row's request is added to the fp32 value before any of
-// that, so it costs no pass over y of its own.
-enum { kEpiGelu = 1, kEpiAmax = 2, kEpiLora = 4 };
+// that, so it costs no pass over y of its own.  kEpiLinear: the whole linear's
+// epilogue (linear.hpp), whose operands are known at run time; with kEpiHeads
+// it norms and rotates the heads of q and k.
+enum { kEpiGelu = 1, kEpiAmax = 2, kEpiLora = 4, kEpiLinear = 8, kEpiHeads = 16 };
 
-// GELU(v) = v Phi(v) = (v / 2) erfc(-v / sqrt 2) in fp32.  erfc comes from
-// the Chebyshev fit published in Numerical Recipes (Press et al., section
-// 6.2, "erfcc": erfc(z) = t exp(-z^2 + P(t)), t = 1 / (1 + z/2), z >= 0, and
-// 2 - erfc(-x) for x < 0), whose fractional error is below 1.2e-7 for every
-// argument.  The fp32 evaluation adds a few ulp plus the rounding of the
-// exponent, a relative error of about v^2 * 1.2e-7 in erfc's tail.  About 20
-// VALU operations, no branches: the library erfcf costs several times that.
-__device__ __forceinline__ float gelu_f32(float v) {
-    const float x = v * -0.70710678118654752f;
-    const float z = __builtin_fabsf(x);
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, z, 1.0f));
-    float p = 0.17087277f;
-    p = __builtin_fmaf(t, p, -0.82215223f);
-    p = __builtin_fmaf(t, p, 1.48851587f);
-    p = __builtin_fmaf(t, p, -1.13520398f);
-    p = __builtin_fmaf(t, p, 0.27886807f);
-    p = __builtin_fmaf(t, p, -0.18628806f);
-    p = __builtin_fmaf(t, p, 0.09678418f);
-    p = __builtin_fmaf(t, p, 0.37409196f);
-    p = __builtin_fmaf(t, p, 1.00002368f);
-    p = __builtin_fmaf(t, p, -1.26551223f);
-    const float e = t * __builtin_amdgcn_exp2f(__builtin_fmaf(-z, z, p) * 1.44269504088896341f);
-    return 0.5f * v * (x >= 0.0f ? e : 2.0f - e);
+// The epilogue's operands as a kernel argument.  (A member type, not an
+// expression of EPI: that one would enter the kernels' names, where host and
+// device spell an unnamed enum differently.)
+template <bool LINEAR>
+struct EpiOperands {
+    typedef LoraEpi type;
+};
+template <>
+struct EpiOperands<true> {
+    typedef LinearEpi type;
+};
+template <int EPI>
+struct EpiArgOf {
+    typedef typename EpiOperands<(EPI & kEpiLinear) != 0>::type type;
+};
+template <int EPI>
+using EpiArg = typename EpiArgOf<EPI>::type;
+__device__ __forceinline__ const LoraEpi &lora_of(const LoraEpi &e) { return e; }
+__device__ __forceinline__ const LoraEpi &lora_of(const LinearEpi &e) { return e.lora; }
+
+// max |value| of the rotated 16-block whose elements 0..7 (lo) or 8..15 the
+// lane holds as bf16; the other half is its neighbour's.  Stages 1, 2, 4 in the
+// lane, stage 8 across the pair, then * 1/4: the quantizer's order.
+__device__ __forceinline__ float block16_amax(const uint4 &v, bool lo) {
+    float f[8];
+    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
+    f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
+#pragma unroll
+    for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if ((i & h) == 0) {
+                const float a = f[i], b = f[i + h];
+                f[i] = a + b;
+                f[i + h] = a - b;
+            }
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        // the partner lane's value: DPP quad_perm [1, 0, 3, 2] swaps
+        // lanes 2k and 2k+1 inside the VALU (no LDS round trip)
+        const float o = dpp_f32<0xB1>(f[i]);
+        const float w = lo ? f[i] + o : o - f[i];
+        m = fmaxf(m, __builtin_fabsf(w * 0.25f));
+    }
+    return m;
 }
 
 // Copy one wave's LDS band (ROWS x 128 values of ESIZE bytes) to y at
@@ -203,29 +229,7 @@ __device__ __forceinline__ float epi_band_to_global(const uint8_t *band, void *y
             }
         }
         if constexpr (AMAX) {
-            float f[8];
-            f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
-            f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
-#pragma unroll
-            for (int h = 1; h < 8; h <<= 1)
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    if ((i & h) == 0) {
-                        const float a = f[i], b = f[i + h];
-                        f[i] = a + b;
-                        f[i + h] = a - b;
-                    }
-            const bool lo = (chunk & 1) == 0;  // this lane holds elements 0..7 of the block
-            float m = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                // the partner lane's value: DPP quad_perm [1, 0, 3, 2] swaps
-                // lanes 2k and 2k+1 inside the VALU (no LDS round trip)
-                const float o = __int_as_float(
-                    __builtin_amdgcn_mov_dpp(__float_as_int(f[i]), 0xB1, 0xF, 0xF, false));
-                const float w = lo ? f[i] + o : o - f[i];
-                m = fmaxf(m, __builtin_fabsf(w * 0.25f));
-            }
+            const float m = block16_amax(v, (chunk & 1) == 0);
             if (row < M && col < N) amax = fmaxf(amax, m);
         }
         if (row >= M || col >= N) continue;
@@ -245,6 +249,55 @@ __device__ __forceinline__ float epi_band_to_global(const uint8_t *band, void *y
                     reinterpret_cast<uint16_t *>(dst)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
             }
         }
+    }
+    return amax;
+}
+
+// The whole linear's epilogue for one wave's fp32 LDS band (rows of
+// kLoraBandStride bytes) of ROWS rows from row0 on, in which the scaled sums (and
+// the adapter term) lie: bias, pre, heads, activation, gate, residual, one
+// rounding, store; returns the lane's part of the fused amax.  A lane has the
+// same 16 bytes of columns in every row, so what depends on the column is
+// loaded once (T, Q).
+template <int ESIZE, int EPI, int ROWS>
+__device__ __forceinline__ float linear_band_out(const uint8_t *band, void *y, int64_t M, int64_t N, int64_t row0,
+                                                 int64_t col0, int lane, bool vec, const LinearEpi &L,
+                                                 const LinearLane<16 / ESIZE> &T, const QkLane<16 / ESIZE> &Q) {
+    constexpr int PER = 16 / ESIZE, LPR = 128 / PER, RPP = 64 / LPR;
+    const int chunk = lane % LPR;
+    const int64_t col = col0 + chunk * PER;
+    float amax = 0.0f;
+    int request = 0;
+    if (T.mode == kGateMixed) {
+        const int64_t r = row0 + (lane & (ROWS - 1));
+        request = request_of(L.gate_start, L.S, (int)(r < M ? r : M - 1));
+    }
+#pragma unroll 2
+    for (int p = 0; p < ROWS / RPP; p++) {
+        const int r = p * RPP + lane / LPR;
+        const int64_t row = row0 + r;
+        const bool in = row < M && col < N;
+        float v[PER];
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(band + r * kLoraBandStride + (chunk * PER + i) * 4);
+            v[i] = a.x + T.bias[i], v[i + 1] = a.y + T.bias[i + 1];
+            v[i + 2] = a.z + T.bias[i + 2], v[i + 3] = a.w + T.bias[i + 3];
+        }
+        if (L.pre && in) store_values<ESIZE, PER>(L.pre, row * N + col, N - col, vec, v);
+        if constexpr ((EPI & kEpiHeads) != 0)
+            Q.apply(L.qk, row < M ? row : M - 1, v);
+        else
+            act_apply<PER>(v, L.act);
+        const int mine = T.mode == kGateMixed ? __shfl(request, r, 64) : 0;
+        T.template finish<ESIZE>(L, row, N, col, in, vec, mine, v);
+        if constexpr ((EPI & kEpiAmax) != 0) {
+            static_assert(ESIZE == 2, "the fused amax reads bf16 outputs");
+            const float m = block16_amax(make_uint4(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]),
+                                                    cvt_pk_bf16(v[4], v[5]), cvt_pk_bf16(v[6], v[7])), (chunk & 1) == 0);
+            if (in) amax = fmaxf(amax, m);
+        }
+        if (in) store_values<ESIZE, PER>(y, row * N + col, N - col, vec, v);
     }
     return amax;
 }
@@ -359,16 +412,63 @@ __device__ __forceinline__ void lora_epilogue(AccV (&acc)[4][4], Scale &sc, uint
     if constexpr ((EPI & kEpiAmax) != 0) epi_tile_amax(amax, wave, lane, slot);
 }
 
+// The epilogue of the whole linear: slices of 32 rows through fp32 bands, as
+// lora_epilogue (and with it, where there are adapters).  A wave's band is its
+// own, so nothing waits for other waves unless b of an adapter is staged.
+template <int OUT, int EPI, int AHEAD, class AccV, class Scale>
+__device__ __forceinline__ void linear_epilogue(AccV (&acc)[4][4], Scale &sc, uint8_t *lds, int64_t M, int64_t N,
+                                                int64_t m0, int64_t n0, int wave, int wm, int wn, int lane, void *y,
+                                                float *slot, const LinearEpi &L) {
+    constexpr int ES = OUT == 1 ? 2 : 4, PER = 16 / ES;
+    constexpr bool LORA = (EPI & kEpiLora) != 0;
+    const int lm = lane & 31, lh = lane >> 5;
+    uint8_t *band = lds + wave * kLoraBandBytes;
+    const bool vec = ((N * ES) & 15) == 0;
+    const int64_t col = n0 + wn * 128 + (lane % (128 / PER)) * PER;
+    LinearLane<PER> T;
+    T.begin(L, m0 + wm * 128, 128, M, N, col);
+    QkLane<PER> Q;
+    if constexpr ((EPI & kEpiHeads) != 0) Q.begin(L.qk, col);
+    LoraRows<LORA ? AHEAD : 1> t;
+    LoraTile A;
+    if constexpr (LORA) A = lora_tile_begin(L.lora, m0, n0, N, lds, lds + kLoraMetaOff, t);
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        sc.row(m0 + wm * 128 + i * 32 + lm);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int g = 0; g < 4; g++)
+                *reinterpret_cast<float4 *>(band + lm * kLoraBandStride + (j * 32 + 8 * g + 4 * lh) * 4) = make_float4(
+                    sc((float)acc[i][j][4 * g], j, g, 0), sc((float)acc[i][j][4 * g + 1], j, g, 1),
+                    sc((float)acc[i][j][4 * g + 2], j, g, 2), sc((float)acc[i][j][4 * g + 3], j, g, 3));
+        if constexpr (LORA) {
+            LoraRows<AHEAD> next;
+            if (i < 3) A.load_t(L.lora, i + 1, next);
+            lora_band_add<AHEAD>(L.lora, A, i, n0, N, lds, t);
+            if (i < 3) t = next;
+        }
+        amax = fmaxf(amax, linear_band_out<ES, EPI, 32>(band, y, M, N, m0 + wm * 128 + i * 32, n0 + wn * 128, lane, vec,
+                                                        L, T, Q));
+        __builtin_amdgcn_sched_barrier(0);  // one slice at a time: its accumulators are free now
+    }
+    if constexpr ((EPI & kEpiAmax) != 0) epi_tile_amax(amax, wave, lane, slot);
+}
+
 // fp32 accumulators -> y = (acc * gA) * gW (fp32 or bf16).  slot: the tile's
 // entry of the fused-amax maxima (used with kEpiAmax only).
 template <int OUT, int EPI = 0>
 __device__ __forceinline__ void f32_band_epilogue(v16f (&acc)[4][4], uint8_t *lds, float gA,
                                                   float gW, int64_t M, int64_t N, int64_t m0,
                                                   int64_t n0, int wave, int wm, int wn, int lane,
-                                                  void *y, float *slot, const LoraEpi &lora) {
-    if constexpr ((EPI & kEpiLora) != 0) {
+                                                  void *y, float *slot, const EpiArg<EPI> &ep) {
+    if constexpr ((EPI & kEpiLinear) != 0) {
         EpiScaleF32 sc{gA, gW};
-        lora_epilogue<OUT, EPI, 3>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot, lora);
+        linear_epilogue<OUT, EPI, 3>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot, ep);
+    } else if constexpr ((EPI & kEpiLora) != 0) {
+        EpiScaleF32 sc{gA, gW};
+        lora_epilogue<OUT, EPI, 3>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot, ep);
     } else {
         EpiScaleF32 sc{gA, gW};
         band_epilogue<OUT, EPI>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot);
@@ -388,14 +488,20 @@ __device__ __forceinline__ void f32_band_epilogue(v16f (&acc)[4][4], uint8_t *ld
 // atomic max (the split kernel zeroed it; the maximum does not depend on the
 // order).
 constexpr int kFixupRows = 32;
+// its LDS: a band of outputs, or of fp32 values where the whole linear's
+// epilogue reads it
+template <int OUT, int EPI>
+constexpr size_t fixup_lds() {
+    return (size_t)kFixupRows * ((EPI & kEpiLinear) != 0 ? kLoraBandStride : EpiBand<OUT == 1 ? 2 : 4>::STRIDE);
+}
 
 template <int OUT, int EPI, class T, int S, class Scale>
 __device__ __forceinline__ void split_fixup_epilogue(const uint32_t *part, Scale &sc, uint8_t *lds,
                                                      int64_t M, int64_t N, int64_t m0, int64_t n0,
                                                      int wave, int i, int lane, void *y, float *slot,
-                                                     const LoraEpi &lora) {
+                                                     const EpiArg<EPI> &ep) {
     constexpr int ES = OUT == 1 ? 2 : 4;
-    constexpr bool LORA = (EPI & kEpiLora) != 0;
+    constexpr bool LORA = (EPI & kEpiLora) != 0, LINEAR = (EPI & kEpiLinear) != 0;
     using Band = EpiBand<ES>;
     constexpr size_t kPieces = kSplitWords / 4;
     const uint4 *p4 = reinterpret_cast<const uint4 *>(part);
@@ -405,7 +511,7 @@ __device__ __forceinline__ void split_fixup_epilogue(const uint32_t *part, Scale
     const bool vec = ((N * ES) & 15) == 0;
     sc.row(m0 + wm * 128 + i * 32 + lm);
     v16f add[4];
-    if constexpr (LORA) lora_slice(lora, m0 + wm * 128 + i * 32 + lm, n0 + wn * 128, N, lane, add);
+    if constexpr (LORA) lora_slice(lora_of(ep), m0 + wm * 128 + i * 32 + lm, n0 + wn * 128, N, lane, add);
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         uint4 v[S][4];
@@ -430,8 +536,9 @@ __device__ __forceinline__ void split_fixup_epilogue(const uint32_t *part, Scale
                 v4[e] = sc((float)x[e], j, g, e);
                 if constexpr (LORA) v4[e] += add[j][4 * g + e];
             }
-            uint8_t *dst = band + lm * Band::STRIDE + (j * 32 + 8 * g + 4 * lh) * ES;
-            if constexpr (OUT == 0)
+            constexpr int STRIDE = LINEAR ? kLoraBandStride : Band::STRIDE, BES = LINEAR ? 4 : ES;
+            uint8_t *dst = band + lm * STRIDE + (j * 32 + 8 * g + 4 * lh) * BES;
+            if constexpr (OUT == 0 || LINEAR)
                 *reinterpret_cast<float4 *>(dst) = make_float4(v4[0], v4[1], v4[2], v4[3]);
             else
                 *reinterpret_cast<uint2 *>(dst) = make_uint2(cvt_pk_bf16(v4[0], v4[1]), cvt_pk_bf16(v4[2], v4[3]));
@@ -439,13 +546,34 @@ __device__ __forceinline__ void split_fixup_epilogue(const uint32_t *part, Scale
         // bound the loads in flight (one block's, two for few splits)
         if (S > 4 || (j & 1)) __builtin_amdgcn_sched_barrier(0);
     }
-    float amax = epi_band_to_global<ES, EPI, kFixupRows>(band, y, M, N, m0 + wm * 128 + i * 32,
-                                                         n0 + wn * 128, lane, vec);
+    float amax;
+    if constexpr (LINEAR) {
+        constexpr int PER = 16 / ES;
+        const int64_t row0 = m0 + wm * 128 + i * 32, col = n0 + wn * 128 + (lane % (128 / PER)) * PER;
+        LinearLane<PER> cols;
+        cols.begin(ep, row0, kFixupRows, M, N, col);
+        QkLane<PER> Q;
+        if constexpr ((EPI & kEpiHeads) != 0) Q.begin(ep.qk, col);
+        amax = linear_band_out<ES, EPI, kFixupRows>(band, y, M, N, row0, n0 + wn * 128, lane, vec, ep, cols, Q);
+    } else {
+        amax = epi_band_to_global<ES, EPI, kFixupRows>(band, y, M, N, m0 + wm * 128 + i * 32, n0 + wn * 128, lane, vec);
+    }
     if constexpr ((EPI & kEpiAmax) != 0) {
         // non-negative floats order as their bit patterns
         amax = wave_max(amax);
         if (lane == 0) atomicMax(reinterpret_cast<unsigned *>(slot), __float_as_uint(amax));
     }
+}
+
+// Host: the fixup launch of a form (fp32 accumulators).
+template <int OUT, int EPI>
+inline hipError_t launch_fixup_of(hipStream_t s, const float *ga, const float *gw, int64_t M, int64_t N, void *y,
+                                  unsigned tiles_m, unsigned tiles_n, unsigned group_m, float *partial,
+                                  const SplitPlan &sp, const uint32_t *spart, const EpiArg<EPI> &ep) {
+    if constexpr ((EPI & kEpiLinear) != 0)
+        return launch_f32_fixup_linear(s, ga, gw, M, N, y, tiles_m, tiles_n, group_m, partial, sp, spart, OUT, EPI, ep);
+    else
+        return launch_f32_fixup(s, ga, gw, M, N, y, tiles_m, tiles_n, group_m, partial, sp, spart, OUT, EPI, &ep);
 }
 
 }  // namespace dmpq

@@ -105,6 +105,28 @@ struct LoraEpi {
     LoraBatch batch;
 };
 
+// ---- the whole linear (linear.hpp) -------------------------------------------
+// The heads of q and k: nq heads of D columns, then nk; norm 0 none, 1 root
+// mean square, 2 layer norm; P rotated pairs a head, layout 0 (2i, 2i + 1), 1
+// (i, i + P); table [rows x P] of (cos, sin).
+struct QkHeads {
+    const void *wq, *bq, *wk, *bk;
+    const float *table;
+    int nq, nk, D, P, norm, layout, w_bf16;
+    float eps;
+};
+constexpr int kMaxHeadDim = 256;
+// The epilogue's operands, any of them NULL; gate_start NULL: the gate has one
+// row, for all.  lora.t NULL: no adapters; qk.D 0: no heads.
+struct LinearEpi {
+    const void *bias, *gate, *residual;
+    const int32_t *gate_start;
+    void *pre;
+    int S, act, bias_bf16, gate_bf16;
+    QkHeads qk;
+    LoraEpi lora;
+};
+
 // epi: bit 0 GELU, bit 1 fused NVFP4 amax of the output into partial[tile]
 // (bf16 output only); the GEMM tile is 256 x 256 on every path.  spart: the
 // split area (kSplitAreaBytes), or NULL to run every tile whole.  lora: the
@@ -112,6 +134,10 @@ struct LoraEpi {
 hipError_t launch_gemm_int8(hipStream_t s, const int8_t *qa, const float *sa, const int8_t *qw,
                             const float *sw, int64_t M, int64_t N, int64_t K, int out_dtype,
                             void *y, int epi, float *partial, uint32_t *spart, const LoraEpi *lora = nullptr);
+// The same with a whole linear's epilogue; amax: partial is written.
+hipError_t launch_gemm_int8_linear(hipStream_t s, const int8_t *qa, const float *sa, const int8_t *qw,
+                                   const float *sw, int64_t M, int64_t N, int64_t K, int out_dtype, void *y,
+                                   bool amax, float *partial, uint32_t *spart, const LinearEpi &lin);
 // The INT8 GEMM against an NVFP4 weight (cw, sw, gw) converted to INT8 in
 // the weight-tile load with the row scales of launch_w8_row_scales; the
 // same result as launch_gemm_int8 on the converted weight.  K % 128 == 0;
@@ -123,12 +149,19 @@ hipError_t launch_gemm_int8_w4(hipStream_t s, const int8_t *qa, const float *sa,
 hipError_t launch_gemm_bf16(hipStream_t s, const uint16_t *x, const uint16_t *w, int64_t M,
                             int64_t N, int64_t K, int out_dtype, void *y, int epi, float *partial,
                             uint32_t *spart, const LoraEpi *lora = nullptr);
+hipError_t launch_gemm_bf16_linear(hipStream_t s, const uint16_t *x, const uint16_t *w, int64_t M, int64_t N,
+                                   int64_t K, int out_dtype, void *y, bool amax, float *partial, uint32_t *spart,
+                                   const LinearEpi &lin);
 // Fixup of a split launch with fp32 accumulators: y = (sum * gA) * gW (gA, gW
 // read from device memory; NULL reads as 1).
 hipError_t launch_f32_fixup(hipStream_t s, const float *ga, const float *gw, int64_t M, int64_t N,
                             void *y, unsigned tiles_m, unsigned tiles_n, unsigned group_m,
                             float *partial, const SplitPlan &sp, const uint32_t *spart,
                             int out_dtype, int epi, const LoraEpi *lora);
+hipError_t launch_f32_fixup_linear(hipStream_t s, const float *ga, const float *gw, int64_t M, int64_t N,
+                                   void *y, unsigned tiles_m, unsigned tiles_n, unsigned group_m,
+                                   float *partial, const SplitPlan &sp, const uint32_t *spart,
+                                   int out_dtype, int epi, const LinearEpi &lin);
 hipError_t launch_outlier_count(hipStream_t s, const uint16_t *x, int64_t M, int64_t K,
                                 double kappa, double *count, const Workspace &ws);
 // Sum ns values per partial over nparts partials, in a fixed order, into out[ns].
@@ -139,6 +172,53 @@ hipError_t launch_gemm_nvfp4(hipStream_t s, const uint8_t *ca, const uint8_t *sa
                              const float *gw, int64_t M, int64_t N, int64_t K, int out_dtype,
                              void *y, int variant, int epi, float *partial, uint32_t *spart,
                              const LoraEpi *lora = nullptr);
+hipError_t launch_gemm_nvfp4_linear(hipStream_t s, const uint8_t *ca, const uint8_t *sa, const float *ga,
+                                    const uint8_t *cw, const uint8_t *sw, const float *gw, int64_t M, int64_t N,
+                                    int64_t K, int out_dtype, void *y, bool amax, float *partial,
+                                    uint32_t *spart, const LinearEpi &lin);
+
+// ---- the whole linear: few rows, gradients; the heads of q and k ---------------
+// Rows up to which the whole linear takes the kernels that read each weight
+// once per 16 to 64 rows (linear.hip).
+constexpr int64_t kFewRows = 64;
+constexpr int64_t kMaxFewWidth = int64_t(1) << 26;
+hipError_t launch_few_bf16(hipStream_t s, const uint16_t *x, const uint16_t *w, int64_t M, int64_t N, int64_t K,
+                           int out_dtype, void *y, const LinearEpi &L);
+hipError_t launch_few_int8(hipStream_t s, const int8_t *qa, const float *sa, const int8_t *qw, const float *sw, int64_t M,
+                           int64_t N, int64_t K, int out_dtype, void *y, const LinearEpi &L);
+hipError_t launch_few_nvfp4(hipStream_t s, const uint8_t *ca, const uint8_t *sa, const float *ga, const uint8_t *cw,
+                            const uint8_t *sw, const float *gw, int64_t M, int64_t N, int64_t K, int out_dtype, void *y,
+                            const LinearEpi &L);
+// du, dgate and dbias may be NULL, pre where neither act nor dgate needs it;
+// gate_start NULL: one row of the gate for all.
+struct LinearGrad {
+    const void *dy, *pre, *gate;
+    const int32_t *gate_start;
+    void *du;
+    float *dgate, *dbias;
+    int S, act, gate_bf16;
+};
+size_t linear_grad_bytes(int64_t M, int64_t N, int64_t S);  // SIZE_MAX: more than 4e18
+hipError_t launch_linear_grad(hipStream_t s, const LinearGrad &G, int64_t M, int64_t N, int dtype, void *ws);
+
+constexpr int kMaxRopeAxes = 8;
+struct RopeAxes {
+    int n;
+    int end[kMaxRopeAxes];  // pairs of the axes so far
+};
+hipError_t launch_rope_table(hipStream_t s, const void *pos, bool pos_f32, const RopeAxes &ax, const double *freq, int64_t M,
+                             float *table);
+// Rows of heads (strides in elements); dq, dk and what follows: gradients only.
+struct QkTensors {
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t ldq, ldk, ldq_out, ldk_out;
+    const void *dq, *dk;
+    int64_t lddq, lddk;
+    float *dwq, *dbq, *dwk, *dbk;
+};
+size_t qk_grad_bytes(int D);
+hipError_t launch_qk(hipStream_t s, const QkTensors &T, const QkHeads &H, int64_t M, int dtype, bool grad, void *ws);
 
 // ---- low-rank adapters: launchers ------------------------------------------
 // t = x a^T by request (fp32, [M x R])

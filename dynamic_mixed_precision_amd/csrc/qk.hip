@@ -1,0 +1,430 @@
+// qk.hip -- the heads of q and k between the QKV linear and attention: the
+// table of rotations of positions with several axes, the per-head norm with the
+// rotation in one pass, and that pass's gradients.
+//
+// Norm of a head x of D values (RMS: m = 0):
+//   n = (x - m) / sqrt(mean((x - m)^2) + eps),  y = n w + b,  m = mean(x)
+// Rotation of pair p by the angle a of its row and axis:
+//   (lo, hi) -> (lo cos a - hi sin a, hi cos a + lo sin a)
+// All in fp32, one rounding at the end.  Both passes read and write each head
+// once and are bound by HBM.  A lane holds 8 values of a head, so that a head
+// of 64 is 8 lanes and one wave takes 8 heads of a row in a step; their
+// rotations are the same for every head of the row and stay in registers.
+#include "device.hpp"
+#include "internal.hpp"
+#include "linear.hpp"
+
+namespace dmpq {
+
+// ---- rotations -----------------------------------------------------------------
+
+// (cos, sin) of pos[m, axis(p)] * freq[p].  The angle is made in 64 bits, as
+// turns: its distance to the nearest quarter turn keeps all of fp32's bits
+// however far the position is.  32 pairs of a long video (106306 rows): 27 MB
+// written.
+__global__ __launch_bounds__(256) void rope_table_kernel(const void *__restrict__ pos, int pos_f32, RopeAxes ax,
+                                                         const double *__restrict__ freq, int64_t M, int P,
+                                                         float2 *__restrict__ table) {
+    const int64_t total = M * P, per = 1024;
+    for (int64_t base = (int64_t)blockIdx.x * per; base < total; base += (int64_t)gridDim.x * per) {
+        const int64_t m0 = base / P;
+        const unsigned p0 = (unsigned)(base - m0 * P);
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const unsigned o = p0 + 256 * k + threadIdx.x;
+            const int64_t m = m0 + o / (unsigned)P;
+            const int p = (int)(o % (unsigned)P);
+            if (m >= M) continue;
+            int a = 0;
+#pragma unroll
+            for (int i = 0; i < kMaxRopeAxes - 1; i++) a += i < ax.n - 1 && p >= ax.end[i];
+            const double at = pos_f32 ? (double)static_cast<const float *>(pos)[m * ax.n + a]
+                                      : (double)static_cast<const int32_t *>(pos)[m * ax.n + a];
+            const double turns = at * freq[p] * 0.15915494309189533577;
+            const double quarter = __builtin_rint(4.0 * turns);
+            const float r = (float)(turns - 0.25 * quarter);
+            float s, c;
+            sincospif(2.0f * r, &s, &c);
+            // which quarter: by a remainder in 64 bits, as it may pass 2^31
+            const int q = (int)(quarter - 4.0 * __builtin_floor(0.25 * quarter));
+            const float cs = q & 1 ? s : c, sn = q & 1 ? c : s;
+            table[m * P + p] = make_float2(q == 1 || q == 2 ? -cs : cs, q >= 2 ? -sn : sn);
+        }
+    }
+}
+
+hipError_t launch_rope_table(hipStream_t s, const void *pos, bool pos_f32, const RopeAxes &ax, const double *freq, int64_t M,
+                             float *table) {
+    const int P = ax.end[ax.n - 1];
+    if (M == 0 || P == 0) return hipSuccess;
+    hipLaunchKernelGGL(rope_table_kernel, dim3(stride_grid(M * P, 1024, 1u << 16)), dim3(256), 0, s, pos, pos_f32 ? 1 : 0, ax,
+                       freq, M, P, reinterpret_cast<float2 *>(table));
+    return hipGetLastError();
+}
+
+// ---- the heads -----------------------------------------------------------------
+
+// A lane's 8 values of a head: two runs of four, so that both members of its
+// four pairs 4 sub .. 4 sub + 3 are the lane's own.  Neighbours (2p, 2p + 1) lie
+// in one run of 8; halves (p, p + P) in one of 4 in either half, and what is
+// behind 2P in runs of 8 again.
+template <int LAYOUT>
+struct Lane8 {
+    int a, b;   // where the runs begin
+    bool live;  // the lane has a part of the head
+    __device__ __forceinline__ Lane8(const QkHeads &H, int sub) {
+        live = 8 * sub < H.D;
+        a = 8 * sub, b = a + 4;
+        if (LAYOUT == 1 && 4 * sub < H.P) a = 4 * sub, b = H.P + a;
+        if (!live) a = 0, b = 4;
+    }
+    // the two members of pair i in the lane's 8 values
+    __device__ static __forceinline__ int lo(int i) { return LAYOUT == 0 ? 2 * i : i; }
+    __device__ static __forceinline__ int hi(int i) { return LAYOUT == 0 ? 2 * i + 1 : i + 4; }
+    template <int ES>
+    __device__ __forceinline__ void load(const void *p, int64_t at, float (&v)[8]) const {
+        if constexpr (ES == 2 && LAYOUT == 0) {
+            fetch_values<2, 8>(p, at + a, 8, true, v);
+        } else {
+            float u[4], w[4];
+            fetch_values<ES, 4>(p, at + a, 4, true, u);
+            fetch_values<ES, 4>(p, at + b, 4, true, w);
+#pragma unroll
+            for (int i = 0; i < 4; i++) v[i] = u[i], v[4 + i] = w[i];
+        }
+    }
+    template <int ES>
+    __device__ __forceinline__ void store(void *p, int64_t at, const float (&v)[8]) const {
+        if constexpr (ES == 2 && LAYOUT == 0) {
+            store_values<2, 8>(p, at + a, 8, true, v);
+        } else {
+            float u[4], w[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) u[i] = v[i], w[i] = v[4 + i];
+            store_values<ES, 4>(p, at + a, 4, true, u);
+            store_values<ES, 4>(p, at + b, 4, true, w);
+        }
+    }
+    __device__ __forceinline__ void weights(const void *p, bool bf16, float other, float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = other;
+        if (!p) return;
+        float u[4], w[4];
+        load_values<4>(p, bf16, a, 4, u);
+        load_values<4>(p, bf16, b, 4, w);
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = u[i], v[4 + i] = w[i];
+    }
+};
+
+// The sum over the G lanes of a head (a power of two), in each of them.
+template <int G>
+__device__ __forceinline__ float head_sum(float v) {
+    if (G >= 2) v += dpp_f32<0xB1>(v);
+    if (G >= 4) v += dpp_f32<0x4E>(v);
+    if (G >= 8) v += dpp_f32<0x141>(v);
+    if (G >= 16) v += dpp_f32<0x140>(v);
+    if (G >= 32) v += __shfl_xor(v, 16, 64);
+    return v;
+}
+
+// The rotations of the lane's four pairs in row m.
+struct Turns {
+    float c[4], s[4];
+    bool on[4];
+    __device__ __forceinline__ void load(const QkHeads &H, int64_t m, int sub) {
+        const float2 *t = reinterpret_cast<const float2 *>(H.table) + m * H.P;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int p = 4 * sub + i;
+            on[i] = p < H.P;
+            const float2 z = on[i] ? t[p] : make_float2(1.0f, 0.0f);
+            c[i] = z.x, s[i] = z.y;
+        }
+    }
+    // values that are not rotated stay as they are (not times 1 plus times 0)
+    template <int LAYOUT, bool BACK>
+    __device__ __forceinline__ void apply(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float lo = v[Lane8<LAYOUT>::lo(i)], hi = v[Lane8<LAYOUT>::hi(i)], sn = BACK ? -s[i] : s[i];
+            v[Lane8<LAYOUT>::lo(i)] = on[i] ? lo * c[i] - hi * sn : lo;
+            v[Lane8<LAYOUT>::hi(i)] = on[i] ? hi * c[i] + lo * sn : hi;
+        }
+    }
+};
+
+// n = the normed values; returns the factor 1 / sqrt(...).
+template <int G>
+__device__ __forceinline__ float norm8(const QkHeads &H, bool live, const float (&x)[8], float (&n)[8]) {
+    const float inv = 1.0f / (float)H.D;
+#pragma unroll
+    for (int i = 0; i < 8; i++) n[i] = x[i];
+    if (H.norm == 2) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) s += n[i];
+        s = head_sum<G>(live ? s : 0.0f) * inv;
+#pragma unroll
+        for (int i = 0; i < 8; i++) n[i] -= s;
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) s = __builtin_fmaf(n[i], n[i], s);
+    s = head_sum<G>(live ? s : 0.0f);
+    const float r = rsqrt_f32(__builtin_fmaf(s, inv, H.eps));
+#pragma unroll
+    for (int i = 0; i < 8; i++) n[i] *= r;
+    return r;
+}
+
+// The steps of a row: 64 / G heads of q each, then of k.  A wave takes `per`
+// consecutive steps of one row.
+template <int ES, int LAYOUT, int G>
+__global__ __launch_bounds__(256) void qk_kernel(QkTensors T, QkHeads H, int64_t M, int sq, int steps, int per,
+                                                 int64_t units, int parts) {
+    constexpr int HEADS = 64 / G, DEEP = 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
+    if (unit >= units) return;
+    const int64_t m = unit / parts;
+    const int first = (int)(unit - m * parts) * per, last = first + per < steps ? first + per : steps;
+    const int sub = lane % G, slot = lane / G;
+    const Lane8<LAYOUT> L(H, sub);
+    Turns t;
+    t.load(H, m, sub);
+    for (int side = 0; side < 2; side++) {  // q, then k: one set of weights at a time
+        const int s0 = side ? (first > sq ? first : sq) : first, s1 = side ? last : (last < sq ? last : sq);
+        if (s0 >= s1) continue;
+        const void *x = side ? T.k : T.q;
+        void *y = side ? T.k_out : T.q_out;
+        const int64_t at = m * (side ? T.ldk : T.ldq), to = m * (side ? T.ldk_out : T.ldq_out);
+        const int heads = side ? H.nk : H.nq, base = side ? sq : 0;
+        float w[8], b[8];
+        L.weights(side ? H.wk : H.wq, H.w_bf16, 1.0f, w);
+        L.weights(side ? H.bk : H.bq, H.w_bf16, 0.0f, b);
+        for (int st = s0; st < s1; st += DEEP) {
+            float v[DEEP][8];
+            int64_t h[DEEP];
+            bool on[DEEP];
+#pragma unroll
+            for (int d = 0; d < DEEP; d++) {
+                const int head = (st + d - base) * HEADS + slot;
+                on[d] = L.live && st + d < s1 && head < heads;
+                h[d] = (int64_t)head * H.D;
+                if (on[d]) {
+                    L.template load<ES>(x, at + h[d], v[d]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) v[d][i] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < DEEP; d++) {
+                if (st + d >= s1) break;
+                if (H.norm != 0) {
+                    float n[8];
+                    norm8<G>(H, L.live, v[d], n);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) v[d][i] = __builtin_fmaf(n[i], w[i], b[i]);
+                }
+                t.apply<LAYOUT, false>(v[d]);
+                if (on[d]) L.template store<ES>(y, to + h[d], v[d]);
+            }
+        }
+    }
+}
+
+// The gradients.  With g' = the rotation's transpose of g, h = g' w, r = the norm's factor:
+//   dx = r (h - mean(h) - n mean(h n))   (RMS: without mean(h));  dw += g' n;  db += g'
+// The weights' sums stay in registers over all a wave's rows, and each
+// workgroup stores its own; a second kernel adds them in order.
+constexpr int kQkGroups = 1024;
+
+template <int ES, int LAYOUT, int G>
+__global__ __launch_bounds__(256) void qk_grad_kernel(QkTensors T, QkHeads H, int64_t M, int sq, int steps, int per,
+                                                      int64_t units, int parts, float *__restrict__ part) {
+    constexpr int HEADS = 64 / G, DEEP = 2;
+    __shared__ float red[4][4][kMaxHeadDim];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int sub = lane % G, slot = lane / G;
+    const Lane8<LAYOUT> L(H, sub);
+    float w[2][8], dw[2][8], db[2][8];
+    L.weights(H.wq, H.w_bf16, 1.0f, w[0]);
+    L.weights(H.wk, H.w_bf16, 1.0f, w[1]);
+#pragma unroll
+    for (int i = 0; i < 8; i++) dw[0][i] = dw[1][i] = db[0][i] = db[1][i] = 0.0f;
+    const float inv = 1.0f / (float)H.D;
+    for (int64_t unit = (int64_t)blockIdx.x * 4 + wave; unit < units; unit += (int64_t)gridDim.x * 4) {
+        const int64_t m = unit / parts;
+        const int first = (int)(unit - m * parts) * per, last = first + per < steps ? first + per : steps;
+        Turns t;
+        t.load(H, m, sub);
+#pragma unroll
+        for (int side = 0; side < 2; side++) {
+            const int s0 = side ? (first > sq ? first : sq) : first, s1 = side ? last : (last < sq ? last : sq);
+            const void *x = side ? T.k : T.q, *g = side ? T.dk : T.dq;
+            void *y = side ? T.k_out : T.q_out;
+            const int64_t at = m * (side ? T.ldk : T.ldq), gat = m * (side ? T.lddk : T.lddq),
+                          to = m * (side ? T.ldk_out : T.ldq_out);
+            const int heads = side ? H.nk : H.nq, base = side ? sq : 0;
+            for (int st = s0; st < s1; st += DEEP) {
+                float v[DEEP][8], e[DEEP][8];
+                int64_t h[DEEP];
+                bool on[DEEP];
+#pragma unroll
+                for (int d = 0; d < DEEP; d++) {
+                    const int head = (st + d - base) * HEADS + slot;
+                    on[d] = L.live && st + d < s1 && head < heads;
+                    h[d] = (int64_t)head * H.D;
+#pragma unroll
+                    for (int i = 0; i < 8; i++) v[d][i] = e[d][i] = 0.0f;
+                    if (on[d]) {
+                        L.template load<ES>(g, gat + h[d], e[d]);
+                        if (H.norm != 0) L.template load<ES>(x, at + h[d], v[d]);
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < DEEP; d++) {
+                    if (st + d >= s1) break;
+                    t.apply<LAYOUT, true>(e[d]);
+                    if (H.norm != 0) {
+                        float n[8], k[8];
+                        const float r = norm8<G>(H, L.live, v[d], n);
+                        float mh = 0.0f, mn = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            if (on[d]) {  // (a head that is not there has n = 0 r, which eps 0 makes NaN)
+                                dw[side][i] = __builtin_fmaf(e[d][i], n[i], dw[side][i]);
+                                db[side][i] += e[d][i];
+                            }
+                            k[i] = e[d][i] * w[side][i];
+                            mh += k[i];
+                            mn = __builtin_fmaf(k[i], n[i], mn);
+                        }
+                        mn = head_sum<G>(L.live ? mn : 0.0f) * inv;
+                        mh = H.norm == 2 ? head_sum<G>(L.live ? mh : 0.0f) * inv : 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 8; i++) e[d][i] = r * (k[i] - mh - n[i] * mn);
+                    }
+                    if (on[d]) L.template store<ES>(y, to + h[d], e[d]);
+                }
+            }
+        }
+    }
+    if (!part) return;
+    // over the wave's heads, then the workgroup's waves
+#pragma unroll
+    for (int side = 0; side < 2; side++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            float a = dw[side][i], b = db[side][i];
+#pragma unroll
+            for (int o = G; o < 64; o <<= 1) {
+                a += __shfl_xor(a, o, 64);
+                b += __shfl_xor(b, o, 64);
+            }
+            if (slot == 0 && L.live) {
+                const int c = i < 4 ? L.a + i : L.b + i - 4;
+                red[wave][2 * side][c] = a;
+                red[wave][2 * side + 1][c] = b;
+            }
+        }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 4 * H.D; e += 256) {
+        const int k = e / H.D, c = e - k * H.D;
+        part[(int64_t)blockIdx.x * 4 * H.D + e] = ((red[0][k][c] + red[1][k][c]) + red[2][k][c]) + red[3][k][c];
+    }
+}
+
+// dwq, dbq, dwk, dbk [D] from the workgroups' sums: 16 columns and 16 parts of
+// the workgroups a workgroup.
+__global__ __launch_bounds__(256) void qk_grad_sums_kernel(const float *__restrict__ part, int groups, int D, float *dwq,
+                                                           float *dbq, float *dwk, float *dbk) {
+    __shared__ float red[16][16];
+    const int x = threadIdx.x & 15, k = threadIdx.x >> 4, e = blockIdx.x * 16 + x;
+    float sum = 0.0f;
+    if (e < 4 * D)
+#pragma unroll 8
+        for (int g = k; g < groups; g += 16) sum += part[(int64_t)g * 4 * D + e];
+    red[k][x] = sum;
+    __syncthreads();
+    if (k == 0 && e < 4 * D) {
+#pragma unroll
+        for (int i = 1; i < 16; i++) sum += red[i][x];
+        const int which = e / D, c = e - which * D;
+        float *out = which == 0 ? dwq : which == 1 ? dbq : which == 2 ? dwk : dbk;
+        if (out) out[c] = sum;
+    }
+}
+
+// How the rows' steps are dealt to waves: whole rows where there are enough of
+// them to fill the chip, parts of rows otherwise.
+struct QkPlan {
+    int sq, steps, per, parts;
+    int64_t units;
+};
+static QkPlan qk_plan(const QkHeads &H, int64_t M, int heads_per_step, int64_t waves) {
+    QkPlan p;
+    p.sq = (H.nq + heads_per_step - 1) / heads_per_step;
+    p.steps = p.sq + (H.nk + heads_per_step - 1) / heads_per_step;
+    int64_t per = (M * p.steps + waves - 1) / waves;
+    if (per > p.steps) per = p.steps;
+    p.per = (int)(per < 1 ? 1 : per);
+    p.parts = p.steps ? (p.steps + p.per - 1) / p.per : 0;
+    p.units = M * p.parts;
+    return p;
+}
+
+template <int ES, int LAYOUT, int G>
+static hipError_t launch_qk_one(hipStream_t s, const QkTensors &T, const QkHeads &H, int64_t M, bool grad, float *part) {
+    const QkPlan p = qk_plan(H, M, 64 / G, 8192);
+    if (!grad) {
+        const int64_t groups = (p.units + 3) / 4;
+        for (int64_t g = 0; g < groups; g += kMaxGroups) {  // long batches take several launches
+            const int64_t n = groups - g < kMaxGroups ? groups - g : kMaxGroups;
+            // a launch's first unit is the first of a row
+            QkTensors t = T;
+            QkHeads h = H;
+            const int64_t rows = g * 4 / p.parts, es = ES;
+            t.q = static_cast<const uint8_t *>(T.q) + rows * T.ldq * es;
+            t.k = static_cast<const uint8_t *>(T.k) + rows * T.ldk * es;
+            t.q_out = static_cast<uint8_t *>(T.q_out) + rows * T.ldq_out * es;
+            t.k_out = static_cast<uint8_t *>(T.k_out) + rows * T.ldk_out * es;
+            h.table = H.table + rows * H.P * 2;
+            hipLaunchKernelGGL((qk_kernel<ES, LAYOUT, G>), dim3((unsigned)n), dim3(256), 0, s, t, h, M, p.sq, p.steps, p.per,
+                               p.units - g * 4, p.parts);
+        }
+        return hipGetLastError();
+    }
+    const unsigned groups = stride_grid(p.units, 4, kQkGroups);
+    hipLaunchKernelGGL((qk_grad_kernel<ES, LAYOUT, G>), dim3(groups), dim3(256), 0, s, T, H, M, p.sq, p.steps, p.per, p.units,
+                       p.parts, part);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !part) return e;
+    hipLaunchKernelGGL(qk_grad_sums_kernel, dim3((4 * H.D + 15) / 16), dim3(256), 0, s, part, (int)groups, H.D, T.dwq, T.dbq,
+                       T.dwk, T.dbk);
+    return hipGetLastError();
+}
+
+template <int ES, int LAYOUT>
+static hipError_t launch_qk_width(hipStream_t s, const QkTensors &T, const QkHeads &H, int64_t M, bool grad, float *part) {
+    const int n = H.D / 8;
+    if (n <= 1) return launch_qk_one<ES, LAYOUT, 1>(s, T, H, M, grad, part);
+    if (n <= 2) return launch_qk_one<ES, LAYOUT, 2>(s, T, H, M, grad, part);
+    if (n <= 4) return launch_qk_one<ES, LAYOUT, 4>(s, T, H, M, grad, part);
+    if (n <= 8) return launch_qk_one<ES, LAYOUT, 8>(s, T, H, M, grad, part);
+    if (n <= 16) return launch_qk_one<ES, LAYOUT, 16>(s, T, H, M, grad, part);
+    return launch_qk_one<ES, LAYOUT, 32>(s, T, H, M, grad, part);
+}
+
+size_t qk_grad_bytes(int D) { return (size_t)kQkGroups * 4 * D * sizeof(float); }
+
+hipError_t launch_qk(hipStream_t s, const QkTensors &T, const QkHeads &H, int64_t M, int dtype, bool grad, void *ws) {
+    float *part = grad && (T.dwq || T.dbq || T.dwk || T.dbk) ? static_cast<float *>(ws) : nullptr;
+    if ((M == 0 || H.nq + H.nk == 0) && !part) return hipSuccess;
+    if (dtype == 0) return H.layout == 0 ? launch_qk_width<4, 0>(s, T, H, M, grad, part) : launch_qk_width<4, 1>(s, T, H, M, grad, part);
+    return H.layout == 0 ? launch_qk_width<2, 0>(s, T, H, M, grad, part) : launch_qk_width<2, 1>(s, T, H, M, grad, part);
+}
+
+}  // namespace dmpq

@@ -549,6 +549,134 @@ dmpq_status dmpq_adamw_step(hipStream_t stream, const void *d_table, int64_t n_t
                             double beta1, double beta2, double eps, double weight_decay,
                             int64_t step, const double *d_norm, double max_norm);
 
+/* ===========================================================================
+ * The whole linear: what stands between a GEMM's sums and the tensor that the
+ * next operator reads, in the GEMM's epilogue.  With v = the linear's fp32 value
+ * (as the *_ex GEMMs'), all in fp32 and rounded once:
+ *   v += scale * t b^T              lora: the adapter term of the *_lora GEMMs
+ *   v += bias                       bias [N]
+ *   pre = v                         pre [M x N] of y's type: v rounded
+ *   v = heads(v)                    the heads of q and k normed and rotated
+ *   y = residual + gate * act(v)    residual [M x N] of y's type (may be y);
+ *                                   gate [gate_rows x N]
+ * Any part may be absent (NULL, DMPQ_ACT_NONE).  Row m takes row s of the gate
+ * for the request s with gate_start[s] <= m < gate_start[s+1] (int32
+ * [gate_rows + 1], ascending, on the device); rows of no request get no gated
+ * term: y is the residual bit for bit there, or 0.  gate_start NULL: the gate
+ * has one row, for all rows.  Boundaries that do not ascend give unspecified
+ * results, and no access out of bounds.
+ * Activations: GELU is v Phi(v), GELU_TANH v/2 (1 + tanh(sqrt(2/pi) (v +
+ * 0.044715 v^3))), SILU v / (1 + e^-v).  At -infinity they give NaN.
+ * heads: the first n_q * dim columns of y are the heads of q, the next n_k * dim
+ * those of k, and the others (v) stay as they are.  dim 32, 64 or 128 (halves:
+ * rope_pairs a multiple of 8); DMPQ_OUT_BF16, without act, gate, residual and
+ * flags.  pre is what dmpq_qk_norm_rope_backward takes as q and k.
+ * flags: DMPQ_EPI_NVFP4_AMAX as in the *_ex GEMMs (bf16 output, N % 16 == 0).
+ * out_dtype F32 or BF16.  ws as in the *_ex GEMMs (NULL: no tail split).
+ * Up to 64 rows without flags take kernels of their own, which read the weight
+ * once over the whole chip and need no workspace.
+ * ========================================================================= */
+enum { DMPQ_ACT_NONE = 0, DMPQ_ACT_GELU = 1, DMPQ_ACT_GELU_TANH = 2, DMPQ_ACT_SILU = 3 };
+enum { DMPQ_NORM_NONE = 0, DMPQ_NORM_RMS = 1, DMPQ_NORM_LAYER = 2 };
+/* Members of rotated pair p: neighbours (2p, 2p + 1), or halves (p, p + rope_pairs). */
+enum { DMPQ_ROPE_PAIRS = 0, DMPQ_ROPE_HALVES = 1 };
+
+/* The heads of q and k (host struct of device pointers).  A head x of dim values:
+ *   n = (x - m) / sqrt(mean((x - m)^2) + eps), m = mean(x) (LAYER) or 0 (RMS)
+ *   y = n * w + b, then pair p is turned by the angle whose (cos, sin) is
+ *   table[row][p]; values behind the pairs are not turned.
+ * w and b [dim] (w_dtype F32 or BF16), of q and of k; NULL: 1 and 0.  dim is a
+ * multiple of 8, at most 256; rope_pairs 0 .. dim/2 (0: no rotation; halves: a
+ * multiple of 4).  fp32 throughout: a head whose squares overflow gives 0 (NaN
+ * where it is infinite). */
+typedef struct dmpq_qk_heads {
+    int32_t n_q, n_k, dim;
+    int32_t norm, layout, w_dtype;
+    int32_t rope_pairs;
+    double eps;
+    const void *wq, *bq, *wk, *bk;
+    const float *table; /* [rows x rope_pairs x 2], dmpq_rope_table */
+} dmpq_qk_heads;
+
+/* The adapter term: as the arguments of the *_lora GEMMs. */
+typedef struct dmpq_lora_term {
+    const float *t;
+    const uint16_t *b;
+    const int32_t *rank;
+    const float *scale;
+    const int32_t *seg_start, *seg_adapter;
+    int64_t R, S, n_adapters;
+} dmpq_lora_term;
+
+/* Host struct of device pointers, read during the call only. */
+typedef struct dmpq_linear_epilogue {
+    const void *bias, *gate, *residual;
+    const int32_t *gate_start;
+    void *pre;
+    int64_t gate_rows;
+    int32_t bias_dtype, gate_dtype; /* DMPQ_OUT_F32 or DMPQ_OUT_BF16 */
+    int32_t act, flags;
+    const dmpq_qk_heads *heads;
+    const dmpq_lora_term *lora;
+} dmpq_linear_epilogue;
+
+dmpq_status dmpq_gemm_bf16_linear(hipStream_t stream, const uint16_t *x, const uint16_t *w, int64_t M, int64_t N,
+                                  int64_t K, int out_dtype, void *y, const dmpq_linear_epilogue *h_epilogue, void *ws,
+                                  size_t ws_bytes);
+dmpq_status dmpq_qgemm_int8_linear(hipStream_t stream, const int8_t *qa, const float *sa, const int8_t *qw,
+                                   const float *sw, int64_t M, int64_t N, int64_t K, int out_dtype, void *y,
+                                   const dmpq_linear_epilogue *h_epilogue, void *ws, size_t ws_bytes);
+dmpq_status dmpq_qgemm_nvfp4_linear(hipStream_t stream, const uint8_t *ca, const uint8_t *sa, const float *d_ga,
+                                    const uint8_t *cw, const uint8_t *sw, const float *d_gw, int64_t M, int64_t N,
+                                    int64_t K, int out_dtype, void *y, const dmpq_linear_epilogue *h_epilogue, void *ws,
+                                    size_t ws_bytes);
+
+/* Gradients of y = residual + gate * act(pre) (the residual's is dy itself):
+ *   du = gate * act'(pre) * dy            [M x N] of dy's type (0 in rows of no request)
+ *   dgate[s] = sum of dy * act(pre) over the rows of s     [gate_rows x N] fp32
+ *   dbias = sum of du, before its rounding, over all rows  [N] fp32
+ * dy, pre and du are F32 or BF16, all three; du may be dy or pre.  du, dgate and
+ * dbias may be NULL (not computed), pre where act is NONE and dgate NULL, gate
+ * where there is none.  Sums are fp32 in a fixed order (the same bits on every
+ * call).  N at most 2^26.  ws for dgate and dbias:
+ * dmpq_linear_backward_bytes(M, N, gate_rows) bytes (0: out of range). */
+size_t dmpq_linear_backward_bytes(int64_t M, int64_t N, int64_t gate_rows);
+dmpq_status dmpq_linear_epilogue_backward(hipStream_t stream, const void *dy, const void *pre, int64_t M, int64_t N,
+                                          int dtype, int act, const void *gate, int gate_dtype,
+                                          const int32_t *gate_start, int64_t gate_rows, void *du, float *dgate,
+                                          float *dbias, void *ws, size_t ws_bytes);
+
+/* ===========================================================================
+ * The heads of q and k as passes of their own.
+ * ========================================================================= */
+
+/* table [M x P x 2] fp32 = (cos, sin) of pos[m][axis of p] * freq[p], the angle
+ * in 64 bits.  pos [M x n_axes], int32 (DMPQ_OUT_I32) or fp32 (DMPQ_OUT_F32);
+ * the first h_axis_pairs[0] pairs turn with axis 0, the next with axis 1, ...;
+ * P, their sum, is at most 128, n_axes at most 8.  freq [P] fp64, radians per
+ * position.  A row whose positions are 0 is not turned. */
+dmpq_status dmpq_rope_table(hipStream_t stream, const void *pos, int pos_dtype, const double *freq, int64_t M,
+                            int n_axes, const int32_t *h_axis_pairs, float *table);
+
+/* q_out, k_out = the heads of q [M x n_q x dim] and k [M x n_k x dim], F32 or
+ * BF16 (all four), normed and rotated.  ld*: elements from one row to the next
+ * (heads of a row are dense; at least n * dim; rows 16-byte aligned), so that q
+ * and k may lie in the rows of QKV.  In place is allowed.  Tensors of zero heads
+ * may be NULL. */
+dmpq_status dmpq_qk_norm_rope(hipStream_t stream, const void *q, int64_t ldq, const void *k, int64_t ldk, int64_t M,
+                              int dtype, const dmpq_qk_heads *h_heads, void *q_out, int64_t ldq_out, void *k_out,
+                              int64_t ldk_out);
+
+/* Gradients: dxq, dxk of the inputs q and k from dq, dk of the outputs (in place
+ * of those is allowed), and dw*, db* [dim] fp32 of the weights (summed over rows
+ * and heads in a fixed order; any may be NULL; with none, ws may be NULL).  q and
+ * k are not read without a norm.  ws: dmpq_qk_backward_bytes(dim) bytes. */
+size_t dmpq_qk_backward_bytes(int dim);
+dmpq_status dmpq_qk_norm_rope_backward(hipStream_t stream, const void *dq, int64_t lddq, const void *dk, int64_t lddk,
+                                       const void *q, int64_t ldq, const void *k, int64_t ldk, int64_t M, int dtype,
+                                       const dmpq_qk_heads *h_heads, void *dxq, int64_t lddxq, void *dxk, int64_t lddxk,
+                                       float *dwq, float *dbq, float *dwk, float *dbk, void *ws, size_t ws_bytes);
+
 #ifdef __cplusplus
 }
 #endif
