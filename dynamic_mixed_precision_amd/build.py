@@ -17,10 +17,12 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libdmpq.so")
 BUILD_DIR = os.path.join(ROOT, "_build", "dmpq")
 
-SOURCES = ["api.hip", "quant.hip", "reduce.hip", "gemm_int8.hip", "gemm_nvfp4.hip", "gemm_bf16.hip",
-           "gemm_int8_linear.hip", "gemm_nvfp4_linear.hip", "gemm_bf16_linear.hip", "linear.hip", "qk.hip",
-           "lora.hip", "adamw.hip", "selftest.hip",
-           "noalloc.hip"]
+# The GEMMs with a linear's epilogue come first: they take longest to compile.
+SOURCES = ["gemm_nvfp4_linear.hip", "gemm_nvfp4_linear_lora.hip", "gemm_bf16_linear.hip", "gemm_int8_linear.hip",
+           "gemm_nvfp4_linear_heads.hip", "gemm_bf16_linear_heads.hip", "gemm_int8_linear_heads.hip",
+           "gemm_int8.hip", "gemm_nvfp4.hip", "gemm_bf16.hip",
+           "linear_mid_bf16.hip", "linear_mid_int8.hip", "linear_mid_nvfp4.hip", "linear.hip", "qk.hip",
+           "api.hip", "quant.hip", "reduce.hip", "lora.hip", "adamw.hip", "selftest.hip", "noalloc.hip"]
 ARCH = "gfx950"
 
 # -ffp-contract=off: every fp32 expression is a sequence of single IEEE RNE

@@ -28,7 +28,7 @@ __global__ __launch_bounds__(256, 1) void gemm_bf16_kernel(
     const int lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
     const unsigned pid = xcd_order(blockIdx.x, gridDim.x);
-    const TileCoord tc = tile_at(pid, tiles_m, tiles_n, GROUP_M);
+    const TileCoord tc = tile_scalar<EPI>(tile_at(pid, tiles_m, tiles_n, GROUP_M));
     const int64_t m0 = (int64_t)tc.m * BM, n0 = (int64_t)tc.n * BN;
 
     if constexpr ((EPI & kEpiLora) != 0) lora_meta_dma(lora_of(ep).batch, lds + kLoraMetaOff, tid);
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(64) void gemm_f32_fixup_kernel(
     // workgroup = (tail tile t, quadrant wave, 32-row slice i)
     const int lane = threadIdx.x, i = blockIdx.x & 3, wave = (blockIdx.x >> 2) & 3;
     const unsigned t = blockIdx.x >> 4, pid = sp.full + t;
-    const TileCoord tc = tile_at(pid, tiles_m, tiles_n, group_m);
+    const TileCoord tc = tile_scalar<EPI>(tile_at(pid, tiles_m, tiles_n, group_m));
     const int64_t m0 = (int64_t)tc.m * 256, n0 = (int64_t)tc.n * 256;
     EpiScaleF32 sc{ga ? *ga : 1.0f, gw ? *gw : 1.0f};
     split_fixup_epilogue<OUT, EPI, float, S>(spart + (size_t)t * S * kSplitWords, sc, lds, M, N, m0, n0, wave,

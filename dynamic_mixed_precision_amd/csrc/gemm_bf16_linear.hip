@@ -15,13 +15,13 @@ hipError_t launch_f32_fixup_linear(hipStream_t s, const float *ga, const float *
         if (epi == (kEpiLinear | kEpiLora)) DMPQ_LINEAR(0, kEpiLinear | kEpiLora);
     }
     if (out_dtype != 1) return hipErrorInvalidValue;
+    if ((epi & kEpiHeads) != 0)
+        return launch_f32_fixup_linear_heads(s, ga, gw, M, N, y, tiles_m, tiles_n, group_m, partial, sp, spart, epi, lin);
     switch (epi) {
         case kEpiLinear: DMPQ_LINEAR(1, kEpiLinear);
         case kEpiLinear | kEpiAmax: DMPQ_LINEAR(1, kEpiLinear | kEpiAmax);
         case kEpiLinear | kEpiLora: DMPQ_LINEAR(1, kEpiLinear | kEpiLora);
         case kEpiLinear | kEpiLora | kEpiAmax: DMPQ_LINEAR(1, kEpiLinear | kEpiLora | kEpiAmax);
-        case kEpiLinear | kEpiHeads: DMPQ_LINEAR(1, kEpiLinear | kEpiHeads);
-        case kEpiLinear | kEpiHeads | kEpiLora: DMPQ_LINEAR(1, kEpiLinear | kEpiHeads | kEpiLora);
     }
 #undef DMPQ_LINEAR
     return hipErrorInvalidValue;
@@ -32,19 +32,19 @@ hipError_t launch_gemm_bf16_linear(hipStream_t s, const uint16_t *x, const uint1
                                    const LinearEpi &lin) {
     if (M == 0 || N == 0) return hipSuccess;
 #define DMPQ_LINEAR(OUT_, EPI_) return launch_bf16_paths<OUT_, (EPI_)>(s, x, w, M, N, K, y, partial, spart, lin)
-    const int epi = kEpiLinear | (amax ? kEpiAmax : 0) | (lin.lora.t ? kEpiLora : 0) | (lin.qk.D ? kEpiHeads : 0);
+    const int epi = linear_epi(amax, lin, N);
     if (out_dtype == 0) {
         if (epi == kEpiLinear) DMPQ_LINEAR(0, kEpiLinear);
         if (epi == (kEpiLinear | kEpiLora)) DMPQ_LINEAR(0, kEpiLinear | kEpiLora);
     }
     if (out_dtype != 1) return hipErrorInvalidValue;
+    if ((epi & kEpiHeads) != 0)
+        return launch_gemm_bf16_linear_heads(s, x, w, M, N, K, y, partial, spart, lin, epi);
     switch (epi) {
         case kEpiLinear: DMPQ_LINEAR(1, kEpiLinear);
         case kEpiLinear | kEpiAmax: DMPQ_LINEAR(1, kEpiLinear | kEpiAmax);
         case kEpiLinear | kEpiLora: DMPQ_LINEAR(1, kEpiLinear | kEpiLora);
         case kEpiLinear | kEpiLora | kEpiAmax: DMPQ_LINEAR(1, kEpiLinear | kEpiLora | kEpiAmax);
-        case kEpiLinear | kEpiHeads: DMPQ_LINEAR(1, kEpiLinear | kEpiHeads);
-        case kEpiLinear | kEpiHeads | kEpiLora: DMPQ_LINEAR(1, kEpiLinear | kEpiHeads | kEpiLora);
     }
 #undef DMPQ_LINEAR
     return hipErrorInvalidValue;

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device.hpp"
 #include "internal.hpp"
 #include "linear.hpp"
@@ -42,6 +44,11 @@ __device__ __forceinline__ TileCoord tile_of(unsigned bid, unsigned nwg, unsigne
                                              unsigned tiles_n, unsigned group_m) {
     return tile_at(xcd_order(bid, nwg), tiles_m, tiles_n, group_m);
 }
+
+// The tile in scalar registers: the forms of the whole linear use it in vector
+// arithmetic too, and the compiler may keep it there only.
+template <int EPI>
+__device__ __forceinline__ TileCoord tile_scalar(TileCoord tc);
 
 // A split workgroup of a SplitPlan launch: workgroup j runs the K stages
 // [s * nk / splits, (s + 1) * nk / splits) of tail tile full + j / splits,
@@ -134,8 +141,22 @@ struct EpiBand {
 // adapter term of the row's request is added to the fp32 value before any of
 // that, so it costs no pass over y of its own.  kEpiLinear: the whole linear's
 // epilogue (linear.hpp), whose operands are known at run time; with kEpiHeads
-// it norms and rotates the heads of q and k.
-enum { kEpiGelu = 1, kEpiAmax = 2, kEpiLora = 4, kEpiLinear = 8, kEpiHeads = 16 };
+// it norms and rotates the heads of q and k, with kEpiBand through LDS bands
+// (adapters, and shapes that the form from registers does not take).
+enum { kEpiGelu = 1, kEpiAmax = 2, kEpiLora = 4, kEpiLinear = 8, kEpiHeads = 16, kEpiBand = 32 };
+// the flags of one call
+inline int linear_epi(bool amax, const LinearEpi &L, int64_t N) {
+    return kEpiLinear | (amax ? kEpiAmax : 0) | (L.lora.t ? kEpiLora : 0) | (L.qk.D ? kEpiHeads : 0) |
+           (L.qk.D && !L.lora.t && !heads_from_regs(L, N) ? kEpiBand : 0);
+}
+constexpr bool heads_in_regs(int epi) { return (epi & kEpiHeads) != 0 && (epi & (kEpiLora | kEpiBand)) == 0; }
+
+template <int EPI>
+__device__ __forceinline__ TileCoord tile_scalar(TileCoord tc) {
+    if constexpr ((EPI & kEpiLinear) != 0)
+        return TileCoord{(unsigned)__builtin_amdgcn_readfirstlane((int)tc.m), (unsigned)__builtin_amdgcn_readfirstlane((int)tc.n)};
+    return tc;
+}
 
 // The epilogue's operands as a kernel argument.  (A member type, not an
 // expression of EPI: that one would enter the kernels' names, where host and
@@ -157,9 +178,19 @@ using EpiArg = typename EpiArgOf<EPI>::type;
 __device__ __forceinline__ const LoraEpi &lora_of(const LoraEpi &e) { return e; }
 __device__ __forceinline__ const LoraEpi &lora_of(const LinearEpi &e) { return e.lora; }
 
+// The other half of a wave's value (lane l: that of lane l ^ 32), by the swap of
+// the halves of two registers.
+__device__ __forceinline__ float other_half(float v) {
+    const uint32_t u = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);  // {lower, lower}, {upper, upper}
+    return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
 // max |value| of the rotated 16-block whose elements 0..7 (lo) or 8..15 the
-// lane holds as bf16; the other half is its neighbour's.  Stages 1, 2, 4 in the
-// lane, stage 8 across the pair, then * 1/4: the quantizer's order.
+// lane holds as bf16; the other half is its neighbour's (HALVES: the lane's in the
+// wave's other half).  Stages 1, 2, 4 in the lane, stage 8 across the pair, then
+// * 1/4: the quantizer's order.
+template <bool HALVES = false>
 __device__ __forceinline__ float block16_amax(const uint4 &v, bool lo) {
     float f[8];
     f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
@@ -178,7 +209,7 @@ __device__ __forceinline__ float block16_amax(const uint4 &v, bool lo) {
     for (int i = 0; i < 8; i++) {
         // the partner lane's value: DPP quad_perm [1, 0, 3, 2] swaps
         // lanes 2k and 2k+1 inside the VALU (no LDS round trip)
-        const float o = dpp_f32<0xB1>(f[i]);
+        const float o = HALVES ? other_half(f[i]) : dpp_f32<0xB1>(f[i]);
         const float w = lo ? f[i] + o : o - f[i];
         m = fmaxf(m, __builtin_fabsf(w * 0.25f));
     }
@@ -253,19 +284,190 @@ __device__ __forceinline__ float epi_band_to_global(const uint8_t *band, void *y
     return amax;
 }
 
-// The whole linear's epilogue for one wave's fp32 LDS band (rows of
-// kLoraBandStride bytes) of ROWS rows from row0 on, in which the scaled sums (and
-// the adapter term) lie: bias, pre, heads, activation, gate, residual, one
-// rounding, store; returns the lane's part of the fused amax.  A lane has the
-// same 16 bytes of columns in every row, so what depends on the column is
-// loaded once (T, Q).
+// The whole linear's epilogue for the 16 bytes of columns from `col` on that a
+// lane holds of one row: v are the scaled sums (with the adapter term); bias, pre,
+// heads, activation, gate, residual, one rounding, store.  A lane has the same
+// columns in every row, so what depends on the column is loaded once (T, Q).
+// chunk: the lane's place in the row; request: of the row, for kGateMixed;
+// residual: the lane's 16 bytes of it, where they are loaded already.
+// Returns the lane's part of the fused amax (kEpiAmax, where want_amax).  All lanes
+// of the wave call it together.
+template <int ESIZE, int EPI>
+__device__ __forceinline__ float linear_row_out(float (&v)[16 / ESIZE], void *y, int64_t M, int64_t N, int64_t row,
+                                                int64_t col, int chunk, bool vec, int request, const LinearEpi &L,
+                                                const LinearLane<16 / ESIZE> &T, const QkLane<16 / ESIZE> &Q,
+                                                bool want_amax, const uint4 *residual = nullptr) {
+    constexpr int PER = 16 / ESIZE;
+    const bool in = row < M && col < N;
+#pragma unroll
+    for (int i = 0; i < PER; i++) v[i] += T.bias[i];
+    if (L.pre && in) store_values<ESIZE, PER>(L.pre, row * N + col, N - col, vec, v);
+    if constexpr ((EPI & kEpiHeads) != 0)
+        Q.apply(L.qk, row < M ? row : M - 1, v);
+    else
+        act_apply<PER>(v, L.act);
+    T.template finish<ESIZE>(L, row, N, col, in, vec, request, v, residual);
+    float m = 0.0f;
+    if constexpr ((EPI & kEpiAmax) != 0) {
+        static_assert(ESIZE == 2, "the fused amax reads bf16 outputs");
+        if (want_amax) {
+            m = block16_amax(make_uint4(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]), cvt_pk_bf16(v[4], v[5]),
+                                        cvt_pk_bf16(v[6], v[7])), (chunk & 1) == 0);
+            if (!in) m = 0.0f;
+        }
+    }
+    if (in) store_values<ESIZE, PER>(y, row * N + col, N - col, vec, v);
+    return m;
+}
+
+// A pointer that is the same in every lane, in scalar registers.
+__device__ __forceinline__ uint8_t *uniform_ptr(uint8_t *p) {
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u), hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
+    return reinterpret_cast<uint8_t *>((uint64_t)hi << 32 | lo);
+}
+
+// The rows of a band where they are whole 16-byte pieces: one pass of the loop is
+// one store of 64 lanes, with as little around it as the call leaves (its wave is
+// alone on its SIMD, and every instruction counts): the activation, and whether
+// there is more than it and the bias, are chosen outside.
+constexpr int64_t kMaxFastN = int64_t(1) << 26;
+template <int ESIZE>
+struct BandPlace {
+    static constexpr int PER = 16 / ESIZE, LPR = 128 / PER, RPP = 64 / LPR, GROUP = 4;  // passes of a group
+    int64_t base, step;  // bytes: of the band's first row and column in y, pre and the residual; of a pass
+    uint32_t off;        // the lane's
+    int rows;            // there are, from the lane's on; none for lanes whose columns are past the end
+    __device__ __forceinline__ BandPlace(int64_t M, int64_t N, int64_t row0, int64_t col0, int lane, int most) {
+        const int lr = lane / LPR, chunk = lane % LPR;
+        base = (row0 * N + col0) * ESIZE, step = RPP * N * ESIZE;
+        off = (uint32_t)lr * (uint32_t)N * ESIZE + 16 * chunk;
+        rows = col0 + chunk * PER < N ? (int)(M - row0 < most ? M - row0 : most) - lr : 0;
+    }
+    // the residual of group g
+    __device__ __forceinline__ void ahead(const LinearEpi &L, int g, uint4 (&r)[GROUP]) const {
+        const uint8_t *p = uniform_ptr(const_cast<uint8_t *>(static_cast<const uint8_t *>(L.residual)) + base + g * GROUP * step);
+#pragma unroll
+        for (int k = 0; k < GROUP; k++) {
+            r[k] = make_uint4(0, 0, 0, 0);
+            if ((g * GROUP + k) * RPP < rows) r[k] = load_nt16(p + k * step + off);
+        }
+    }
+};
+
+// With more than bias and activation (MORE) the residual comes in a group of
+// passes ahead, the first one (r) before the band was written: waited for pass by
+// pass it cost 30 us a tile.
+template <int ESIZE, int EPI, int ROWS, int ACT, bool MORE>
+__device__ __forceinline__ float linear_band_rows(const uint8_t *band, void *y, int64_t N, int64_t row0, int64_t col0, int lane,
+                                                  const LinearEpi &L, const LinearLane<16 / ESIZE> &T,
+                                                  const BandPlace<ESIZE> &B, uint4 (&r)[4]) {
+    typedef BandPlace<ESIZE> P;
+    constexpr int PER = P::PER, LPR = P::LPR, RPP = P::RPP, GROUP = P::GROUP;
+    const int chunk = lane % LPR, lr = lane / LPR;
+    const uint8_t *src = band + lr * kLoraBandStride + 4 * PER * chunk;
+    uint8_t *py = uniform_ptr(static_cast<uint8_t *>(y) + B.base), *pp = nullptr;
+    if (MORE && L.pre) pp = uniform_ptr(static_cast<uint8_t *>(L.pre) + B.base);
+    float amax = 0.0f;
+#pragma unroll 1
+    for (int g = 0; g < ROWS / RPP / GROUP; g++) {
+        uint4 next[GROUP];
+        if (MORE && L.residual && (g + 1) * GROUP < ROWS / RPP) B.ahead(L, g + 1, next);
+#pragma unroll
+        for (int k = 0; k < GROUP; k++) {
+            const bool in = (g * GROUP + k) * RPP < B.rows;
+            float v[PER];
+#pragma unroll
+            for (int i = 0; i < PER; i += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(src + k * RPP * kLoraBandStride + 4 * i);
+                v[i] = a.x + T.bias[i], v[i + 1] = a.y + T.bias[i + 1];
+                v[i + 2] = a.z + T.bias[i + 2], v[i + 3] = a.w + T.bias[i + 3];
+            }
+            auto store = [&](uint8_t *to) __attribute__((always_inline)) {
+                uint4 u;
+                if constexpr (ESIZE == 4)
+                    u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+                else
+                    u = make_uint4(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]), cvt_pk_bf16(v[PER - 4], v[PER - 3]),
+                                   cvt_pk_bf16(v[PER - 2], v[PER - 1]));
+                if (in) store_nt16(to + k * B.step + B.off, u);
+                return u;
+            };
+            if (MORE && pp) store(pp);
+            act_apply<PER>(v, ACT);
+            if constexpr (MORE) {
+                if (T.mode == kGateOne) {
+#pragma unroll
+                    for (int i = 0; i < PER; i++) v[i] *= T.gate[i];
+                } else if (T.mode != kGateNone) {
+                    // rows of no request take no term at all, not zero times one
+                    const int row = (int)row0 + (g * GROUP + k) * RPP + lr;
+                    const int s = T.mode == kGateMixed && in ? request_of(L.gate_start, L.S, row) : -1;
+                    const bool some = s >= 0 && s < L.S;
+                    float w[PER];
+                    if (some) load_values<PER>(L.gate, L.gate_bf16, s * N + col0 + chunk * PER, PER, w);
+#pragma unroll
+                    for (int i = 0; i < PER; i++) v[i] = some ? v[i] * w[i] : L.residual ? -0.0f : 0.0f;
+                }
+                if (L.residual) {
+                    const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+#pragma unroll
+                    for (int i = 0; i < PER; i++)
+                        v[i] += ESIZE == 4 ? __uint_as_float(w[i * ESIZE / 4]) : i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+                }
+            }
+            const uint4 u = store(py);
+            if constexpr ((EPI & kEpiAmax) != 0) {
+                const float m = block16_amax(u, (chunk & 1) == 0);
+                if (in) amax = fmaxf(amax, m);
+            }
+        }
+        src += GROUP * RPP * kLoraBandStride;
+        py += GROUP * B.step;
+        if (MORE) {
+            if (pp) pp += GROUP * B.step;
+#pragma unroll
+            for (int k = 0; k < GROUP; k++) r[k] = next[k];
+        }
+    }
+    return amax;
+}
+
+template <int ESIZE, int EPI, int ROWS>
+__device__ __forceinline__ float linear_band_fast(const uint8_t *band, void *y, int64_t M, int64_t N, int64_t row0,
+                                                  int64_t col0, int lane, const LinearEpi &L,
+                                                  const LinearLane<16 / ESIZE> &T, uint4 (&r)[4]) {
+    const bool more = L.pre || L.residual || T.mode != kGateNone;
+    const BandPlace<ESIZE> B(M, N, row0, col0, lane, ROWS);
+#define DMPQ_ROWS(ACT_)                                                                                            \
+    return more ? linear_band_rows<ESIZE, EPI, ROWS, ACT_, true>(band, y, N, row0, col0, lane, L, T, B, r)        \
+                : linear_band_rows<ESIZE, EPI, ROWS, ACT_, false>(band, y, N, row0, col0, lane, L, T, B, r)
+    if (L.act == kActNone) DMPQ_ROWS(kActNone);
+    if (L.act == kActGelu) DMPQ_ROWS(kActGelu);
+    if (L.act == kActGeluTanh) DMPQ_ROWS(kActGeluTanh);
+    DMPQ_ROWS(kActSilu);
+#undef DMPQ_ROWS
+}
+
+// The same for one wave's fp32 LDS band of ROWS rows of 128 columns from row0 on
+// (kLoraBandStride bytes apart).  residual: linear_residual's.
+// The first rows' residual of a band, to be loaded before the band is written.
+template <int ESIZE>
+__device__ __forceinline__ void linear_residual(const LinearEpi &L, int64_t M, int64_t N, int64_t row0, int64_t col0, int lane,
+                                                bool vec, int rows, uint4 (&r)[4]) {
+    if (L.residual && vec && N <= kMaxFastN) BandPlace<ESIZE>(M, N, row0, col0, lane, rows).ahead(L, 0, r);
+}
+
 template <int ESIZE, int EPI, int ROWS>
 __device__ __forceinline__ float linear_band_out(const uint8_t *band, void *y, int64_t M, int64_t N, int64_t row0,
                                                  int64_t col0, int lane, bool vec, const LinearEpi &L,
-                                                 const LinearLane<16 / ESIZE> &T, const QkLane<16 / ESIZE> &Q) {
+                                                 const LinearLane<16 / ESIZE> &T, const QkLane<16 / ESIZE> &Q,
+                                                 uint4 (&residual)[4]) {
     constexpr int PER = 16 / ESIZE, LPR = 128 / PER, RPP = 64 / LPR;
     const int chunk = lane % LPR;
     const int64_t col = col0 + chunk * PER;
+    if constexpr ((EPI & kEpiHeads) == 0)
+        if (vec && N <= kMaxFastN) return linear_band_fast<ESIZE, EPI, ROWS>(band, y, M, N, row0, col0, lane, L, T, residual);
     float amax = 0.0f;
     int request = 0;
     if (T.mode == kGateMixed) {
@@ -275,29 +477,14 @@ __device__ __forceinline__ float linear_band_out(const uint8_t *band, void *y, i
 #pragma unroll 2
     for (int p = 0; p < ROWS / RPP; p++) {
         const int r = p * RPP + lane / LPR;
-        const int64_t row = row0 + r;
-        const bool in = row < M && col < N;
         float v[PER];
 #pragma unroll
         for (int i = 0; i < PER; i += 4) {
             const float4 a = *reinterpret_cast<const float4 *>(band + r * kLoraBandStride + (chunk * PER + i) * 4);
-            v[i] = a.x + T.bias[i], v[i + 1] = a.y + T.bias[i + 1];
-            v[i + 2] = a.z + T.bias[i + 2], v[i + 3] = a.w + T.bias[i + 3];
+            v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
         }
-        if (L.pre && in) store_values<ESIZE, PER>(L.pre, row * N + col, N - col, vec, v);
-        if constexpr ((EPI & kEpiHeads) != 0)
-            Q.apply(L.qk, row < M ? row : M - 1, v);
-        else
-            act_apply<PER>(v, L.act);
         const int mine = T.mode == kGateMixed ? __shfl(request, r, 64) : 0;
-        T.template finish<ESIZE>(L, row, N, col, in, vec, mine, v);
-        if constexpr ((EPI & kEpiAmax) != 0) {
-            static_assert(ESIZE == 2, "the fused amax reads bf16 outputs");
-            const float m = block16_amax(make_uint4(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]),
-                                                    cvt_pk_bf16(v[4], v[5]), cvt_pk_bf16(v[6], v[7])), (chunk & 1) == 0);
-            if (in) amax = fmaxf(amax, m);
-        }
-        if (in) store_values<ESIZE, PER>(y, row * N + col, N - col, vec, v);
+        amax = fmaxf(amax, linear_row_out<ESIZE, EPI>(v, y, M, N, row0 + r, col, chunk, vec, mine, L, T, Q, true));
     }
     return amax;
 }
@@ -373,7 +560,8 @@ __device__ __forceinline__ void band_epilogue(AccV (&acc)[4][4], Scale &sc, uint
 constexpr int kLoraMetaOff = kLoraLds + 2048;
 template <int EPI>
 constexpr size_t epi_lds(size_t bytes) {
-    return (EPI & kEpiLora) != 0 ? (size_t)kLoraMetaOff + kLoraMeta : bytes;
+    constexpr size_t bands = (EPI & kEpiLinear) != 0 ? 8 * kLoraBandBytes : 0;  // 4 of 64 rows
+    return (EPI & kEpiLora) != 0 ? (size_t)kLoraMetaOff + kLoraMeta : bytes > bands ? bytes : bands;
 }
 
 // The epilogue with the adapter term: as band_epilogue, but in slices of 32
@@ -412,48 +600,249 @@ __device__ __forceinline__ void lora_epilogue(AccV (&acc)[4][4], Scale &sc, uint
     if constexpr ((EPI & kEpiAmax) != 0) epi_tile_amax(amax, wave, lane, slot);
 }
 
-// The epilogue of the whole linear: slices of 32 rows through fp32 bands, as
-// lora_epilogue (and with it, where there are adapters).  A wave's band is its
-// own, so nothing waits for other waves unless b of an adapter is staged.
+// The epilogue of the whole linear: fp32 bands of 64 rows (32 with adapters, as
+// lora_epilogue and with it), bias to store row by row.  A wave's band is its own,
+// so nothing waits for other waves unless b of an adapter is staged.
 template <int OUT, int EPI, int AHEAD, class AccV, class Scale>
-__device__ __forceinline__ void linear_epilogue(AccV (&acc)[4][4], Scale &sc, uint8_t *lds, int64_t M, int64_t N,
-                                                int64_t m0, int64_t n0, int wave, int wm, int wn, int lane, void *y,
-                                                float *slot, const LinearEpi &L) {
+__device__ __forceinline__ void linear_band_epilogue(AccV (&acc)[4][4], Scale &sc, uint8_t *lds, int64_t M, int64_t N,
+                                                     int64_t m0, int64_t n0, int wave, int wm, int wn, int lane, void *y,
+                                                     float *slot, const LinearEpi &L) {
     constexpr int ES = OUT == 1 ? 2 : 4, PER = 16 / ES;
     constexpr bool LORA = (EPI & kEpiLora) != 0;
+    constexpr int SLICES = LORA ? 1 : 2;  // of 32 rows a band
     const int lm = lane & 31, lh = lane >> 5;
-    uint8_t *band = lds + wave * kLoraBandBytes;
+    uint8_t *band = lds + wave * SLICES * kLoraBandBytes;
     const bool vec = ((N * ES) & 15) == 0;
-    const int64_t col = n0 + wn * 128 + (lane % (128 / PER)) * PER;
+    const int64_t row0 = m0 + __builtin_amdgcn_readfirstlane(wm) * 128, col0 = n0 + __builtin_amdgcn_readfirstlane(wn) * 128;
+    const int64_t col = col0 + (lane % (128 / PER)) * PER;
     LinearLane<PER> T;
-    T.begin(L, m0 + wm * 128, 128, M, N, col);
+    T.begin(L, row0, 128, M, N, col);
     QkLane<PER> Q;
     if constexpr ((EPI & kEpiHeads) != 0) Q.begin(L.qk, col);
     LoraRows<LORA ? AHEAD : 1> t;
     LoraTile A;
     if constexpr (LORA) A = lora_tile_begin(L.lora, m0, n0, N, lds, lds + kLoraMetaOff, t);
     float amax = 0.0f;
+    auto one = [&](auto number) __attribute__((always_inline)) {
+        constexpr int h = decltype(number)::value;
+        uint4 residual[4];
+        linear_residual<ES>(L, M, N, row0 + 32 * SLICES * h, col0, lane, vec, 32 * SLICES, residual);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        sc.row(m0 + wm * 128 + i * 32 + lm);
+        for (int ii = 0; ii < SLICES; ii++) {
+            const int i = SLICES * h + ii;
+            sc.row(m0 + wm * 128 + i * 32 + lm);
 #pragma unroll
-        for (int j = 0; j < 4; j++)
+            for (int j = 0; j < 4; j++)
 #pragma unroll
-            for (int g = 0; g < 4; g++)
-                *reinterpret_cast<float4 *>(band + lm * kLoraBandStride + (j * 32 + 8 * g + 4 * lh) * 4) = make_float4(
-                    sc((float)acc[i][j][4 * g], j, g, 0), sc((float)acc[i][j][4 * g + 1], j, g, 1),
-                    sc((float)acc[i][j][4 * g + 2], j, g, 2), sc((float)acc[i][j][4 * g + 3], j, g, 3));
+                for (int g = 0; g < 4; g++)
+                    *reinterpret_cast<float4 *>(band + (32 * ii + lm) * kLoraBandStride + (j * 32 + 8 * g + 4 * lh) * 4) =
+                        make_float4(sc((float)acc[i][j][4 * g], j, g, 0), sc((float)acc[i][j][4 * g + 1], j, g, 1),
+                                    sc((float)acc[i][j][4 * g + 2], j, g, 2), sc((float)acc[i][j][4 * g + 3], j, g, 3));
+        }
         if constexpr (LORA) {
             LoraRows<AHEAD> next;
-            if (i < 3) A.load_t(L.lora, i + 1, next);
-            lora_band_add<AHEAD>(L.lora, A, i, n0, N, lds, t);
-            if (i < 3) t = next;
+            if (h < 3) A.load_t(L.lora, h + 1, next);
+            lora_band_add<AHEAD>(L.lora, A, h, n0, N, lds, t);
+            if (h < 3) t = next;
         }
-        amax = fmaxf(amax, linear_band_out<ES, EPI, 32>(band, y, M, N, m0 + wm * 128 + i * 32, n0 + wn * 128, lane, vec,
-                                                        L, T, Q));
-        __builtin_amdgcn_sched_barrier(0);  // one slice at a time: its accumulators are free now
-    }
+        amax = fmaxf(amax, linear_band_out<ES, EPI, 32 * SLICES>(band, y, M, N, row0 + 32 * SLICES * h, col0, lane, vec, L, T, Q,
+                                                                     residual));
+        __builtin_amdgcn_sched_barrier(0);  // one band at a time: its accumulators are free now
+    };
+    // written out: as a loop that is not unrolled the accumulators would live in memory
+    one(std::integral_constant<int, 0>()), one(std::integral_constant<int, 1>());
+    if constexpr (LORA) one(std::integral_constant<int, 2>()), one(std::integral_constant<int, 3>());
     if constexpr ((EPI & kEpiAmax) != 0) epi_tile_amax(amax, wave, lane, slot);
+}
+
+// ---- the heads of a QKV linear from registers ------------------------------------------
+// The accumulators are transposed: lane (row lm, half lh) has columns 8 g + 4 lh ..
+// + 3 of register group g.  Swapping the upper half of group 2 q with the lower
+// one of group 2 q + 1 gives every lane 8 consecutive columns of its row, 16 p +
+// 8 lh with p = 2 j + q.  Two lanes then hold a row's head, so that its sums take
+// one exchange, where 8 lanes that read it from a band take three for each sum
+// (17776 x 1920 x 5760, NVFP4: 506 us through bands, 425 from registers).  The
+// columns' parameters are in LDS, the wave's own.
+template <class AccV>
+__device__ __forceinline__ void acc_row8(const AccV &a, int q, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const float lo = (float)a[8 * q + e], hi = (float)a[8 * q + 4 + e];
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(lo), __float_as_uint(hi), false, false);
+        v[e] = __uint_as_float(r[0]);
+        v[4 + e] = __uint_as_float(r[1]);
+    }
+}
+
+// The wave's column parameters in LDS: bias, the heads' w and b, each of 128.
+constexpr int kColParams = 3 * 128;
+struct ColParams {
+    const float *p;  // the lane's, columns 8 lh ..
+    __device__ __forceinline__ void get(int which, int at, float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(p + which * 128 + at + i);
+            v[i] = u.x, v[i + 1] = u.y, v[i + 2] = u.z, v[i + 3] = u.w;
+        }
+    }
+};
+
+// The heads of 128 columns (16 p + 8 lh .. of row lm a lane): a head of D columns is
+// NP = D / 16 eights of a lane and as many of its partner's in the other half, so
+// its sums are in the lane but for one exchange, and both members of a rotated
+// pair are the lane's own (halves: 2 P = D).  The results of 32 rows go out through
+// the wave's bf16 band, whole rows a store: 64 bytes of 16 rows a store, straight
+// from registers, took 13 us more (17776 x 1920 x 5760).
+template <int D, bool PRE, class Get, class Cols>
+__device__ __forceinline__ void linear_heads_out(Get &&get, Cols &&cols, const ColParams &C, void *y, int64_t M, int64_t N,
+                                                 int64_t row0, int64_t col0, int lm, int lh, uint8_t *band, const LinearEpi &L) {
+    constexpr int NP = D / 16, HEADS = 128 / D;
+    const QkHeads &H = L.qk;
+    const float inv = 1.0f / (float)D;
+    const int h0 = (int)(col0 / D);
+    uint8_t *mine_at = band + lm * EpiBand<2>::STRIDE + 16 * lh;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        // the row's turns of the lane's pairs, two at a time: neighbours, 4 of each eight;
+        // halves, 8 of each eight of the first half
+        float4 z[NP][2];
+        if (!PRE && H.P > 0 && h0 < H.nq + H.nk) {
+            const int64_t row = row0 + 32 * i + lm < M ? row0 + 32 * i + lm : M - 1;
+            const float2 *t = reinterpret_cast<const float2 *>(H.table) + row * H.P;
+#pragma unroll
+            for (int p = 0; p < NP; p++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const int k = H.layout == 0 ? 8 * p + 4 * lh + 2 * e : 16 * (p >> 1) + 8 * lh + 4 * (p & 1) + 2 * e;
+                    z[p][e] = *reinterpret_cast<const float4 *>(t + (k < H.P ? k : 0));
+                }
+        }
+#pragma unroll
+        for (int hh = 0; hh < HEADS; hh++) {
+            const bool mine = h0 + hh < H.nq + H.nk;  // wave-uniform
+            float x[NP][8];
+            auto out = [&](int p) __attribute__((always_inline)) {
+                *reinterpret_cast<uint4 *>(mine_at + 32 * (NP * hh + p)) =
+                    make_uint4(cvt_pk_bf16(x[p][0], x[p][1]), cvt_pk_bf16(x[p][2], x[p][3]), cvt_pk_bf16(x[p][4], x[p][5]),
+                               cvt_pk_bf16(x[p][6], x[p][7]));
+            };
+#pragma unroll
+            for (int p = 0; p < NP; p++) {
+                float bias[8];
+                cols(16 * (NP * hh + p));
+                get(i, NP * hh + p, x[p]);
+                C.get(0, D * hh + 16 * p, bias);
+#pragma unroll
+                for (int e = 0; e < 8; e++) x[p][e] += bias[e];
+            }
+            if (PRE) {
+#pragma unroll
+                for (int p = 0; p < NP; p++) out(p);
+                continue;
+            }
+            if (mine && H.norm != 0) {
+                if (H.norm == 2) {
+                    float s = 0.0f;
+#pragma unroll
+                    for (int p = 0; p < NP; p++)
+#pragma unroll
+                        for (int e = 0; e < 8; e++) s += x[p][e];
+                    s = (s + other_half(s)) * inv;
+#pragma unroll
+                    for (int p = 0; p < NP; p++)
+#pragma unroll
+                        for (int e = 0; e < 8; e++) x[p][e] -= s;
+                }
+                float s = 0.0f;
+#pragma unroll
+                for (int p = 0; p < NP; p++)
+#pragma unroll
+                    for (int e = 0; e < 8; e++) s = __builtin_fmaf(x[p][e], x[p][e], s);
+                s += other_half(s);
+                const float r = rsqrt_f32(__builtin_fmaf(s, inv, H.eps));
+#pragma unroll
+                for (int p = 0; p < NP; p++) {
+                    float w[8], b[8];
+                    C.get(1, D * hh + 16 * p, w);
+                    C.get(2, D * hh + 16 * p, b);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) x[p][e] = __builtin_fmaf(x[p][e] * r, w[e], b[e]);
+                }
+            }
+            if (mine && H.P > 0) {
+                if (H.layout == 0) {
+#pragma unroll
+                    for (int p = 0; p < NP; p++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            const bool on = 8 * p + 4 * lh + e < H.P;
+                            const float4 f = z[p][e >> 1];
+                            const float cs = e & 1 ? f.z : f.x, sn = e & 1 ? f.w : f.y;
+                            const float a = x[p][2 * e], b = x[p][2 * e + 1];
+                            x[p][2 * e] = on ? a * cs - b * sn : a;
+                            x[p][2 * e + 1] = on ? b * cs + a * sn : b;
+                        }
+                } else {
+#pragma unroll
+                    for (int p = 0; p < NP / 2; p++)
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            const float4 f = z[2 * p + (e >> 2)][e >> 1 & 1];
+                            const float cs = e & 1 ? f.z : f.x, sn = e & 1 ? f.w : f.y;
+                            const float a = x[p][e], b = x[p + NP / 2][e];
+                            x[p][e] = a * cs - b * sn;
+                            x[p + NP / 2][e] = b * cs + a * sn;
+                        }
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < NP; p++) out(p);
+        }
+        epi_band_to_global<2, 0, 32>(band, PRE ? L.pre : y, M, N, row0 + 32 * i, col0, 32 * lh + lm, true);
+        __builtin_amdgcn_sched_barrier(0);  // one row's heads at a time
+    }
+}
+
+// Output scalings for it: cols(at) before 8 columns, then each value of slice i,
+// column e of them.
+struct RegScaleF32 {
+    float gA, gW;
+    __device__ __forceinline__ void cols(int) {}
+    __device__ __forceinline__ float operator()(float a, int, int) const { return (a * gA) * gW; }
+};
+
+// The epilogue of a QKV tile.  lds: 16 * kColParams bytes and four bf16 bands.
+template <class AccV, class Scale>
+__device__ __forceinline__ void linear_heads_epilogue(AccV (&acc)[4][4], Scale &sc, uint8_t *lds, int64_t M, int64_t N,
+                                                      int64_t m0, int64_t n0, int wave, int wm, int wn, int lane, void *y,
+                                                      const LinearEpi &L) {
+    const int64_t row0 = m0 + __builtin_amdgcn_readfirstlane(wm) * 128, col0 = n0 + __builtin_amdgcn_readfirstlane(wn) * 128;
+    // two columns a lane into the wave's LDS
+    LinearLane<2> T;
+    T.begin(L, row0, 128, M, N, col0 + 2 * lane);
+    QkLane<2> Q;
+    Q.begin(L.qk, col0 + 2 * lane);
+    float *params = reinterpret_cast<float *>(lds) + wave * kColParams;
+    const int lm = lane & 31, lh = lane >> 5;
+    const ColParams P{params + 8 * lh};
+    *reinterpret_cast<float2 *>(params + 2 * lane) = make_float2(T.bias[0], T.bias[1]);
+    *reinterpret_cast<float2 *>(params + 128 + 2 * lane) = make_float2(Q.w[0], Q.w[1]);
+    *reinterpret_cast<float2 *>(params + 256 + 2 * lane) = make_float2(Q.b[0], Q.b[1]);
+    auto get = [&](int i, int p, float (&v)[8]) __attribute__((always_inline)) {
+        acc_row8(acc[i][p >> 1], p & 1, v);
+#pragma unroll
+        for (int e = 0; e < 8; e++) v[e] = sc(v[e], i, e);
+    };
+    auto cols = [&](int at) __attribute__((always_inline)) { sc.cols(at); };
+    uint8_t *band = lds + 16 * kColParams + wave * 32 * EpiBand<2>::STRIDE;
+    // (with pre the accumulators are read twice: both at once would not fit the registers)
+    if (L.qk.D == 64) {
+        if (L.pre) linear_heads_out<64, true>(get, cols, P, y, M, N, row0, col0, lm, lh, band, L);
+        linear_heads_out<64, false>(get, cols, P, y, M, N, row0, col0, lm, lh, band, L);
+    } else {
+        if (L.pre) linear_heads_out<128, true>(get, cols, P, y, M, N, row0, col0, lm, lh, band, L);
+        linear_heads_out<128, false>(get, cols, P, y, M, N, row0, col0, lm, lh, band, L);
+    }
 }
 
 // fp32 accumulators -> y = (acc * gA) * gW (fp32 or bf16).  slot: the tile's
@@ -464,8 +853,13 @@ __device__ __forceinline__ void f32_band_epilogue(v16f (&acc)[4][4], uint8_t *ld
                                                   int64_t n0, int wave, int wm, int wn, int lane,
                                                   void *y, float *slot, const EpiArg<EPI> &ep) {
     if constexpr ((EPI & kEpiLinear) != 0) {
-        EpiScaleF32 sc{gA, gW};
-        linear_epilogue<OUT, EPI, 3>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot, ep);
+        if constexpr (heads_in_regs(EPI)) {
+            RegScaleF32 sc{gA, gW};
+            linear_heads_epilogue(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, ep);
+        } else {
+            EpiScaleF32 sc{gA, gW};
+            linear_band_epilogue<OUT, EPI, 3>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot, ep);
+        }
     } else if constexpr ((EPI & kEpiLora) != 0) {
         EpiScaleF32 sc{gA, gW};
         lora_epilogue<OUT, EPI, 3>(acc, sc, lds, M, N, m0, n0, wave, wm, wn, lane, y, slot, ep);
@@ -554,7 +948,9 @@ __device__ __forceinline__ void split_fixup_epilogue(const uint32_t *part, Scale
         cols.begin(ep, row0, kFixupRows, M, N, col);
         QkLane<PER> Q;
         if constexpr ((EPI & kEpiHeads) != 0) Q.begin(ep.qk, col);
-        amax = linear_band_out<ES, EPI, kFixupRows>(band, y, M, N, row0, n0 + wn * 128, lane, vec, ep, cols, Q);
+        uint4 residual[4];
+        linear_residual<ES>(ep, M, N, row0, n0 + wn * 128, lane, vec, kFixupRows, residual);
+        amax = linear_band_out<ES, EPI, kFixupRows>(band, y, M, N, row0, n0 + wn * 128, lane, vec, ep, cols, Q, residual);
     } else {
         amax = epi_band_to_global<ES, EPI, kFixupRows>(band, y, M, N, m0 + wm * 128 + i * 32, n0 + wn * 128, lane, vec);
     }

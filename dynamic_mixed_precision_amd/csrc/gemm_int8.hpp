@@ -128,6 +128,7 @@ struct EpiScaleI8Lds {
         return (a * sar) * cols[j * 32 + 8 * g + e];
     }
 };
+static_assert(8 * kLoraBandBytes <= gdma::LDS_BYTES && 8 * kLoraBandBytes <= 2 * i8gemm::STAGE, "bands below the scales");
 static_assert(kLoraLds + kI8ScaleBytes <= kLoraMetaOff && kLoraLds % 16 == 0 && 2 * i8gemm::STAGE <= kLoraLds &&
                   gdma::LDS_BYTES <= kLoraLds, "LDS of the adapter epilogue");
 
@@ -145,11 +146,36 @@ constexpr size_t i8_scale_off(size_t bytes) {
                                 (EPI & kEpiAmax) ? partial + pid : nullptr, ep);                \
     }
 
+// And for the epilogue from registers: sA of the lane's four rows, sW of its 8
+// columns.
+struct RegScaleI8 {
+    const float *sw;  // the lane's, columns 8 lh ..
+    float sar[4], c[8];
+    __device__ __forceinline__ RegScaleI8(const float *scl, int wm, int wn, int lane) : sw(scl + 256 + wn * 128 + 8 * (lane >> 5)) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) sar[i] = scl[wm * 128 + 32 * i + (lane & 31)];
+    }
+    __device__ __forceinline__ void cols(int at) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(sw + at + e);
+            c[e] = u.x, c[e + 1] = u.y, c[e + 2] = u.z, c[e + 3] = u.w;
+        }
+    }
+    __device__ __forceinline__ float operator()(float a, int i, int e) const { return (a * sar[i]) * c[e]; }
+};
+
 #define DMPQ_I8_LINEAR_EPILOGUE(SCL)                                                              \
     {                                                                                             \
-        EpiScaleI8Lds sc{(SCL), (SCL) + 256 + wn * 128 + 4 * (lane >> 5), m0, 0.0f};              \
-        linear_epilogue<OUT, EPI, 1>(acc, sc, reinterpret_cast<uint8_t *>(lds), M, N, m0, n0, wave, wm, wn, lane, y, \
-                                     (EPI & kEpiAmax) ? partial + pid : nullptr, ep);             \
+        uint8_t *lds_ = reinterpret_cast<uint8_t *>(lds);                                         \
+        float *slot_ = (EPI & kEpiAmax) ? partial + pid : nullptr;                                \
+        if constexpr (heads_in_regs(EPI)) {                                                       \
+            RegScaleI8 sc((SCL), wm, wn, lane);                                                   \
+            linear_heads_epilogue(acc, sc, lds_, M, N, m0, n0, wave, wm, wn, lane, y, ep);        \
+        } else {                                                                                  \
+            EpiScaleI8Lds sc{(SCL), (SCL) + 256 + wn * 128 + 4 * (lane >> 5), m0, 0.0f};          \
+            linear_band_epilogue<OUT, EPI, 1>(acc, sc, lds_, M, N, m0, n0, wave, wm, wn, lane, y, slot_, ep); \
+        }                                                                                         \
     }
 
 template <int OUT, int EPI>
@@ -163,7 +189,7 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_kernel(
     const int lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
     const unsigned pid = xcd_order(blockIdx.x, gridDim.x);
-    const TileCoord tc = tile_at(pid, tiles_m, tiles_n, GROUP_M);
+    const TileCoord tc = tile_scalar<EPI>(tile_at(pid, tiles_m, tiles_n, GROUP_M));
     const int64_t m0 = (int64_t)tc.m * BM, n0 = (int64_t)tc.n * BN;
 
     v16i acc[4][4];
@@ -402,7 +428,7 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_dma_kernel(
     const int lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
     const unsigned pid = xcd_order(blockIdx.x, gridDim.x);
-    const TileCoord tc = tile_at(pid, tiles_m, tiles_n, GROUP_M);
+    const TileCoord tc = tile_scalar<EPI>(tile_at(pid, tiles_m, tiles_n, GROUP_M));
     const int64_t m0 = (int64_t)tc.m * BM, n0 = (int64_t)tc.n * BN;
 
     float *scl = reinterpret_cast<float *>(lds + i8_scale_off<EPI>(LDS_BYTES));
@@ -488,7 +514,7 @@ __global__ __launch_bounds__(64) void gemm_i8_fixup_kernel(
     // workgroup = (tail tile t, quadrant wave, 32-row slice i)
     const int lane = threadIdx.x, i = blockIdx.x & 3, wave = (blockIdx.x >> 2) & 3;
     const unsigned t = blockIdx.x >> 4, pid = sp.full + t;
-    const TileCoord tc = tile_at(pid, tiles_m, tiles_n, GROUP_M);
+    const TileCoord tc = tile_scalar<EPI>(tile_at(pid, tiles_m, tiles_n, GROUP_M));
     const int64_t m0 = (int64_t)tc.m * BM, n0 = (int64_t)tc.n * BN;
     EpiScaleI8 sc(sa, sw, M, N, n0 + (wave & 1) * 128 + 4 * (lane >> 5));
     split_fixup_epilogue<OUT, EPI, int, S>(spart + (size_t)t * S * kSplitWords, sc, lds8, M, N, m0, n0, wave,

@@ -109,7 +109,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_f16_kernel(
     const int lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
     const unsigned pid = xcd_order(blockIdx.x, gridDim.x);
-    const TileCoord tc = tile_at(pid, tiles_m, tiles_n, GROUP_M);
+    const TileCoord tc = tile_scalar<EPI>(tile_at(pid, tiles_m, tiles_n, GROUP_M));
     const int64_t m0 = (int64_t)tc.m * BM, n0 = (int64_t)tc.n * BN;
     const int64_t nb = K / 16;  // scale groups per row
     const int64_t rb = K / 2;   // code bytes per row
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fp4_fast_kernel(
     const int lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
     const unsigned pid = xcd_order(blockIdx.x, gridDim.x);
-    const TileCoord tc = tile_at(pid, tiles_m, tiles_n, GROUP_M);
+    const TileCoord tc = tile_scalar<EPI>(tile_at(pid, tiles_m, tiles_n, GROUP_M));
     const int64_t m0 = (int64_t)tc.m * BM, n0 = (int64_t)tc.n * BN;
     const int64_t nb = K / 16, rb = K / 2;
     const int nk = (int)(nb / 4);
@@ -646,7 +646,7 @@ __device__ __forceinline__ void fp4dma_tile(const uint8_t *__restrict__ ca, cons
     const int lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
     const unsigned pid = xcd_order(blockIdx.x, gridDim.x);
-    const TileCoord tc = tile_at(pid, tiles_m, tiles_n, GROUP_M);
+    const TileCoord tc = tile_scalar<EPI>(tile_at(pid, tiles_m, tiles_n, GROUP_M));
     const int64_t m0 = (int64_t)tc.m * BM, n0 = (int64_t)tc.n * BN;
     if constexpr ((EPI & kEpiLora) != 0) lora_meta_dma(lora_of(ep).batch, lds + kLoraMetaOff, tid);
     v16f acc[4][4];
@@ -746,7 +746,8 @@ static hipError_t launch_fp4_paths(hipStream_t s, const uint8_t *ca, const uint8
     using namespace fp4gemm;
     static const hipError_t attr = [] {
         hipError_t e = allow_lds(gemm_fp4_f16_kernel<OUT, EPI>, epi_lds<EPI>(2 * STAGE));
-        if (e == hipSuccess) e = allow_lds(gemm_fp4_fast_kernel<OUT, EPI>, epi_lds<EPI>(2 * STAGE));
+        if constexpr ((EPI & kEpiLinear) == 0)
+            if (e == hipSuccess) e = allow_lds(gemm_fp4_fast_kernel<OUT, EPI>, epi_lds<EPI>(2 * STAGE));
         if (e == hipSuccess) e = allow_lds(gemm_fp4_dma_kernel<OUT, EPI>, epi_lds<EPI>(fp4dma::LDS_BYTES));
         if (e == hipSuccess) e = allow_lds(gemm_fp4_split_kernel, fp4dma::LDS_BYTES);
         if (e == hipSuccess) e = allow_lds(gemm_fp4_dma_tail_kernel<OUT, EPI>, epi_lds<EPI>(fp4dma::LDS_BYTES));
@@ -763,13 +764,16 @@ static hipError_t launch_fp4_paths(hipStream_t s, const uint8_t *ca, const uint8
     if (K % 128 == 0 && K >= 384)
         return launch_fp4_dma<OUT, EPI, true>(s, gemm_fp4_dma_tail_kernel<OUT, EPI>, gemm_fp4_split_tail_kernel, ca,
                                               sa, ga, cw, sw, gw, M, N, K, y, partial, spart, utm, utn, ep);
-    if (K % (4 * 16) == 0) {
-        hipLaunchKernelGGL((gemm_fp4_fast_kernel<OUT, EPI>), grid, block, epi_lds<EPI>(2 * STAGE), s, ca, sa, ga, cw,
-                           sw, gw, M, N, K, y, utm, utn, partial, ep);
-    } else {
-        hipLaunchKernelGGL((gemm_fp4_f16_kernel<OUT, EPI>), grid, block, epi_lds<EPI>(2 * STAGE), s, ca, sa, ga, cw,
-                           sw, gw, M, N, K, y, utm, utn, partial, ep);
+    // (the whole linear takes the form for any K: its smaller tiles have most of these)
+    if constexpr ((EPI & kEpiLinear) == 0) {
+        if (K % (4 * 16) == 0) {
+            hipLaunchKernelGGL((gemm_fp4_fast_kernel<OUT, EPI>), grid, block, epi_lds<EPI>(2 * STAGE), s, ca, sa, ga, cw,
+                               sw, gw, M, N, K, y, utm, utn, partial, ep);
+            return hipGetLastError();
+        }
     }
+    hipLaunchKernelGGL((gemm_fp4_f16_kernel<OUT, EPI>), grid, block, epi_lds<EPI>(2 * STAGE), s, ca, sa, ga, cw, sw, gw, M,
+                       N, K, y, utm, utn, partial, ep);
     return hipGetLastError();
 }
 

@@ -10,19 +10,16 @@ hipError_t launch_gemm_nvfp4_linear(hipStream_t s, const uint8_t *ca, const uint
     if (M == 0 || N == 0) return hipSuccess;
 #define DMPQ_LINEAR(OUT_, EPI_) \
     return launch_fp4_paths<OUT_, (EPI_)>(s, ca, sa, ga, cw, sw, gw, M, N, K, y, partial, spart, lin)
-    const int epi = kEpiLinear | (amax ? kEpiAmax : 0) | (lin.lora.t ? kEpiLora : 0) | (lin.qk.D ? kEpiHeads : 0);
-    if (out_dtype == 0) {
-        if (epi == kEpiLinear) DMPQ_LINEAR(0, kEpiLinear);
-        if (epi == (kEpiLinear | kEpiLora)) DMPQ_LINEAR(0, kEpiLinear | kEpiLora);
-    }
+    const int epi = linear_epi(amax, lin, N);
+    if ((epi & kEpiHeads) == 0 && (epi & kEpiLora) != 0)
+        return launch_gemm_nvfp4_linear_lora(s, ca, sa, ga, cw, sw, gw, M, N, K, out_dtype, y, partial, spart, lin, epi);
+    if (out_dtype == 0 && epi == kEpiLinear) DMPQ_LINEAR(0, kEpiLinear);
     if (out_dtype != 1) return hipErrorInvalidValue;
+    if ((epi & kEpiHeads) != 0)
+        return launch_gemm_nvfp4_linear_heads(s, ca, sa, ga, cw, sw, gw, M, N, K, y, partial, spart, lin, epi);
     switch (epi) {
         case kEpiLinear: DMPQ_LINEAR(1, kEpiLinear);
         case kEpiLinear | kEpiAmax: DMPQ_LINEAR(1, kEpiLinear | kEpiAmax);
-        case kEpiLinear | kEpiLora: DMPQ_LINEAR(1, kEpiLinear | kEpiLora);
-        case kEpiLinear | kEpiLora | kEpiAmax: DMPQ_LINEAR(1, kEpiLinear | kEpiLora | kEpiAmax);
-        case kEpiLinear | kEpiHeads: DMPQ_LINEAR(1, kEpiLinear | kEpiHeads);
-        case kEpiLinear | kEpiHeads | kEpiLora: DMPQ_LINEAR(1, kEpiLinear | kEpiHeads | kEpiLora);
     }
 #undef DMPQ_LINEAR
     return hipErrorInvalidValue;

@@ -126,6 +126,14 @@ struct LinearEpi {
     QkHeads qk;
     LoraEpi lora;
 };
+// Whether a QKV linear's heads are normed and rotated from registers
+// (gemm_common.hpp): heads of 64 or 128, whole 16-byte pieces of rows, no adapters,
+// and both members of every rotated pair, of which there is an even number, in a
+// lane (neighbours are, halves where they are the whole head).
+inline bool heads_from_regs(const LinearEpi &L, int64_t N) {
+    return !L.lora.t && N % 8 == 0 && N <= (int64_t(1) << 22) && L.qk.D != 32 &&
+           L.qk.P % 2 == 0 && (L.qk.layout == 0 || L.qk.P == 0 || 2 * L.qk.P == L.qk.D);
+}
 
 // epi: bit 0 GELU, bit 1 fused NVFP4 amax of the output into partial[tile]
 // (bf16 output only); the GEMM tile is 256 x 256 on every path.  spart: the
@@ -152,6 +160,21 @@ hipError_t launch_gemm_bf16(hipStream_t s, const uint16_t *x, const uint16_t *w,
 hipError_t launch_gemm_bf16_linear(hipStream_t s, const uint16_t *x, const uint16_t *w, int64_t M, int64_t N,
                                    int64_t K, int out_dtype, void *y, bool amax, float *partial, uint32_t *spart,
                                    const LinearEpi &lin);
+// their forms with adapters and with the heads of q and k (epi from linear_epi)
+hipError_t launch_gemm_nvfp4_linear_lora(hipStream_t s, const uint8_t *ca, const uint8_t *sa, const float *ga,
+                                         const uint8_t *cw, const uint8_t *sw, const float *gw, int64_t M, int64_t N,
+                                         int64_t K, int out_dtype, void *y, float *partial, uint32_t *spart,
+                                         const LinearEpi &lin, int epi);
+hipError_t launch_gemm_bf16_linear_heads(hipStream_t s, const uint16_t *x, const uint16_t *w, int64_t M, int64_t N,
+                                         int64_t K, void *y, float *partial, uint32_t *spart, const LinearEpi &lin,
+                                         int epi);
+hipError_t launch_gemm_int8_linear_heads(hipStream_t s, const int8_t *qa, const float *sa, const int8_t *qw,
+                                         const float *sw, int64_t M, int64_t N, int64_t K, void *y, float *partial,
+                                         uint32_t *spart, const LinearEpi &lin, int epi);
+hipError_t launch_gemm_nvfp4_linear_heads(hipStream_t s, const uint8_t *ca, const uint8_t *sa, const float *ga,
+                                          const uint8_t *cw, const uint8_t *sw, const float *gw, int64_t M, int64_t N,
+                                          int64_t K, void *y, float *partial, uint32_t *spart, const LinearEpi &lin,
+                                          int epi);
 // Fixup of a split launch with fp32 accumulators: y = (sum * gA) * gW (gA, gW
 // read from device memory; NULL reads as 1).
 hipError_t launch_f32_fixup(hipStream_t s, const float *ga, const float *gw, int64_t M, int64_t N,
@@ -162,6 +185,9 @@ hipError_t launch_f32_fixup_linear(hipStream_t s, const float *ga, const float *
                                    void *y, unsigned tiles_m, unsigned tiles_n, unsigned group_m,
                                    float *partial, const SplitPlan &sp, const uint32_t *spart,
                                    int out_dtype, int epi, const LinearEpi &lin);
+hipError_t launch_f32_fixup_linear_heads(hipStream_t s, const float *ga, const float *gw, int64_t M, int64_t N, void *y,
+                                         unsigned tiles_m, unsigned tiles_n, unsigned group_m, float *partial,
+                                         const SplitPlan &sp, const uint32_t *spart, int epi, const LinearEpi &lin);
 hipError_t launch_outlier_count(hipStream_t s, const uint16_t *x, int64_t M, int64_t K,
                                 double kappa, double *count, const Workspace &ws);
 // Sum ns values per partial over nparts partials, in a fixed order, into out[ns].
@@ -178,10 +204,8 @@ hipError_t launch_gemm_nvfp4_linear(hipStream_t s, const uint8_t *ca, const uint
                                     uint32_t *spart, const LinearEpi &lin);
 
 // ---- the whole linear: few rows, gradients; the heads of q and k ---------------
-// Rows up to which the whole linear takes the kernels that read each weight
-// once per 16 to 64 rows (linear.hip).
-constexpr int64_t kFewRows = 64;
-constexpr int64_t kMaxFewWidth = int64_t(1) << 26;
+// Few rows (linear.hip): widths and rows whose grids stay within 2^31 threads.
+constexpr int64_t kMaxFewWidth = int64_t(1) << 26, kMaxFewRows = int64_t(1) << 16;
 hipError_t launch_few_bf16(hipStream_t s, const uint16_t *x, const uint16_t *w, int64_t M, int64_t N, int64_t K,
                            int out_dtype, void *y, const LinearEpi &L);
 hipError_t launch_few_int8(hipStream_t s, const int8_t *qa, const float *sa, const int8_t *qw, const float *sw, int64_t M,
@@ -189,6 +213,16 @@ hipError_t launch_few_int8(hipStream_t s, const int8_t *qa, const float *sa, con
 hipError_t launch_few_nvfp4(hipStream_t s, const uint8_t *ca, const uint8_t *sa, const float *ga, const uint8_t *cw,
                             const uint8_t *sw, const float *gw, int64_t M, int64_t N, int64_t K, int out_dtype, void *y,
                             const LinearEpi &L);
+// Tiles of 64 and 128 (linear_mid.hpp); amax: the tiles' maxima, zero, or NULL.
+hipError_t launch_mid_bf16(hipStream_t s, const uint16_t *x, const uint16_t *w, int64_t M, int64_t N, int64_t K,
+                           int out_dtype, void *y, const LinearEpi &L, float *amax);
+hipError_t launch_mid_int8(hipStream_t s, const int8_t *qa, const float *sa, const int8_t *qw, const float *sw, int64_t M,
+                           int64_t N, int64_t K, int out_dtype, void *y, const LinearEpi &L, float *amax);
+hipError_t launch_mid_nvfp4(hipStream_t s, const uint8_t *ca, const uint8_t *sa, const float *ga, const uint8_t *cw,
+                            const uint8_t *sw, const float *gw, int64_t M, int64_t N, int64_t K, int out_dtype, void *y,
+                            const LinearEpi &L, float *amax);
+// p[0 .. n-1] = 0 (a kernel, so that graphs may hold it)
+hipError_t launch_zero(hipStream_t s, float *p, int64_t n);
 // du, dgate and dbias may be NULL, pre where neither act nor dgate needs it;
 // gate_start NULL: one row of the gate for all.
 struct LinearGrad {

@@ -278,6 +278,15 @@ hipError_t launch_few_nvfp4(hipStream_t s, const uint8_t *ca, const uint8_t *sa,
     return launch_skinny<SkinnyFP4>(s, {ca, sa, ga, cw, sw, gw}, M, N, K, out_dtype, y, L);
 }
 
+__global__ __launch_bounds__(256) void zero_kernel(float *__restrict__ p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0.0f;
+}
+
+hipError_t launch_zero(hipStream_t s, float *p, int64_t n) {
+    hipLaunchKernelGGL(zero_kernel, dim3(stride_grid(n, 256, 256)), dim3(256), 0, s, p, n);
+    return hipGetLastError();
+}
+
 // ---------------------------------------------------------------------------
 // Gradients of y = residual + gate[s] * act(pre):
 //   du = gate[s] act'(pre) dy            (0 in rows of no request)

@@ -78,14 +78,14 @@ template <int N>
 __device__ __forceinline__ void load_values(const void *p, bool bf16, int64_t at, int64_t left, float (&v)[N]) {
 #pragma unroll
     for (int i = 0; i < N; i++) v[i] = 0.0f;
-    if (left >= N && at % N == 0) {
+    if (N >= 4 && left >= N && at % N == 0) {
         if (bf16) {
             const uint16_t *q = static_cast<const uint16_t *>(p) + at;
-            uint32_t w[N / 2];
+            uint32_t w[N / 2] = {};
             if constexpr (N == 8) {
                 const uint4 u = *reinterpret_cast<const uint4 *>(q);
                 w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-            } else {
+            } else if constexpr (N == 4) {
                 const uint2 u = *reinterpret_cast<const uint2 *>(q);
                 w[0] = u.x, w[1] = u.y;
             }
@@ -93,7 +93,7 @@ __device__ __forceinline__ void load_values(const void *p, bool bf16, int64_t at
             for (int i = 0; i < N / 2; i++) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
         } else {
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
+            for (int i = 0; i + 3 < N; i += 4) {
                 const float4 u = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at + i);
                 v[i] = u.x, v[i + 1] = u.y, v[i + 2] = u.z, v[i + 3] = u.w;
             }
@@ -302,6 +302,23 @@ __device__ __forceinline__ void fetch_values(const void *p, int64_t at, int64_t 
     }
 }
 
+// The same as they lie, 16 bytes.
+template <int ESIZE>
+__device__ __forceinline__ uint4 fetch_raw(const void *p, int64_t at, int64_t left, bool vec) {
+    constexpr int N = 16 / ESIZE;
+    if (vec && left >= N) return load_nt16(static_cast<const uint8_t *>(p) + at * ESIZE);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < N; i++)
+        if (i < left) {
+            if constexpr (ESIZE == 4)
+                w[i] = static_cast<const uint32_t *>(p)[at + i];
+            else
+                w[i >> 1] |= (uint32_t) static_cast<const uint16_t *>(p)[at + i] << (16 * (i & 1));
+        }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // What a lane that holds the N columns from `col` on keeps over its rows: the
 // bias, and the gate where all rows belong to one request.
 enum { kGateNone = 0, kGateOne = 1, kGateZero = 2, kGateMixed = 3 };
@@ -328,10 +345,10 @@ struct LinearLane {
         }
     }
     // gate and residual of one row: v becomes y.  in: the lane has columns there;
-    // request: of the row, for kGateMixed.
+    // request: of the row, for kGateMixed; ahead: its residual, where it is loaded already.
     template <int ESIZE>
     __device__ __forceinline__ void finish(const LinearEpi &L, int64_t row, int64_t N_, int64_t col, bool in, bool vec,
-                                           int request, float (&v)[N]) const {
+                                           int request, float (&v)[N], const uint4 *ahead = nullptr) const {
         if (mode == kGateOne) {
 #pragma unroll
             for (int i = 0; i < N; i++) v[i] *= gate[i];
@@ -349,7 +366,14 @@ struct LinearLane {
         }
         if (L.residual && in) {
             float r[N];
-            fetch_values<ESIZE, N>(L.residual, row * N_ + col, N_ - col, vec, r);
+            if (ahead) {
+                const uint32_t w[4] = {ahead->x, ahead->y, ahead->z, ahead->w};
+#pragma unroll
+                for (int i = 0; i < N; i++)
+                    r[i] = ESIZE == 4 ? __uint_as_float(w[i & 3]) : i & 1 ? bf16_hi(w[i >> 1 & 3]) : bf16_lo(w[i >> 1 & 3]);
+            } else {
+                fetch_values<ESIZE, N>(L.residual, row * N_ + col, N_ - col, vec, r);
+            }
 #pragma unroll
             for (int i = 0; i < N; i++) v[i] += r[i];
         }

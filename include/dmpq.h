@@ -573,8 +573,8 @@ dmpq_status dmpq_adamw_step(hipStream_t stream, const void *d_table, int64_t n_t
  * flags.  pre is what dmpq_qk_norm_rope_backward takes as q and k.
  * flags: DMPQ_EPI_NVFP4_AMAX as in the *_ex GEMMs (bf16 output, N % 16 == 0).
  * out_dtype F32 or BF16.  ws as in the *_ex GEMMs (NULL: no tail split).
- * Up to 64 rows without flags take kernels of their own, which read the weight
- * once over the whole chip and need no workspace.
+ * Few rows and short batches take kernels of their own, which need no workspace
+ * but for flags.
  * ========================================================================= */
 enum { DMPQ_ACT_NONE = 0, DMPQ_ACT_GELU = 1, DMPQ_ACT_GELU_TANH = 2, DMPQ_ACT_SILU = 3 };
 enum { DMPQ_NORM_NONE = 0, DMPQ_NORM_RMS = 1, DMPQ_NORM_LAYER = 2 };
