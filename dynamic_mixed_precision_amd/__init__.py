@@ -10,6 +10,7 @@ tensors are allocated by the caller, as the C ABI requires.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import numpy as np
@@ -518,7 +519,7 @@ def _load_types():
     8-bit codes also as bytes."""
     global _types
     import torch
-    _types = {"fp32": frozenset((torch.float32,)), "int32": frozenset((torch.int32,)),
+    _types = {"fp32": frozenset((torch.float32,)), "fp64": frozenset((torch.float64,)), "int32": frozenset((torch.int32,)),
               "bf16": frozenset((torch.bfloat16, torch.int16, torch.uint16)),
               "E4M3": frozenset((torch.float8_e4m3fn, torch.uint8, torch.int8))}
     return _types
@@ -929,6 +930,11 @@ def linear_epilogue_backward(dy, pre, du, ws=None, act: int = ACT_NONE, gate=Non
 
 # ---- the heads of q and k ---------------------------------------------------------
 
+@functools.lru_cache(64)
+def _int32s(values: tuple):
+    return (C.c_int32 * len(values))(*values)
+
+
 def rope_table(pos, freqs, axis_pairs, table, stream=None) -> None:
     """table [M, P, 2] fp32 = (cos, sin) of pos[m, axis] * freqs[p]: pos [M, axes]
     int32 or fp32, freqs [P] fp64 (radians per position), axis_pairs: how many of
@@ -940,11 +946,11 @@ def rope_table(pos, freqs, axis_pairs, table, stream=None) -> None:
     kind = OUT_F32 if pos.dtype in kinds["fp32"] else OUT_I32 if pos.dtype in kinds["int32"] else None
     if kind is None:
         raise ValueError(f"pos is {pos.dtype}, needs int32 or fp32")
-    if str(freqs.dtype) != "torch.float64":
+    if freqs.dtype not in kinds["fp64"]:
         raise ValueError(f"freqs is {freqs.dtype}, needs fp64")
     _need(freqs, "freqs", 8 * P)
     _need_type(table, "table", 8 * M * P, "fp32")
-    pairs = (C.c_int32 * len(axis_pairs))(*axis_pairs)
+    pairs = _int32s(tuple(axis_pairs))
     _check(lib().dmpq_rope_table(_stream(stream), _ptr(pos), kind, _ptr(freqs), M, len(axis_pairs), pairs,
                                  _ptr(table)), "dmpq_rope_table")
 
@@ -955,7 +961,7 @@ def _rows(t, name: str, M: int, n: int, dim: int, kind: str):
         if n * M > 0:
             raise ValueError(f"{name} is missing")
         return None, n * dim
-    if tuple(t.shape) != (M, n, dim):
+    if t.shape != (M, n, dim):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {(M, n, dim)}")
     if t.dtype not in (_types or _load_types())[kind]:
         raise ValueError(f"{name} is {t.dtype}, needs {kind}")
@@ -964,7 +970,7 @@ def _rows(t, name: str, M: int, n: int, dim: int, kind: str):
     st = t.stride()
     if (dim > 1 and st[2] != 1) or (n > 1 and st[1] != dim):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return (t.data_ptr() if t.numel() else None), (st[0] if M > 1 else n * dim)
+    return (t.data_ptr() if M and n else None), (st[0] if M > 1 else n * dim)
 
 
 def _qk_shape(q, k, heads: QkHeads):

@@ -338,11 +338,14 @@ struct BandPlace {
     int64_t base, step;  // bytes: of the band's first row and column in y, pre and the residual; of a pass
     uint32_t off;        // the lane's
     int rows;            // there are, from the lane's on; none for lanes whose columns are past the end
+    int last;            // the band's last row, or its first where there is none
     __device__ __forceinline__ BandPlace(int64_t M, int64_t N, int64_t row0, int64_t col0, int lane, int most) {
         const int lr = lane / LPR, chunk = lane % LPR;
         base = (row0 * N + col0) * ESIZE, step = RPP * N * ESIZE;
         off = (uint32_t)lr * (uint32_t)N * ESIZE + 16 * chunk;
-        rows = col0 + chunk * PER < N ? (int)(M - row0 < most ? M - row0 : most) - lr : 0;
+        const int count = M <= row0 ? 0 : (int)(M - row0 < most ? M - row0 : most);
+        rows = col0 + chunk * PER < N ? count - lr : 0;
+        last = count > 0 ? count - 1 : 0;
     }
     // the residual of group g
     __device__ __forceinline__ void ahead(const LinearEpi &L, int g, uint4 (&r)[GROUP]) const {
@@ -368,7 +371,13 @@ __device__ __forceinline__ float linear_band_rows(const uint8_t *band, void *y, 
     const uint8_t *src = band + lr * kLoraBandStride + 4 * PER * chunk;
     uint8_t *py = uniform_ptr(static_cast<uint8_t *>(y) + B.base), *pp = nullptr;
     if (MORE && L.pre) pp = uniform_ptr(static_cast<uint8_t *>(L.pre) + B.base);
-    float amax = 0.0f;
+    float amax = 0.0f, gate[PER];
+    int requests = 0, held = -2;  // of the band's rows, in its first ROWS lanes; the one whose gate the lane has
+    if constexpr (MORE) {
+#pragma unroll
+        for (int i = 0; i < PER; i++) gate[i] = T.gate[i];
+        if (T.mode == kGateMixed) requests = request_of(L.gate_start, L.S, (int)(row0 + (lane < B.last ? lane : B.last)));
+    }
 #pragma unroll 1
     for (int g = 0; g < ROWS / RPP / GROUP; g++) {
         uint4 next[GROUP];
@@ -396,18 +405,22 @@ __device__ __forceinline__ float linear_band_rows(const uint8_t *band, void *y, 
             if (MORE && pp) store(pp);
             act_apply<PER>(v, ACT);
             if constexpr (MORE) {
+                if (T.mode == kGateMixed) {
+                    // the gate of the lane's row is loaded where a row's request is not the one before it
+                    const int s = __shfl(requests, (g * GROUP + k) * RPP + lr, 64);
+                    if (__any(s != held)) {
+                        held = s;
+                        if (s >= 0 && s < L.S && in) load_values<PER>(L.gate, L.gate_bf16, s * N + col0 + chunk * PER, PER, gate);
+                    }
+                }
                 if (T.mode == kGateOne) {
 #pragma unroll
-                    for (int i = 0; i < PER; i++) v[i] *= T.gate[i];
+                    for (int i = 0; i < PER; i++) v[i] *= gate[i];
                 } else if (T.mode != kGateNone) {
                     // rows of no request take no term at all, not zero times one
-                    const int row = (int)row0 + (g * GROUP + k) * RPP + lr;
-                    const int s = T.mode == kGateMixed && in ? request_of(L.gate_start, L.S, row) : -1;
-                    const bool some = s >= 0 && s < L.S;
-                    float w[PER];
-                    if (some) load_values<PER>(L.gate, L.gate_bf16, s * N + col0 + chunk * PER, PER, w);
+                    const bool some = T.mode == kGateMixed && held >= 0 && held < L.S;
 #pragma unroll
-                    for (int i = 0; i < PER; i++) v[i] = some ? v[i] * w[i] : L.residual ? -0.0f : 0.0f;
+                    for (int i = 0; i < PER; i++) v[i] = some ? v[i] * gate[i] : L.residual ? -0.0f : 0.0f;
                 }
                 if (L.residual) {
                     const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};

@@ -301,53 +301,64 @@ hipError_t launch_zero(hipStream_t s, float *p, int64_t n) {
 // ---------------------------------------------------------------------------
 namespace lgrad {
 constexpr int COLS = 512;  // columns of a wave
+constexpr int DEEP = 4;    // rows on their way together
 }
 
 // act(v) and act'(v).  Far out the derivative is its limit and what it is made
-// of would be infinity times zero, so it is taken at +-kActFar at most, where
-// e^-kActFar is 0 in fp32.
+// of would be infinity times zero, so the factors that grow are taken at
+// +-kActFar at most, where e^-kActFar is 0 in fp32 (NaN stays: it comes with the
+// exponential).  The sigmoids share one exponential: with E = e^-z,
+// s(z) = 1 / (1 + E) and s(-z) = E s(z); where E is past 1e30 s(z) is nothing next to it.
 constexpr float kActFar = 128.0f;
-__device__ __forceinline__ void act_and_slope(float v, int act, float &a, float &d) {
-    a = v, d = 1.0f;
-    if (act == kActNone) return;
-    // (NaN stays: a comparison with it is false)
-    const float u = v > kActFar ? kActFar : v < -kActFar ? -kActFar : v;
-    if (act == kActGelu) {
+template <int ACT>
+__device__ __forceinline__ void act_and_slope(float v, float &a, float &d) {
+    if constexpr (ACT == kActNone) {
+        a = v, d = 1.0f;
+    } else if constexpr (ACT == kActGelu) {
+        const float u = v > kActFar ? kActFar : v < -kActFar ? -kActFar : v;
         const float phi2 = gelu_phi2(u);
         a = 0.5f * v * phi2;
         d = 0.5f * phi2 + u * 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.5f * kLog2e * u * u);
     } else {
-        const float z = act == kActSilu ? u : gelu_tanh_arg(u), e = sigmoid_f32(z), f = sigmoid_f32(-z);
+        const float u = __builtin_amdgcn_fmed3f(v, -kActFar, kActFar);
+        const float t = ACT == kActSilu ? -kLog2e * v : gelu_tanh_exponent(v);
+        const float E = __builtin_amdgcn_exp2f(t), e = __builtin_amdgcn_rcpf(1.0f + E);
+        const float f = __builtin_fminf(E, 1e30f) * e;
         a = v * e;
-        d = __builtin_fmaf(u * e * f, act == kActSilu ? 1.0f : kGt * __builtin_fmaf(0.134145f * u, u, 1.0f), e);
+        d = __builtin_fmaf(u * e * f, ACT == kActSilu ? 1.0f : __builtin_fmaf(kGt * 0.134145f * u, u, kGt), e);
     }
 }
 
 // VEC: rows are 16-byte aligned and a lane has 8 columns in a row; otherwise
 // its columns are 64 apart, so that every access of a wave is contiguous.
 template <int ES, bool VEC>
-__device__ __forceinline__ void grad_load(const void *p, int64_t row, int64_t N, const int64_t (&cols)[8], float (&v)[8]) {
-    if constexpr (VEC) {
-        if (cols[0] < N) {
-            float a[16 / ES], b[16 / ES];
-            fetch_values<ES, 16 / ES>(p, row * N + cols[0], 16 / ES, true, a);
-            if constexpr (ES == 4) fetch_values<ES, 4>(p, row * N + cols[0] + 4, N - cols[0] - 4, true, b);
+struct GradValues {  // as they lie, so that many rows fit the registers
+    static constexpr int WORDS = ES == 2 && VEC ? 4 : 8;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const void *p, int64_t row, int64_t N, const int64_t (&cols)[8]) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = i < 16 / ES ? a[i & (16 / ES - 1)] : b[i & (16 / ES - 1)];
+        for (int i = 0; i < WORDS; i++) w[i] = 0;
+        if constexpr (VEC) {
+            const uint8_t *q = static_cast<const uint8_t *>(p) + (row * N + cols[0]) * ES;
+#pragma unroll
+            for (int i = 0; i < WORDS; i += 4)
+                if (cols[i] < N) {
+                    const uint4 u = load_nt16(q + 4 * i);
+                    w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
+                }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = 0.0f;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            v[i] = 0.0f;
-            if (cols[i] < N)
-                v[i] = ES == 4 ? static_cast<const float *>(p)[row * N + cols[i]]
-                               : __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[row * N + cols[i]] << 16);
+            for (int i = 0; i < 8; i++)
+                if (cols[i] < N)
+                    w[i] = ES == 4 ? static_cast<const uint32_t *>(p)[row * N + cols[i]]
+                                   : (uint32_t) static_cast<const uint16_t *>(p)[row * N + cols[i]] << 16;
         }
     }
-}
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (WORDS == 8) return __uint_as_float(w[i]);
+        return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+    }
+};
 
 template <int ES, bool VEC>
 __device__ __forceinline__ void grad_store(void *p, int64_t row, int64_t N, const int64_t (&cols)[8], const float (&v)[8]) {
@@ -381,7 +392,7 @@ __device__ __forceinline__ void grad_sums(float *out, int64_t at, int64_t N, con
         if (cols[i] < N) out[at * N + cols[i]] = v[i];
 }
 
-template <int ES, bool VEC>
+template <int ES, bool VEC, int ACT>
 __global__ __launch_bounds__(256) void linear_grad_kernel(LinearGrad G, int64_t M, int64_t N, int rows, int64_t chunks,
                                                           float *__restrict__ bias_part, float *__restrict__ gate_part) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -422,41 +433,38 @@ __global__ __launch_bounds__(256) void linear_grad_kernel(LinearGrad G, int64_t 
                     g[i] = G.gate_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(G.gate)[s * N + cols[i]] << 16)
                                        : static_cast<const float *>(G.gate)[s * N + cols[i]];
             }
-            auto one = [&](int64_t r, const float (&dy)[8], const float (&u)[8]) {
+            typedef GradValues<ES, VEC> Row;
+            auto one = [&](int64_t r, const Row &dy, const Row &pre) {
                 float o[8];
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     float a, d;
-                    act_and_slope(u[i], G.act, a, d);
-                    dg[i] = __builtin_fmaf(dy[i], a, dg[i]);
-                    o[i] = g[i] * dy[i] * d;
+                    act_and_slope<ACT>(pre.get(i), a, d);
+                    dg[i] = __builtin_fmaf(dy.get(i), a, dg[i]);
+                    o[i] = g[i] * dy.get(i) * d;
                     db[i] += o[i];
                 }
                 if (G.du) grad_store<ES, VEC>(G.du, r, N, cols, o);
             };
-            auto pre_of = [&](int64_t r, float (&u)[8]) {
+            constexpr int DEEP = lgrad::DEEP;
+            for (; row + DEEP <= end; row += DEEP) {
+                Row dy[DEEP], u[DEEP];
+#pragma unroll
+                for (int k = 0; k < DEEP; k++) dy[k].load(G.dy, row + k, N, cols);
                 if (G.pre) {
-                    grad_load<ES, VEC>(G.pre, r, N, cols, u);
+#pragma unroll
+                    for (int k = 0; k < DEEP; k++) u[k].load(G.pre, row + k, N, cols);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; i++) u[i] = 0.0f;
-                }
-            };
-            constexpr int DEEP = 4;
-            for (; row + DEEP <= end; row += DEEP) {
-                float dy[DEEP][8], u[DEEP][8];
-#pragma unroll
-                for (int k = 0; k < DEEP; k++) {
-                    grad_load<ES, VEC>(G.dy, row + k, N, cols, dy[k]);
-                    pre_of(row + k, u[k]);
+                    for (int k = 0; k < DEEP; k++) u[k] = Row();
                 }
 #pragma unroll
                 for (int k = 0; k < DEEP; k++) one(row + k, dy[k], u[k]);
             }
             for (; row < end; row++) {
-                float dy[8], u[8];
-                grad_load<ES, VEC>(G.dy, row, N, cols, dy);
-                pre_of(row, u);
+                Row dy, u = Row();
+                dy.load(G.dy, row, N, cols);
+                if (G.pre) u.load(G.pre, row, N, cols);
                 one(row, dy, u);
             }
             if (G.dgate) grad_sums(gate_part, chunk + s, N, cols, dg);
@@ -523,15 +531,23 @@ hipError_t launch_linear_grad(hipStream_t s, const LinearGrad &G, int64_t M, int
     const bool vec = (N * (dtype == 0 ? 4 : 2)) % 16 == 0;
     if (M > 0) {
         const dim3 grid((unsigned)((chunks + 3) / 4), (unsigned)(blocks < 65535 ? blocks : 65535));
-#define DMPQ_GRAD(ES_, VEC_) \
-    hipLaunchKernelGGL((linear_grad_kernel<ES_, VEC_>), grid, dim3(256), 0, s, G, M, N, rows, chunks, bias_part, gate_part)
+#define DMPQ_GRAD(ES_, VEC_, ACT_) \
+    hipLaunchKernelGGL((linear_grad_kernel<ES_, VEC_, ACT_>), grid, dim3(256), 0, s, G, M, N, rows, chunks, bias_part, gate_part)
+#define DMPQ_GRAD_ACT(ES_, VEC_)                          \
+    switch (G.act) {                                      \
+        case kActNone: DMPQ_GRAD(ES_, VEC_, kActNone); break;         \
+        case kActGelu: DMPQ_GRAD(ES_, VEC_, kActGelu); break;         \
+        case kActGeluTanh: DMPQ_GRAD(ES_, VEC_, kActGeluTanh); break; \
+        default: DMPQ_GRAD(ES_, VEC_, kActSilu);          \
+    }
         if (dtype == 0) {
-            if (vec) DMPQ_GRAD(4, true);
-            else DMPQ_GRAD(4, false);
+            if (vec) DMPQ_GRAD_ACT(4, true)
+            else DMPQ_GRAD_ACT(4, false)
         } else {
-            if (vec) DMPQ_GRAD(2, true);
-            else DMPQ_GRAD(2, false);
+            if (vec) DMPQ_GRAD_ACT(2, true)
+            else DMPQ_GRAD_ACT(2, false)
         }
+#undef DMPQ_GRAD_ACT
 #undef DMPQ_GRAD
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;

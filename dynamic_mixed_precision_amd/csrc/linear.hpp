@@ -52,7 +52,10 @@ __device__ __forceinline__ float sigmoid_f32(float z) {
 
 // GELU with tanh, v / 2 (1 + tanh(u)) = v sigmoid(2u), 2u = kGt (v + 0.044715 v^3)
 constexpr float kGt = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-__device__ __forceinline__ float gelu_tanh_arg(float v) { return kGt * __builtin_fmaf(0.044715f * v * v, v, v); }
+// the exponent of e^-2u as a power of 2
+__device__ __forceinline__ float gelu_tanh_exponent(float v) {
+    return v * __builtin_fmaf(-kLog2e * kGt * 0.044715f, v * v, -kLog2e * kGt);
+}
 
 enum { kActNone = 0, kActGelu = 1, kActGeluTanh = 2, kActSilu = 3 };
 
@@ -64,7 +67,7 @@ __device__ __forceinline__ void act_apply(float (&v)[N], int act) {
         for (int i = 0; i < N; i++) v[i] = gelu_f32(v[i]);
     } else if (act == kActGeluTanh) {
 #pragma unroll
-        for (int i = 0; i < N; i++) v[i] *= sigmoid_f32(gelu_tanh_arg(v[i]));
+        for (int i = 0; i < N; i++) v[i] *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(gelu_tanh_exponent(v[i])));
     } else if (act == kActSilu) {
 #pragma unroll
         for (int i = 0; i < N; i++) v[i] *= sigmoid_f32(v[i]);

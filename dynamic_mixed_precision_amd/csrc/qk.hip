@@ -25,31 +25,28 @@ namespace dmpq {
 __global__ __launch_bounds__(256) void rope_table_kernel(const void *__restrict__ pos, int pos_f32, RopeAxes ax,
                                                          const double *__restrict__ freq, int64_t M, int P,
                                                          float2 *__restrict__ table) {
-    const int64_t total = M * P, per = 1024;
+    const int64_t total = M * P, per = 256;
     for (int64_t base = (int64_t)blockIdx.x * per; base < total; base += (int64_t)gridDim.x * per) {
         const int64_t m0 = base / P;
         const unsigned p0 = (unsigned)(base - m0 * P);
+        const unsigned o = p0 + threadIdx.x;
+        const int64_t m = m0 + o / (unsigned)P;
+        const int p = (int)(o % (unsigned)P);
+        if (m >= M) continue;
+        int a = 0;
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-            const unsigned o = p0 + 256 * k + threadIdx.x;
-            const int64_t m = m0 + o / (unsigned)P;
-            const int p = (int)(o % (unsigned)P);
-            if (m >= M) continue;
-            int a = 0;
-#pragma unroll
-            for (int i = 0; i < kMaxRopeAxes - 1; i++) a += i < ax.n - 1 && p >= ax.end[i];
-            const double at = pos_f32 ? (double)static_cast<const float *>(pos)[m * ax.n + a]
-                                      : (double)static_cast<const int32_t *>(pos)[m * ax.n + a];
-            const double turns = at * freq[p] * 0.15915494309189533577;
-            const double quarter = __builtin_rint(4.0 * turns);
-            const float r = (float)(turns - 0.25 * quarter);
-            float s, c;
-            sincospif(2.0f * r, &s, &c);
-            // which quarter: by a remainder in 64 bits, as it may pass 2^31
-            const int q = (int)(quarter - 4.0 * __builtin_floor(0.25 * quarter));
-            const float cs = q & 1 ? s : c, sn = q & 1 ? c : s;
-            table[m * P + p] = make_float2(q == 1 || q == 2 ? -cs : cs, q >= 2 ? -sn : sn);
-        }
+        for (int i = 0; i < kMaxRopeAxes - 1; i++) a += i < ax.n - 1 && p >= ax.end[i];
+        const double at = pos_f32 ? (double)static_cast<const float *>(pos)[m * ax.n + a]
+                                  : (double)static_cast<const int32_t *>(pos)[m * ax.n + a];
+        const double turns = at * freq[p] * 0.15915494309189533577;
+        const double quarter = __builtin_rint(4.0 * turns);
+        const float r = (float)(turns - 0.25 * quarter);
+        float s, c;
+        sincospif(2.0f * r, &s, &c);
+        // which quarter: by a remainder in 64 bits, as it may pass 2^31
+        const int q = (int)(quarter - 4.0 * __builtin_floor(0.25 * quarter));
+        const float cs = q & 1 ? s : c, sn = q & 1 ? c : s;
+        table[m * P + p] = make_float2(q == 1 || q == 2 ? -cs : cs, q >= 2 ? -sn : sn);
     }
 }
 
@@ -57,7 +54,7 @@ hipError_t launch_rope_table(hipStream_t s, const void *pos, bool pos_f32, const
                              float *table) {
     const int P = ax.end[ax.n - 1];
     if (M == 0 || P == 0) return hipSuccess;
-    hipLaunchKernelGGL(rope_table_kernel, dim3(stride_grid(M * P, 1024, 1u << 16)), dim3(256), 0, s, pos, pos_f32 ? 1 : 0, ax,
+    hipLaunchKernelGGL(rope_table_kernel, dim3(stride_grid(M * P, 256, 1u << 18)), dim3(256), 0, s, pos, pos_f32 ? 1 : 0, ax,
                        freq, M, P, reinterpret_cast<float2 *>(table));
     return hipGetLastError();
 }
@@ -179,11 +176,13 @@ __device__ __forceinline__ float norm8(const QkHeads &H, bool live, const float 
 }
 
 // The steps of a row: 64 / G heads of q each, then of k.  A wave takes `per`
-// consecutive steps of one row.
+// consecutive steps of one row, one after the other: a full chip of waves keeps
+// more loads on their way than several steps of fewer waves do (17776 rows of 30 +
+// 30 heads of 64, bf16, with the table: 1 / 2 / 4 / 8 steps at once 61 / 62 / 74 / 85 us).
 template <int ES, int LAYOUT, int G>
 __global__ __launch_bounds__(256) void qk_kernel(QkTensors T, QkHeads H, int64_t M, int sq, int steps, int per,
                                                  int64_t units, int parts) {
-    constexpr int HEADS = 64 / G, DEEP = 4;
+    constexpr int HEADS = 64 / G;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
     if (unit >= units) return;
@@ -203,34 +202,20 @@ __global__ __launch_bounds__(256) void qk_kernel(QkTensors T, QkHeads H, int64_t
         float w[8], b[8];
         L.weights(side ? H.wk : H.wq, H.w_bf16, 1.0f, w);
         L.weights(side ? H.bk : H.bq, H.w_bf16, 0.0f, b);
-        for (int st = s0; st < s1; st += DEEP) {
-            float v[DEEP][8];
-            int64_t h[DEEP];
-            bool on[DEEP];
+        for (int st = s0; st < s1; st++) {
+            const int head = (st - base) * HEADS + slot;
+            const bool on = L.live && head < heads;
+            const int64_t h = (int64_t)head * H.D;
+            float v[8] = {};
+            if (on) L.template load<ES>(x, at + h, v);
+            if (H.norm != 0) {
+                float n[8];
+                norm8<G>(H, L.live, v, n);
 #pragma unroll
-            for (int d = 0; d < DEEP; d++) {
-                const int head = (st + d - base) * HEADS + slot;
-                on[d] = L.live && st + d < s1 && head < heads;
-                h[d] = (int64_t)head * H.D;
-                if (on[d]) {
-                    L.template load<ES>(x, at + h[d], v[d]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; i++) v[d][i] = 0.0f;
-                }
+                for (int i = 0; i < 8; i++) v[i] = __builtin_fmaf(n[i], w[i], b[i]);
             }
-#pragma unroll
-            for (int d = 0; d < DEEP; d++) {
-                if (st + d >= s1) break;
-                if (H.norm != 0) {
-                    float n[8];
-                    norm8<G>(H, L.live, v[d], n);
-#pragma unroll
-                    for (int i = 0; i < 8; i++) v[d][i] = __builtin_fmaf(n[i], w[i], b[i]);
-                }
-                t.apply<LAYOUT, false>(v[d]);
-                if (on[d]) L.template store<ES>(y, to + h[d], v[d]);
-            }
+            t.apply<LAYOUT, false>(v);
+            if (on) L.template store<ES>(y, to + h, v);
         }
     }
 }
@@ -238,13 +223,15 @@ __global__ __launch_bounds__(256) void qk_kernel(QkTensors T, QkHeads H, int64_t
 // The gradients.  With g' = the rotation's transpose of g, h = g' w, r = the norm's factor:
 //   dx = r (h - mean(h) - n mean(h n))   (RMS: without mean(h));  dw += g' n;  db += g'
 // The weights' sums stay in registers over all a wave's rows, and each
-// workgroup stores its own; a second kernel adds them in order.
+// workgroup stores its own; a second kernel adds them in order.  Four workgroups a
+// CU (17776 rows of 30 + 30 heads of 64, bf16, with the second kernel: 2 / 3 / 4 / 5 / 8 a CU
+// 108 / 89 / 81 / 97 / 90 us; two steps at once 120, four 130).
 constexpr int kQkGroups = 1024;
 
 template <int ES, int LAYOUT, int G>
 __global__ __launch_bounds__(256) void qk_grad_kernel(QkTensors T, QkHeads H, int64_t M, int sq, int steps, int per,
                                                       int64_t units, int parts, float *__restrict__ part) {
-    constexpr int HEADS = 64 / G, DEEP = 2;
+    constexpr int HEADS = 64 / G;
     __shared__ float red[4][4][kMaxHeadDim];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int sub = lane % G, slot = lane / G;
@@ -268,47 +255,36 @@ __global__ __launch_bounds__(256) void qk_grad_kernel(QkTensors T, QkHeads H, in
             const int64_t at = m * (side ? T.ldk : T.ldq), gat = m * (side ? T.lddk : T.lddq),
                           to = m * (side ? T.ldk_out : T.ldq_out);
             const int heads = side ? H.nk : H.nq, base = side ? sq : 0;
-            for (int st = s0; st < s1; st += DEEP) {
-                float v[DEEP][8], e[DEEP][8];
-                int64_t h[DEEP];
-                bool on[DEEP];
-#pragma unroll
-                for (int d = 0; d < DEEP; d++) {
-                    const int head = (st + d - base) * HEADS + slot;
-                    on[d] = L.live && st + d < s1 && head < heads;
-                    h[d] = (int64_t)head * H.D;
-#pragma unroll
-                    for (int i = 0; i < 8; i++) v[d][i] = e[d][i] = 0.0f;
-                    if (on[d]) {
-                        L.template load<ES>(g, gat + h[d], e[d]);
-                        if (H.norm != 0) L.template load<ES>(x, at + h[d], v[d]);
-                    }
+            for (int st = s0; st < s1; st++) {
+                const int head = (st - base) * HEADS + slot;
+                const bool on = L.live && head < heads;
+                const int64_t h = (int64_t)head * H.D;
+                float v[8] = {}, e[8] = {};
+                if (on) {
+                    L.template load<ES>(g, gat + h, e);
+                    if (H.norm != 0) L.template load<ES>(x, at + h, v);
                 }
+                t.apply<LAYOUT, true>(e);
+                if (H.norm != 0) {
+                    float n[8], k[8];
+                    const float r = norm8<G>(H, L.live, v, n);
+                    float mh = 0.0f, mn = 0.0f;
 #pragma unroll
-                for (int d = 0; d < DEEP; d++) {
-                    if (st + d >= s1) break;
-                    t.apply<LAYOUT, true>(e[d]);
-                    if (H.norm != 0) {
-                        float n[8], k[8];
-                        const float r = norm8<G>(H, L.live, v[d], n);
-                        float mh = 0.0f, mn = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            if (on[d]) {  // (a head that is not there has n = 0 r, which eps 0 makes NaN)
-                                dw[side][i] = __builtin_fmaf(e[d][i], n[i], dw[side][i]);
-                                db[side][i] += e[d][i];
-                            }
-                            k[i] = e[d][i] * w[side][i];
-                            mh += k[i];
-                            mn = __builtin_fmaf(k[i], n[i], mn);
+                    for (int i = 0; i < 8; i++) {
+                        if (on) {  // (a head that is not there has n = 0 r, which eps 0 makes NaN)
+                            dw[side][i] = __builtin_fmaf(e[i], n[i], dw[side][i]);
+                            db[side][i] += e[i];
                         }
-                        mn = head_sum<G>(L.live ? mn : 0.0f) * inv;
-                        mh = H.norm == 2 ? head_sum<G>(L.live ? mh : 0.0f) * inv : 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 8; i++) e[d][i] = r * (k[i] - mh - n[i] * mn);
+                        k[i] = e[i] * w[side][i];
+                        mh += k[i];
+                        mn = __builtin_fmaf(k[i], n[i], mn);
                     }
-                    if (on[d]) L.template store<ES>(y, to + h[d], e[d]);
+                    mn = head_sum<G>(L.live ? mn : 0.0f) * inv;
+                    mh = H.norm == 2 ? head_sum<G>(L.live ? mh : 0.0f) * inv : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; i++) e[i] = r * (k[i] - mh - n[i] * mn);
                 }
+                if (on) L.template store<ES>(y, to + h, e);
             }
         }
     }
@@ -358,27 +334,31 @@ __global__ __launch_bounds__(256) void qk_grad_sums_kernel(const float *__restri
     }
 }
 
-// How the rows' steps are dealt to waves: whole rows where there are enough of
-// them to fill the chip, parts of rows otherwise.
+// How the rows' steps are dealt to waves: at most `most` steps of a row each (as
+// evenly as they go), less where `waves` waves are not there yet.
 struct QkPlan {
     int sq, steps, per, parts;
     int64_t units;
 };
-static QkPlan qk_plan(const QkHeads &H, int64_t M, int heads_per_step, int64_t waves) {
+static QkPlan qk_plan(const QkHeads &H, int64_t M, int heads_per_step, int64_t waves, int most) {
     QkPlan p;
     p.sq = (H.nq + heads_per_step - 1) / heads_per_step;
     p.steps = p.sq + (H.nk + heads_per_step - 1) / heads_per_step;
     int64_t per = (M * p.steps + waves - 1) / waves;
+    if (per > most) per = most;
     if (per > p.steps) per = p.steps;
-    p.per = (int)(per < 1 ? 1 : per);
-    p.parts = p.steps ? (p.steps + p.per - 1) / p.per : 0;
+    if (per < 1) per = 1;
+    p.parts = (int)((p.steps + per - 1) / per);
+    p.per = p.parts ? (p.steps + p.parts - 1) / p.parts : 1;
     p.units = M * p.parts;
     return p;
 }
 
 template <int ES, int LAYOUT, int G>
 static hipError_t launch_qk_one(hipStream_t s, const QkTensors &T, const QkHeads &H, int64_t M, bool grad, float *part) {
-    const QkPlan p = qk_plan(H, M, 64 / G, 8192);
+    // 17776 rows of 4 + 4 steps: 2 / 3 / 4 / 8 steps a wave 72 / 65 / 61 / 66 us; the
+    // gradients' waves go on to other rows, and take whole ones
+    const QkPlan p = grad ? qk_plan(H, M, 64 / G, 8192, 1 << 30) : qk_plan(H, M, 64 / G, 32768, 4);
     if (!grad) {
         const int64_t groups = (p.units + 3) / 4;
         for (int64_t g = 0; g < groups; g += kMaxGroups) {  // long batches take several launches
