@@ -703,7 +703,7 @@ struct ColParams {
 // The heads of 128 columns (16 p + 8 lh .. of row lm a lane): a head of D columns is
 // NP = D / 16 eights of a lane and as many of its partner's in the other half, so
 // its sums are in the lane but for one exchange, and both members of a rotated
-// pair are the lane's own (halves: 2 P = D).  The results of 32 rows go out through
+// pair are the lane's own (2 P = D, or nothing is rotated).  The results of 32 rows go out through
 // the wave's bf16 band, whole rows a store: 64 bytes of 16 rows a store, straight
 // from registers, took 13 us more (17776 x 1920 x 5760).
 template <int D, bool PRE, class Get, class Cols>
@@ -714,22 +714,23 @@ __device__ __forceinline__ void linear_heads_out(Get &&get, Cols &&cols, const C
     const float inv = 1.0f / (float)D;
     const int h0 = (int)(col0 / D);
     uint8_t *mine_at = band + lm * EpiBand<2>::STRIDE + 16 * lh;
+    // The row's turns of the lane's pairs, two at a time: neighbours, 4 of each eight;
+    // halves, 8 of each eight of the first half.  They come a slice ahead.
+    float4 z[NP][2];
+    auto turns = [&](int i) __attribute__((always_inline)) {
+        if (PRE || H.P == 0 || h0 >= H.nq + H.nk) return;
+        const int64_t row = row0 + 32 * i + lm < M ? row0 + 32 * i + lm : M - 1;
+        const float2 *t = reinterpret_cast<const float2 *>(H.table) + row * H.P;
+#pragma unroll
+        for (int p = 0; p < NP; p++)
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+                z[p][e] = *reinterpret_cast<const float4 *>(
+                    t + (H.layout == 0 ? 8 * p + 4 * lh + 2 * e : 16 * (p >> 1) + 8 * lh + 4 * (p & 1) + 2 * e));
+    };
+    turns(0);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        // the row's turns of the lane's pairs, two at a time: neighbours, 4 of each eight;
-        // halves, 8 of each eight of the first half
-        float4 z[NP][2];
-        if (!PRE && H.P > 0 && h0 < H.nq + H.nk) {
-            const int64_t row = row0 + 32 * i + lm < M ? row0 + 32 * i + lm : M - 1;
-            const float2 *t = reinterpret_cast<const float2 *>(H.table) + row * H.P;
-#pragma unroll
-            for (int p = 0; p < NP; p++)
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const int k = H.layout == 0 ? 8 * p + 4 * lh + 2 * e : 16 * (p >> 1) + 8 * lh + 4 * (p & 1) + 2 * e;
-                    z[p][e] = *reinterpret_cast<const float4 *>(t + (k < H.P ? k : 0));
-                }
-        }
 #pragma unroll
         for (int hh = 0; hh < HEADS; hh++) {
             const bool mine = h0 + hh < H.nq + H.nk;  // wave-uniform
@@ -788,12 +789,11 @@ __device__ __forceinline__ void linear_heads_out(Get &&get, Cols &&cols, const C
                     for (int p = 0; p < NP; p++)
 #pragma unroll
                         for (int e = 0; e < 4; e++) {
-                            const bool on = 8 * p + 4 * lh + e < H.P;
                             const float4 f = z[p][e >> 1];
                             const float cs = e & 1 ? f.z : f.x, sn = e & 1 ? f.w : f.y;
                             const float a = x[p][2 * e], b = x[p][2 * e + 1];
-                            x[p][2 * e] = on ? a * cs - b * sn : a;
-                            x[p][2 * e + 1] = on ? b * cs + a * sn : b;
+                            x[p][2 * e] = a * cs - b * sn;
+                            x[p][2 * e + 1] = b * cs + a * sn;
                         }
                 } else {
 #pragma unroll
@@ -811,6 +811,7 @@ __device__ __forceinline__ void linear_heads_out(Get &&get, Cols &&cols, const C
 #pragma unroll
             for (int p = 0; p < NP; p++) out(p);
         }
+        if (i < 3) turns(i + 1);
         epi_band_to_global<2, 0, 32>(band, PRE ? L.pre : y, M, N, row0 + 32 * i, col0, 32 * lh + lm, true);
         __builtin_amdgcn_sched_barrier(0);  // one row's heads at a time
     }

@@ -127,12 +127,11 @@ struct LinearEpi {
     LoraEpi lora;
 };
 // Whether a QKV linear's heads are normed and rotated from registers
-// (gemm_common.hpp): heads of 64 or 128, whole 16-byte pieces of rows, no adapters,
-// and both members of every rotated pair, of which there is an even number, in a
-// lane (neighbours are, halves where they are the whole head).
+// (gemm_common.hpp): heads of 64 or 128, rotated whole or not at all, whole 16-byte
+// pieces of rows and no adapters.
 inline bool heads_from_regs(const LinearEpi &L, int64_t N) {
     return !L.lora.t && N % 8 == 0 && N <= (int64_t(1) << 22) && L.qk.D != 32 &&
-           L.qk.P % 2 == 0 && (L.qk.layout == 0 || L.qk.P == 0 || 2 * L.qk.P == L.qk.D);
+           (L.qk.P == 0 || 2 * L.qk.P == L.qk.D);
 }
 
 // epi: bit 0 GELU, bit 1 fused NVFP4 amax of the output into partial[tile]

@@ -386,10 +386,18 @@ __device__ __forceinline__ void grad_store(void *p, int64_t row, int64_t N, cons
     }
 }
 
+template <bool VEC>
 __device__ __forceinline__ void grad_sums(float *out, int64_t at, int64_t N, const int64_t (&cols)[8], const float (&v)[8]) {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < 8; i++)
-        if (cols[i] < N) out[at * N + cols[i]] = v[i];
+        for (int i = 0; i < 8; i += 4)
+            if (cols[i] < N)
+                *reinterpret_cast<float4 *>(out + at * N + cols[i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (cols[i] < N) out[at * N + cols[i]] = v[i];
+    }
 }
 
 template <int ES, bool VEC, int ACT>
@@ -427,11 +435,18 @@ __global__ __launch_bounds__(256) void linear_grad_kernel(LinearGrad G, int64_t 
             }
             float g[8], dg[8];
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                g[i] = 1.0f, dg[i] = 0.0f;
-                if (G.gate && cols[i] < N)
-                    g[i] = G.gate_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(G.gate)[s * N + cols[i]] << 16)
+            for (int i = 0; i < 8; i++) g[i] = 1.0f, dg[i] = 0.0f;
+            if (G.gate) {
+                if constexpr (VEC) {
+                    load_values<8>(G.gate, G.gate_bf16, s * N + cols[0], N - cols[0], g);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        if (cols[i] < N)
+                            g[i] = G.gate_bf16
+                                       ? __uint_as_float((uint32_t) static_cast<const uint16_t *>(G.gate)[s * N + cols[i]] << 16)
                                        : static_cast<const float *>(G.gate)[s * N + cols[i]];
+                }
             }
             typedef GradValues<ES, VEC> Row;
             auto one = [&](int64_t r, const Row &dy, const Row &pre) {
@@ -447,29 +462,26 @@ __global__ __launch_bounds__(256) void linear_grad_kernel(LinearGrad G, int64_t 
                 if (G.du) grad_store<ES, VEC>(G.du, r, N, cols, o);
             };
             constexpr int DEEP = lgrad::DEEP;
-            for (; row + DEEP <= end; row += DEEP) {
+            // rows past the request's end are loaded as its last one and left out
+            for (; row < end; row += DEEP) {
                 Row dy[DEEP], u[DEEP];
 #pragma unroll
-                for (int k = 0; k < DEEP; k++) dy[k].load(G.dy, row + k, N, cols);
+                for (int k = 0; k < DEEP; k++) dy[k].load(G.dy, row + k < end ? row + k : end - 1, N, cols);
                 if (G.pre) {
 #pragma unroll
-                    for (int k = 0; k < DEEP; k++) u[k].load(G.pre, row + k, N, cols);
+                    for (int k = 0; k < DEEP; k++) u[k].load(G.pre, row + k < end ? row + k : end - 1, N, cols);
                 } else {
 #pragma unroll
                     for (int k = 0; k < DEEP; k++) u[k] = Row();
                 }
 #pragma unroll
-                for (int k = 0; k < DEEP; k++) one(row + k, dy[k], u[k]);
+                for (int k = 0; k < DEEP; k++)
+                    if (row + k < end) one(row + k, dy[k], u[k]);
             }
-            for (; row < end; row++) {
-                Row dy, u = Row();
-                dy.load(G.dy, row, N, cols);
-                if (G.pre) u.load(G.pre, row, N, cols);
-                one(row, dy, u);
-            }
-            if (G.dgate) grad_sums(gate_part, chunk + s, N, cols, dg);
+            row = end;
+            if (G.dgate) grad_sums<VEC>(gate_part, chunk + s, N, cols, dg);
         }
-        if (G.dbias) grad_sums(bias_part, chunk, N, cols, db);
+        if (G.dbias) grad_sums<VEC>(bias_part, chunk, N, cols, db);
     }
 }
 

@@ -313,21 +313,21 @@ __global__ __launch_bounds__(256) void qk_grad_kernel(QkTensors T, QkHeads H, in
     }
 }
 
-// dwq, dbq, dwk, dbk [D] from the workgroups' sums: 16 columns and 16 parts of
+// dwq, dbq, dwk, dbk [D] from the workgroups' sums: 8 columns and 32 parts of
 // the workgroups a workgroup.
 __global__ __launch_bounds__(256) void qk_grad_sums_kernel(const float *__restrict__ part, int groups, int D, float *dwq,
                                                            float *dbq, float *dwk, float *dbk) {
-    __shared__ float red[16][16];
-    const int x = threadIdx.x & 15, k = threadIdx.x >> 4, e = blockIdx.x * 16 + x;
+    __shared__ float red[32][8];
+    const int x = threadIdx.x & 7, k = threadIdx.x >> 3, e = blockIdx.x * 8 + x;
     float sum = 0.0f;
     if (e < 4 * D)
 #pragma unroll 8
-        for (int g = k; g < groups; g += 16) sum += part[(int64_t)g * 4 * D + e];
+        for (int g = k; g < groups; g += 32) sum += part[(int64_t)g * 4 * D + e];
     red[k][x] = sum;
     __syncthreads();
     if (k == 0 && e < 4 * D) {
 #pragma unroll
-        for (int i = 1; i < 16; i++) sum += red[i][x];
+        for (int i = 1; i < 32; i++) sum += red[i][x];
         const int which = e / D, c = e - which * D;
         float *out = which == 0 ? dwq : which == 1 ? dbq : which == 2 ? dwk : dbk;
         if (out) out[c] = sum;
@@ -382,7 +382,7 @@ static hipError_t launch_qk_one(hipStream_t s, const QkTensors &T, const QkHeads
                        p.parts, part);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !part) return e;
-    hipLaunchKernelGGL(qk_grad_sums_kernel, dim3((4 * H.D + 15) / 16), dim3(256), 0, s, part, (int)groups, H.D, T.dwq, T.dbq,
+    hipLaunchKernelGGL(qk_grad_sums_kernel, dim3((4 * H.D + 7) / 8), dim3(256), 0, s, part, (int)groups, H.D, T.dwq, T.dbq,
                        T.dwk, T.dbk);
     return hipGetLastError();
 }
