@@ -113,12 +113,12 @@ struct MidI8 {
 };
 
 namespace lmid {
-// Tiles of 64 MI x 64 NI: KG groups of 4 waves, each with its own stages, and as
-// many stage buffers as fit a CU.
+// Tiles of 64 MI x 64 NI: groups of 4 waves, each with its own stages, and as many
+// stage buffers as fit a CU.
 template <int MI, int NI>
-constexpr int groups() { return 2; }
+constexpr int groups() { return MI * NI == 4 ? 1 : 2; }
 template <int MI, int NI>
-constexpr int bufs() { return MI * NI == 1 ? 4 : 3; }
+constexpr int bufs() { return MI * NI == 2 ? 3 : 4; }
 template <int MI, int NI>
 constexpr int stage() { return 64 * (MI + NI) * 128; }
 template <int MI, int NI>
@@ -288,15 +288,20 @@ __global__ __launch_bounds__((256 * lmid::groups<MI, NI>()), (lmid::groups<MI, N
     const int chunk = lane % LPR;
     const int64_t col = n0 + chunk * PER;
     const bool vec = ((N * ES) & 15) == 0;
-    // The epilogue's operands before the sums go through LDS: all rows' residual
-    // loads are on their way together, and each row's request is looked up once.
-    uint4 residual[ROWS / RPP];
+    // The epilogue's operands before the sums go through LDS: the residual of a group
+    // of steps is on its way together, a group ahead, and each row's request is
+    // looked up once.
+    constexpr int STEPS = ROWS / RPP, GROUP = STEPS < 4 ? STEPS : 4;
+    uint4 residual[GROUP];
+    auto ahead = [&](int q0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < ROWS / RPP; q++) {
-        const int64_t row = m0 + wave * ROWS + q * RPP + lane / LPR;
-        residual[q] = make_uint4(0, 0, 0, 0);
-        if (L.residual && row < M && col < N) residual[q] = fetch_raw<ES>(L.residual, row * N + col, N - col, vec);
-    }
+        for (int q = 0; q < GROUP; q++) {
+            const int64_t row = m0 + wave * ROWS + (q0 + q) * RPP + lane / LPR;
+            residual[q] = make_uint4(0, 0, 0, 0);
+            if (L.residual && row < M && col < N) residual[q] = fetch_raw<ES>(L.residual, row * N + col, N - col, vec);
+        }
+    };
+    ahead(0);
     LinearLane<PER> T0;
     T0.begin(L, m0, BM, M, N, col);
     int requests = 0;  // of the wave's rows, in its first ROWS lanes
@@ -328,30 +333,38 @@ __global__ __launch_bounds__((256 * lmid::groups<MI, NI>()), (lmid::groups<MI, N
     __syncthreads();
     constexpr int FORM = EPI | (OUT == 1 && (EPI & kEpiHeads) == 0 ? kEpiAmax : 0);
     float top = 0.0f;
+#pragma unroll 1
+    for (int q0 = 0; q0 < STEPS; q0 += GROUP) {
+        uint4 now[GROUP];
 #pragma unroll
-    for (int r0 = 0; r0 < ROWS; r0 += RPP) {
-        const int r = wave * ROWS + r0 + lane / LPR;
-        const int64_t row = m0 + r, mr = row < M ? row : M - 1;
-        T sum[PER];
+        for (int q = 0; q < GROUP; q++) now[q] = residual[q];
+        if (q0 + GROUP < STEPS) ahead(q0 + GROUP);
 #pragma unroll
-        for (int i = 0; i < PER; i += 4) {
+        for (int q = 0; q < GROUP; q++) {
+            const int r0 = (q0 + q) * RPP;
+            const int r = wave * ROWS + r0 + lane / LPR;
+            const int64_t row = m0 + r, mr = row < M ? row : M - 1;
+            T sum[PER];
 #pragma unroll
-            for (int k = 0; k < KG; k++) {
-                const uint4 u = *reinterpret_cast<const uint4 *>(lds + k * BAND + r * STRIDE + 4 * (PER * chunk + i));
-                const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+            for (int i = 0; i < PER; i += 4) {
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const T p = __builtin_bit_cast(T, d[e]);
-                    sum[i + e] = k == 0 ? p : sum[i + e] + p;
+                for (int k = 0; k < KG; k++) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(lds + k * BAND + r * STRIDE + 4 * (PER * chunk + i));
+                    const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const T p = __builtin_bit_cast(T, d[e]);
+                        sum[i + e] = k == 0 ? p : sum[i + e] + p;
+                    }
                 }
             }
+            float v[PER];
+            Op::template scale<PER>(op, mr, col, N, sum, v);
+            if constexpr ((EPI & kEpiLora) != 0) lora_row<PER>(L.lora, mr, col, N, v);
+            const int request = __shfl(requests, r0 + lane / LPR, 64);
+            top = fmaxf(top, linear_row_out<ES, FORM>(v, y, M, N, row, col, chunk, vec, request, L, T0, Q, amax != nullptr,
+                                                      &now[q]));
         }
-        float v[PER];
-        Op::template scale<PER>(op, mr, col, N, sum, v);
-        if constexpr ((EPI & kEpiLora) != 0) lora_row<PER>(L.lora, mr, col, N, v);
-        const int request = __shfl(requests, r0 + lane / LPR, 64);
-        top = fmaxf(top, linear_row_out<ES, FORM>(v, y, M, N, row, col, chunk, vec, request, L, T0, Q, amax != nullptr,
-                                                  &residual[r0 / RPP]));
     }
     mid_amax_max(amax, top, m0, n0, M);
 }
@@ -629,8 +642,11 @@ static hipError_t launch_mid_one(hipStream_t s, const typename Op::Arg &op, int6
     return hipGetLastError();
 }
 
-// The largest tile that gives (nearly) every CU one; NVFP4: 64 x 64, and 32 x 128
-// for heads of 128, which need a tile of their width.
+// A CU holds one tile at a time, and a round of 256 of them takes about (K = 1920,
+// us, BF16 / INT8) 9 / 6 with 64 x 64, 14.5 / 10 with 64 x 128 and 25 / 18 with 128 x 128: the
+// smallest as long as it is one round, 128 x 128 where it takes at most 4/7 of the
+// rounds of 64 x 128 (1693 x 1920 x 1920: 28.9 / 19.7 and 25.9 / 18.4).  NVFP4: 64 x 64, and 32 x
+// 128 for heads of 128, which need a tile of their width.
 template <class Op, int OUT, int EPI, bool TAIL>
 static hipError_t launch_mid_tail(hipStream_t s, const typename Op::Arg &op, int64_t M, int64_t N, int64_t K, void *y,
                                   const LinearEpi &L, float *amax) {
@@ -641,6 +657,9 @@ static hipError_t launch_mid_tail(hipStream_t s, const typename Op::Arg &op, int
         return launch_mid_one<Op, 2, 2, OUT, EPI, TAIL>(s, op, M, N, K, y, L, amax);
     } else {
         const int64_t m64 = (M + 63) / 64, n64 = (N + 63) / 64;
+        const int64_t wides = m64 * ((N + 127) / 128), larges = (M + 127) / 128 * ((N + 127) / 128);
+        if (!wide && (larges + 255) / 256 * 7 <= (wides + 255) / 256 * 4)
+            return launch_mid_one<Op, 2, 2, OUT, EPI, TAIL>(s, op, M, N, K, y, L, amax);
         if (m64 * n64 > 256 || wide) return launch_mid_one<Op, 1, 2, OUT, EPI, TAIL>(s, op, M, N, K, y, L, amax);
         return launch_mid_one<Op, 1, 1, OUT, EPI, TAIL>(s, op, M, N, K, y, L, amax);
     }
