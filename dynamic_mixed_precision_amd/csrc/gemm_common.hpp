@@ -288,13 +288,13 @@ __device__ __forceinline__ float epi_band_to_global(const uint8_t *band, void *y
 // lane holds of one row: v are the scaled sums (with the adapter term); bias, pre,
 // heads, activation, gate, residual, one rounding, store.  A lane has the same
 // columns in every row, so what depends on the column is loaded once (T, Q).
-// chunk: the lane's place in the row; request: of the row, for kGateMixed;
-// residual: the lane's 16 bytes of it, where they are loaded already.
+// chunk: the lane's place in the row; residual: the lane's 16 bytes of it, where
+// they are loaded already.
 // Returns the lane's part of the fused amax (kEpiAmax, where want_amax).  All lanes
 // of the wave call it together.
 template <int ESIZE, int EPI>
 __device__ __forceinline__ float linear_row_out(float (&v)[16 / ESIZE], void *y, int64_t M, int64_t N, int64_t row,
-                                                int64_t col, int chunk, bool vec, int request, const LinearEpi &L,
+                                                int64_t col, int chunk, bool vec, const LinearEpi &L,
                                                 const LinearLane<16 / ESIZE> &T, const QkLane<16 / ESIZE> &Q,
                                                 bool want_amax, const uint4 *residual = nullptr) {
     constexpr int PER = 16 / ESIZE;
@@ -306,7 +306,7 @@ __device__ __forceinline__ float linear_row_out(float (&v)[16 / ESIZE], void *y,
         Q.apply(L.qk, row < M ? row : M - 1, v);
     else
         act_apply<PER>(v, L.act);
-    T.template finish<ESIZE>(L, row, N, col, in, vec, request, v, residual);
+    T.template finish<ESIZE>(L, row, N, col, in, vec, v, residual);
     float m = 0.0f;
     if constexpr ((EPI & kEpiAmax) != 0) {
         static_assert(ESIZE == 2, "the fused amax reads bf16 outputs");
@@ -363,7 +363,7 @@ struct BandPlace {
 // pass it cost 30 us a tile.
 template <int ESIZE, int EPI, int ROWS, int ACT, bool MORE>
 __device__ __forceinline__ float linear_band_rows(const uint8_t *band, void *y, int64_t N, int64_t row0, int64_t col0, int lane,
-                                                  const LinearEpi &L, const LinearLane<16 / ESIZE> &T,
+                                                  const LinearEpi &L, LinearLane<16 / ESIZE> &T,
                                                   const BandPlace<ESIZE> &B, uint4 (&r)[4]) {
     typedef BandPlace<ESIZE> P;
     constexpr int PER = P::PER, LPR = P::LPR, RPP = P::RPP, GROUP = P::GROUP;
@@ -371,13 +371,9 @@ __device__ __forceinline__ float linear_band_rows(const uint8_t *band, void *y, 
     const uint8_t *src = band + lr * kLoraBandStride + 4 * PER * chunk;
     uint8_t *py = uniform_ptr(static_cast<uint8_t *>(y) + B.base), *pp = nullptr;
     if (MORE && L.pre) pp = uniform_ptr(static_cast<uint8_t *>(L.pre) + B.base);
-    float amax = 0.0f, gate[PER];
-    int requests = 0, held = -2;  // of the band's rows, in its first ROWS lanes; the one whose gate the lane has
-    if constexpr (MORE) {
-#pragma unroll
-        for (int i = 0; i < PER; i++) gate[i] = T.gate[i];
-        if (T.mode == kGateMixed) requests = request_of(L.gate_start, L.S, (int)(row0 + (lane < B.last ? lane : B.last)));
-    }
+    float amax = 0.0f;
+    int requests = 0;  // of the band's rows, in its first ROWS lanes
+    if (MORE && T.mode == kGateMixed) requests = request_of(L.gate_start, L.S, (int)(row0 + (lane < B.last ? lane : B.last)));
 #pragma unroll 1
     for (int g = 0; g < ROWS / RPP / GROUP; g++) {
         uint4 next[GROUP];
@@ -405,22 +401,15 @@ __device__ __forceinline__ float linear_band_rows(const uint8_t *band, void *y, 
             if (MORE && pp) store(pp);
             act_apply<PER>(v, ACT);
             if constexpr (MORE) {
-                if (T.mode == kGateMixed) {
-                    // the gate of the lane's row is loaded where a row's request is not the one before it
-                    const int s = __shfl(requests, (g * GROUP + k) * RPP + lr, 64);
-                    if (__any(s != held)) {
-                        held = s;
-                        if (s >= 0 && s < L.S && in) load_values<PER>(L.gate, L.gate_bf16, s * N + col0 + chunk * PER, PER, gate);
-                    }
-                }
+                if (T.mode == kGateMixed) T.turn(L, __shfl(requests, (g * GROUP + k) * RPP + lr, 64), N, col0 + chunk * PER);
                 if (T.mode == kGateOne) {
 #pragma unroll
-                    for (int i = 0; i < PER; i++) v[i] *= gate[i];
+                    for (int i = 0; i < PER; i++) v[i] *= T.gate[i];
                 } else if (T.mode != kGateNone) {
                     // rows of no request take no term at all, not zero times one
-                    const bool some = T.mode == kGateMixed && held >= 0 && held < L.S;
+                    const bool some = T.mode == kGateMixed && T.held >= 0 && T.held < L.S;
 #pragma unroll
-                    for (int i = 0; i < PER; i++) v[i] = some ? v[i] * gate[i] : L.residual ? -0.0f : 0.0f;
+                    for (int i = 0; i < PER; i++) v[i] = some ? v[i] * T.gate[i] : L.residual ? -0.0f : 0.0f;
                 }
                 if (L.residual) {
                     const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
@@ -449,7 +438,7 @@ __device__ __forceinline__ float linear_band_rows(const uint8_t *band, void *y, 
 template <int ESIZE, int EPI, int ROWS>
 __device__ __forceinline__ float linear_band_fast(const uint8_t *band, void *y, int64_t M, int64_t N, int64_t row0,
                                                   int64_t col0, int lane, const LinearEpi &L,
-                                                  const LinearLane<16 / ESIZE> &T, uint4 (&r)[4]) {
+                                                  LinearLane<16 / ESIZE> &T, uint4 (&r)[4]) {
     const bool more = L.pre || L.residual || T.mode != kGateNone;
     const BandPlace<ESIZE> B(M, N, row0, col0, lane, ROWS);
 #define DMPQ_ROWS(ACT_)                                                                                            \
@@ -474,7 +463,7 @@ __device__ __forceinline__ void linear_residual(const LinearEpi &L, int64_t M, i
 template <int ESIZE, int EPI, int ROWS>
 __device__ __forceinline__ float linear_band_out(const uint8_t *band, void *y, int64_t M, int64_t N, int64_t row0,
                                                  int64_t col0, int lane, bool vec, const LinearEpi &L,
-                                                 const LinearLane<16 / ESIZE> &T, const QkLane<16 / ESIZE> &Q,
+                                                 LinearLane<16 / ESIZE> &T, const QkLane<16 / ESIZE> &Q,
                                                  uint4 (&residual)[4]) {
     constexpr int PER = 16 / ESIZE, LPR = 128 / PER, RPP = 64 / LPR;
     const int chunk = lane % LPR;
@@ -496,8 +485,8 @@ __device__ __forceinline__ float linear_band_out(const uint8_t *band, void *y, i
             const float4 a = *reinterpret_cast<const float4 *>(band + r * kLoraBandStride + (chunk * PER + i) * 4);
             v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
         }
-        const int mine = T.mode == kGateMixed ? __shfl(request, r, 64) : 0;
-        amax = fmaxf(amax, linear_row_out<ESIZE, EPI>(v, y, M, N, row0 + r, col, chunk, vec, mine, L, T, Q, true));
+        T.turn(L, __shfl(request, r, 64), N, col);
+        amax = fmaxf(amax, linear_row_out<ESIZE, EPI>(v, y, M, N, row0 + r, col, chunk, vec, L, T, Q, true));
     }
     return amax;
 }

@@ -223,13 +223,12 @@ __global__ __launch_bounds__(64 * skinny::WAVES) void skinny_kernel(typename Op:
             act_apply<4>(v, L.act);
         }
         LinearLane<4> G;
-        int request = 0;
-        G.mode = kGateNone;
+        G.mode = kGateNone, G.held = -2;
         if (L.gate) {
             G.mode = kGateMixed;
-            if (L.gate_start) request = request_of(L.gate_start, L.S, (int)mr);
+            G.turn(L, L.gate_start ? request_of(L.gate_start, L.S, (int)mr) : 0, N, col);
         }
-        G.template finish<ES>(L, row, N, col, in, vec, request, v);
+        G.template finish<ES>(L, row, N, col, in, vec, v);
         if (in) store_values<ES, 4>(y, row * N + col, N - col, vec, v);
     }
 }

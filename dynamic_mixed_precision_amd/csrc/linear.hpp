@@ -329,13 +329,14 @@ template <int N>
 struct LinearLane {
     float bias[N], gate[N];
     int mode;  // wave-uniform
+    int held;  // kGateMixed: the request whose gate the lane has
 
     // rows row0 .. row0 + rows - 1 (those below M count)
     __device__ __forceinline__ void begin(const LinearEpi &L, int64_t row0, int rows, int64_t M, int64_t N_, int64_t col) {
 #pragma unroll
         for (int i = 0; i < N; i++) bias[i] = 0.0f, gate[i] = 1.0f;
         if (L.bias) load_values<N>(L.bias, L.bias_bf16, col, N_ - col, bias);
-        mode = kGateNone;
+        mode = kGateNone, held = -2;
         if (L.gate) {
             int a = 0, b = 0;
             if (L.gate_start) {
@@ -347,25 +348,26 @@ struct LinearLane {
             if (mode == kGateOne) load_values<N>(L.gate, L.gate_bf16, a * N_ + col, N_ - col, gate);
         }
     }
-    // gate and residual of one row: v becomes y.  in: the lane has columns there;
-    // request: of the row, for kGateMixed; ahead: its residual, where it is loaded already.
+    // On to a row of that request (kGateMixed): its gate is loaded where it is not the
+    // one that the lane has.
+    __device__ __forceinline__ void turn(const LinearEpi &L, int request, int64_t N_, int64_t col) {
+        if (mode != kGateMixed || request == held) return;
+        held = request;
+        if (request >= 0 && request < L.S) load_values<N>(L.gate, L.gate_bf16, request * N_ + col, N_ - col, gate);
+    }
+    // gate (of the row's request, turn) and residual of one row: v becomes y.  in: the
+    // lane has columns there; ahead: its residual, where it is loaded already.
     template <int ESIZE>
     __device__ __forceinline__ void finish(const LinearEpi &L, int64_t row, int64_t N_, int64_t col, bool in, bool vec,
-                                           int request, float (&v)[N], const uint4 *ahead = nullptr) const {
+                                           float (&v)[N], const uint4 *ahead = nullptr) const {
         if (mode == kGateOne) {
 #pragma unroll
             for (int i = 0; i < N; i++) v[i] *= gate[i];
         } else if (mode != kGateNone) {
             // rows of no request take no term at all, not zero times one
-            const bool some = mode == kGateMixed && request >= 0 && request < L.S;
-            if (some && in) {
-                float g[N];
-                load_values<N>(L.gate, L.gate_bf16, request * N_ + col, N_ - col, g);
+            const bool some = mode == kGateMixed && held >= 0 && held < L.S;
 #pragma unroll
-                for (int i = 0; i < N; i++) v[i] *= g[i];
-            }
-#pragma unroll
-            for (int i = 0; i < N; i++) v[i] = some ? v[i] : L.residual ? -0.0f : 0.0f;
+            for (int i = 0; i < N; i++) v[i] = some ? v[i] * gate[i] : L.residual ? -0.0f : 0.0f;
         }
         if (L.residual && in) {
             float r[N];

@@ -361,8 +361,8 @@ __global__ __launch_bounds__((256 * lmid::groups<MI, NI>()), (lmid::groups<MI, N
             float v[PER];
             Op::template scale<PER>(op, mr, col, N, sum, v);
             if constexpr ((EPI & kEpiLora) != 0) lora_row<PER>(L.lora, mr, col, N, v);
-            const int request = __shfl(requests, r0 + lane / LPR, 64);
-            top = fmaxf(top, linear_row_out<ES, FORM>(v, y, M, N, row, col, chunk, vec, request, L, T0, Q, amax != nullptr,
+            T0.turn(L, __shfl(requests, r0 + lane / LPR, 64), N, col);
+            top = fmaxf(top, linear_row_out<ES, FORM>(v, y, M, N, row, col, chunk, vec, L, T0, Q, amax != nullptr,
                                                       &now[q]));
         }
     }
@@ -606,8 +606,8 @@ __global__ __launch_bounds__(64 * lmid::WAVES, 2) void linear_codes_kernel(typen
         float v[PER];
         Op::template scale<PER>(op, mr, col, N, sum, v);
         if constexpr ((EPI & kEpiLora) != 0) lora_row<PER>(L.lora, mr, col, N, v);
-        const int request = P.mode == kGateMixed ? request_of(L.gate_start, L.S, (int)mr) : 0;
-        top = fmaxf(top, linear_row_out<ES, FORM>(v, y, M, N, row, col, chunk, vec, request, L, P, Q, amax != nullptr,
+        if (P.mode == kGateMixed) P.turn(L, request_of(L.gate_start, L.S, (int)mr), N, col);
+        top = fmaxf(top, linear_row_out<ES, FORM>(v, y, M, N, row, col, chunk, vec, L, P, Q, amax != nullptr,
                                                   &residual[r0 / (RPP * WAVES)]));
     }
     mid_amax_max(amax, top, m0, n0, M);
