@@ -361,9 +361,10 @@ static hipError_t launch_qk_one(hipStream_t s, const QkTensors &T, const QkHeads
     const QkPlan p = grad ? qk_plan(H, M, 64 / G, 8192, 1 << 30) : qk_plan(H, M, 64 / G, 32768, 4);
     if (!grad) {
         const int64_t groups = (p.units + 3) / 4;
-        for (int64_t g = 0; g < groups; g += kMaxGroups) {  // long batches take several launches
-            const int64_t n = groups - g < kMaxGroups ? groups - g : kMaxGroups;
-            // a launch's first unit is the first of a row
+        // long batches take several launches, each of which begins with the first unit of a row
+        const int64_t most = kMaxGroups / p.parts * p.parts;
+        for (int64_t g = 0; g < groups; g += most) {
+            const int64_t n = groups - g < most ? groups - g : most;
             QkTensors t = T;
             QkHeads h = H;
             const int64_t rows = g * 4 / p.parts, es = ES;
