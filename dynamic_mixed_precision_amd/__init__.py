@@ -821,9 +821,7 @@ def linear_epilogue(bias=None, act: int = ACT_NONE, gate=None, gate_start=None, 
     if gate is not None:
         if gate.dim() != 2:
             raise ValueError(f"gate has shape {tuple(gate.shape)}, needs (requests, N)")
-        rows = gate.shape[0]
-        if gate_start is not None:
-            _need_type(gate_start, "gate_start", 4 * (rows + 1), "int32")
+        rows = _gate_rows(gate, gate_start)
     elif gate_start is not None:
         raise ValueError("gate is missing")
     lora = None
@@ -836,6 +834,15 @@ def linear_epilogue(bias=None, act: int = ACT_NONE, gate=None, gate_start=None, 
         EPI_NVFP4_AMAX if amax else 0, None if heads is None else C.pointer(heads.struct),
         None if lora is None else C.pointer(lora))
     return LinearEpilogue(st, bias, gate, gate_start, residual, pre, heads, adapters, lora)
+
+
+def _gate_rows(gate, gate_start) -> int:
+    rows = gate.shape[0]
+    if gate_start is not None:
+        _need_type(gate_start, "gate_start", 4 * (rows + 1), "int32")
+    elif rows == 0:  # an empty tensor has no address: the library would see no gate
+        raise ValueError("a gate of 0 rows needs gate_start")
+    return rows
 
 
 def _pool_n(b) -> int:
@@ -913,9 +920,7 @@ def linear_epilogue_backward(dy, pre, du, ws=None, act: int = ACT_NONE, gate=Non
     if gate is not None:
         if gate.dim() != 2 or gate.shape[1] != N:
             raise ValueError(f"gate has shape {tuple(gate.shape)}, needs (requests, {N})")
-        rows = gate.shape[0]
-        if gate_start is not None:
-            _need_type(gate_start, "gate_start", 4 * (rows + 1), "int32")
+        rows = _gate_rows(gate, gate_start)
         if dgate is not None:
             _need_type(dgate, "dgate", 4 * rows * N, "fp32")
     elif gate_start is not None or dgate is not None:

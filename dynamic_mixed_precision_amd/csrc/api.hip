@@ -738,6 +738,10 @@ static dmpq_status check_heads(const char *fn, const dmpq_qk_heads *h, int64_t M
     return DMPQ_OK;
 }
 
+// A gate of no requests may be NULL and still leaves every row without one: the
+// kernels look at whether there is a gate, and read none of its rows then.
+static const void *gate_or_start(const void *gate, const int32_t *gate_start) { return gate ? gate : gate_start; }
+
 // The epilogue of a *_linear GEMM, after check_gemm.
 static dmpq_status check_linear(const char *fn, const dmpq_linear_epilogue *e, int64_t M, int64_t N, int64_t K,
                                 const void *y, int out_dtype, const void *ws, size_t ws_bytes, LinearEpi *out) {
@@ -762,7 +766,8 @@ static dmpq_status check_linear(const char *fn, const dmpq_linear_epilogue *e, i
     REQUIRE_PTR_NF(fn, e->residual, 0);
     REQUIRE_PTR_NF(fn, e->pre, 0);
     *out = LinearEpi{};
-    out->bias = e->bias, out->gate = e->gate, out->residual = e->residual, out->gate_start = e->gate_start;
+    out->bias = e->bias, out->gate = gate_or_start(e->gate, e->gate_start), out->residual = e->residual;
+    out->gate_start = e->gate_start;
     out->pre = e->pre, out->S = (int)e->gate_rows, out->act = e->act;
     out->bias_bf16 = e->bias_dtype == DMPQ_OUT_BF16, out->gate_bf16 = e->gate_dtype == DMPQ_OUT_BF16;
     if (e->heads) {
@@ -775,7 +780,7 @@ static dmpq_status check_linear(const char *fn, const dmpq_linear_epilogue *e, i
         if (((int64_t)h->n_q + h->n_k) * h->dim > N)
             return fail(DMPQ_ERR_BAD_SHAPE, "%s: %d + %d heads of %d exceed N = %lld", fn, h->n_q, h->n_k, h->dim,
                         (long long)N);
-        if (out_dtype != DMPQ_OUT_BF16 || e->act != DMPQ_ACT_NONE || e->gate || e->residual || e->flags)
+        if (out_dtype != DMPQ_OUT_BF16 || e->act != DMPQ_ACT_NONE || out->gate || e->residual || e->flags)
             return fail(DMPQ_ERR_UNSUPPORTED, "%s: heads go with DMPQ_OUT_BF16, bias, pre and adapters only", fn);
     }
     if (e->lora) {
@@ -914,7 +919,7 @@ dmpq_status dmpq_linear_epilogue_backward(hipStream_t stream, const void *dy, co
         return fail(DMPQ_ERR_INVALID_ARG, "%s: unknown activation %d", __func__, act);
     if (gate && !float_type(gate_dtype))
         return fail(DMPQ_ERR_INVALID_ARG, "%s: gate_dtype %d is not F32 or BF16", __func__, gate_dtype);
-    if ((gate_rows > 0 || dgate) && !gate) return fail(DMPQ_ERR_INVALID_ARG, "%s: gate is NULL", __func__);
+    if ((gate_rows > 0 || (dgate && !gate_start)) && !gate) return fail(DMPQ_ERR_INVALID_ARG, "%s: gate is NULL", __func__);
     if (gate && !gate_start && gate_rows != 1)
         return fail(DMPQ_ERR_BAD_SHAPE, "%s: a gate of %lld rows needs gate_start", __func__, (long long)gate_rows);
     REQUIRE_PTR_N(dy, M * N);
@@ -932,7 +937,7 @@ dmpq_status dmpq_linear_epilogue_backward(hipStream_t stream, const void *dy, co
         if (ws_bytes < need)
             return fail(DMPQ_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", __func__, ws_bytes, need);
     }
-    const LinearGrad G{dy, pre, gate, gate ? gate_start : nullptr, du, dgate, dbias, (int)gate_rows, act,
+    const LinearGrad G{dy, pre, gate_or_start(gate, gate_start), gate_start, du, dgate, dbias, (int)gate_rows, act,
                        gate_dtype == DMPQ_OUT_BF16};
     return hip_status(launch_linear_grad(stream, G, M, N, dtype, ws), __func__);
 }

@@ -563,8 +563,9 @@ dmpq_status dmpq_adamw_step(hipStream_t stream, const void *d_table, int64_t n_t
  * for the request s with gate_start[s] <= m < gate_start[s+1] (int32
  * [gate_rows + 1], ascending, on the device); rows of no request get no gated
  * term: y is the residual bit for bit there, or 0.  gate_start NULL: the gate
- * has one row, for all rows.  Boundaries that do not ascend give unspecified
- * results, and no access out of bounds.
+ * has one row, for all rows.  gate_start with gate_rows 0: no row has a request
+ * (gate may be NULL).  Boundaries that do not ascend give unspecified results,
+ * and no access out of bounds.
  * Activations: GELU is v Phi(v), GELU_TANH v/2 (1 + tanh(sqrt(2/pi) (v +
  * 0.044715 v^3))), SILU v / (1 + e^-v).  At -infinity they give NaN.
  * heads: the first n_q * dim columns of y are the heads of q, the next n_k * dim
