@@ -753,7 +753,7 @@ static dmpq_status check_linear(const char *fn, const dmpq_linear_epilogue *e, i
         return fail(DMPQ_ERR_INVALID_ARG, "%s: bias_dtype %d or gate_dtype %d is not F32 or BF16", fn, e->bias_dtype,
                     e->gate_dtype);
     if (e->gate_rows < 0) return fail(DMPQ_ERR_BAD_SHAPE, "%s: gate_rows = %lld < 0", fn, (long long)e->gate_rows);
-    if (e->gate_rows > 0 && !e->gate) return fail(DMPQ_ERR_INVALID_ARG, "%s: gate is NULL", fn);
+    if (e->gate_rows > 0 && N > 0 && !e->gate) return fail(DMPQ_ERR_INVALID_ARG, "%s: gate is NULL", fn);
     if (e->gate && !e->gate_start && e->gate_rows != 1)
         return fail(DMPQ_ERR_BAD_SHAPE, "%s: a gate of %lld rows needs gate_start", fn, (long long)e->gate_rows);
     if (M > INT32_MAX / 2 || e->gate_rows > INT32_MAX / 4)
@@ -919,7 +919,8 @@ dmpq_status dmpq_linear_epilogue_backward(hipStream_t stream, const void *dy, co
         return fail(DMPQ_ERR_INVALID_ARG, "%s: unknown activation %d", __func__, act);
     if (gate && !float_type(gate_dtype))
         return fail(DMPQ_ERR_INVALID_ARG, "%s: gate_dtype %d is not F32 or BF16", __func__, gate_dtype);
-    if ((gate_rows > 0 || (dgate && !gate_start)) && !gate) return fail(DMPQ_ERR_INVALID_ARG, "%s: gate is NULL", __func__);
+    if ((gate_rows > 0 || (dgate && !gate_start)) && N > 0 && !gate)
+        return fail(DMPQ_ERR_INVALID_ARG, "%s: gate is NULL", __func__);
     if (gate && !gate_start && gate_rows != 1)
         return fail(DMPQ_ERR_BAD_SHAPE, "%s: a gate of %lld rows needs gate_start", __func__, (long long)gate_rows);
     REQUIRE_PTR_N(dy, M * N);

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import dynamic_mixed_precision_amd as dm
-from test_linear_qk_abi import GEMMS, P, PLAIN, epilogue, gemm, heads_of, refused
+from test_linear_qk_abi import GEMMS, P, PLAIN, backward, epilogue, gemm, heads_of, refused
 
 
 def test_gate_without_rows_needs_gate_start():
@@ -19,3 +19,16 @@ def test_gate_without_rows_and_heads():
     """It is a gate to the checks, too."""
     for name, ops in GEMMS:
         refused(4, name, *gemm(ops, epilogue(heads_of(), **{**PLAIN, "gate_start": P})))
+
+
+@pytest.mark.parametrize("name,ops", GEMMS)
+def test_no_columns(name, ops):
+    """N = 0: w, y, bias, gate, residual and pre have no elements, and no addresses."""
+    args = list(gemm(ops, epilogue(bias=None, gate=None, residual=None, pre=None), N=0, y=None))
+    args[{2: 2, 4: 3, 6: 4}[ops]] = None  # w
+    assert getattr(dm.lib(), name)(*args) == 0, dm.last_error()
+
+
+def test_no_columns_backward():
+    assert dm.lib().dmpq_linear_epilogue_backward(
+        *backward(N=0, dy=None, pre=None, gate=None, du=None, dgate=None, dbias=None, ws=None, bytes=0)) == 0, dm.last_error()
