@@ -788,7 +788,7 @@ static dmpq_status check_linear(const char *fn, const dmpq_linear_epilogue *e, i
         if (dmpq_status s = check_lora(fn, M, N, K, l->R, l->S, l->n_adapters, l->rank, l->scale, true, l->seg_start,
                                        l->seg_adapter, &out->lora.batch))
             return s;
-        REQUIRE_PTR_NF(fn, l->t, 1);
+        REQUIRE_PTR_NF(fn, l->t, M);
         REQUIRE_PTR_NF(fn, l->b, l->n_adapters * N);
         out->lora.t = l->t, out->lora.b = l->b;
     }

@@ -32,3 +32,10 @@ def test_no_columns(name, ops):
 def test_no_columns_backward():
     assert dm.lib().dmpq_linear_epilogue_backward(
         *backward(N=0, dy=None, pre=None, gate=None, du=None, dgate=None, dbias=None, ws=None, bytes=0)) == 0, dm.last_error()
+
+
+@pytest.mark.parametrize("name,ops", GEMMS)
+def test_no_rows_with_adapters(name, ops):
+    """M = 0: x, t, y, residual and pre have no elements, and no addresses."""
+    args = list(gemm(ops, epilogue(residual=None, pre=None, lora=dict(t=None)), M=0, y=None, first=None))
+    assert getattr(dm.lib(), name)(*args) == 0, dm.last_error()
