@@ -3,6 +3,7 @@
 // bookkeeping, and dispatch to the gfx950 kernels.
 #include "dmpq.h"
 #include "internal.hpp"
+#include "linear_plan.hpp"
 
 #include <math.h>
 #include <stdarg.h>
@@ -795,26 +796,6 @@ static dmpq_status check_linear(const char *fn, const dmpq_linear_epilogue *e, i
     return check_epilogue(fn, M, N, out_dtype, 3, e->flags, ws, ws_bytes);
 }
 
-// Which kernels a whole linear takes.  bytes: of a value of K as the MFMA takes
-// it (bf16, and NVFP4 as fp16: 2).
-// kPathFew reads the weight once over the whole chip, 16 columns a workgroup: up
-// to 16 rows, and more while the product is small (us, few / mid, bf16: 16 x 1920 x
-// 1920 6.5 / 9.1, 32 rows 8.2 / 9.1, 64 rows 11.9 / 9.3; 226 x 600 x 688 5.2 / 8.5).
-// kPathMid has tiles of 64 and 128, for products whose 256 x 256 tiles leave much
-// of the chip idle.  Those take about the same for any number of them up to 256,
-// and K long enough to be split shortens it (us, mid / tiles: bf16 900 x 1920 x 1920
-// 16 / 39, 900 x 5760 x 1920 43 / 46, 900 x 7680 x 1920 56 / 51, 900 x 1920 x 7680 46 / 52,
-// 1700 x 1920 x 7680 93 / 71; INT8 900 x 7680 x 1920 38 / 38, 1700 x 1920 x 7680 52 / 51;
-// NVFP4 450 x 7680 x 1920 40 / 42, 900 x 5760 x 1920 57 / 48, 900 x 1920 x 7680 71 / 53).
-// The fused amax comes from tiles.
-enum LinearPath { kPathFew, kPathMid, kPathTiles };
-static LinearPath linear_path(const dmpq_linear_epilogue *e, int64_t M, int64_t N, int64_t K, int bytes, int most_short,
-                              int most_long) {
-    if (!e->flags && N <= kMaxFewWidth && M <= kMaxFewRows &&
-        (M <= 16 || (M + 15) / 16 * 16 * N <= (int64_t(1) << 28) / (K * bytes)))
-        return kPathFew;
-    return gemm_tiles(M, N) <= (K < 4096 ? most_short : most_long) ? kPathMid : kPathTiles;
-}
 static hipError_t mid_amax(hipStream_t s, const dmpq_linear_epilogue *e, int64_t M, int64_t N, void *ws, float **amax) {
     *amax = e->flags ? static_cast<float *>(ws) : nullptr;
     return e->flags ? launch_zero(s, *amax, gemm_tiles(M, N)) : hipSuccess;
@@ -831,7 +812,7 @@ dmpq_status dmpq_gemm_bf16_linear(hipStream_t stream, const uint16_t *x, const u
     if (M == 0 || N == 0) return ok();
     hipError_t e;
     float *amax;
-    switch (linear_path(h_epilogue, M, N, K, 2, 92, 40)) {
+    switch (linear_path(kLinearBF16, h_epilogue->flags != 0, M, N, K)) {
         case kPathFew: e = launch_few_bf16(stream, x, w, M, N, K, out_dtype, y, lin); break;
         case kPathMid:
             e = mid_amax(stream, h_epilogue, M, N, ws, &amax);
@@ -857,7 +838,7 @@ dmpq_status dmpq_qgemm_int8_linear(hipStream_t stream, const int8_t *qa, const f
     if (M == 0 || N == 0) return ok();
     hipError_t e;
     float *amax;
-    switch (linear_path(h_epilogue, M, N, K, 1, 120, 56)) {
+    switch (linear_path(kLinearInt8, h_epilogue->flags != 0, M, N, K)) {
         case kPathFew: e = launch_few_int8(stream, qa, sa, qw, sw, M, N, K, out_dtype, y, lin); break;
         case kPathMid:
             e = mid_amax(stream, h_epilogue, M, N, ws, &amax);
@@ -886,7 +867,7 @@ dmpq_status dmpq_qgemm_nvfp4_linear(hipStream_t stream, const uint8_t *ca, const
     if (M == 0 || N == 0) return ok();
     hipError_t e;
     float *amax;
-    switch (linear_path(h_epilogue, M, N, K, 2, 60, 24)) {
+    switch (linear_path(kLinearNVFP4, h_epilogue->flags != 0, M, N, K)) {
         case kPathFew: e = launch_few_nvfp4(stream, ca, sa, d_ga, cw, sw, d_gw, M, N, K, out_dtype, y, lin); break;
         case kPathMid:
             e = mid_amax(stream, h_epilogue, M, N, ws, &amax);
@@ -897,6 +878,14 @@ dmpq_status dmpq_qgemm_nvfp4_linear(hipStream_t stream, const uint8_t *ca, const
                                         static_cast<float *>(ws), split_area(ws, ws_bytes, M, N), lin);
     }
     return hip_status(e, __func__);
+}
+
+// What the rules above choose, for their tests; not part of the ABI.  tile: rows and
+// columns of a middling product's tiles.
+extern "C" int dmpq_test_linear_path(int route, int amax, int head_dim, int64_t M, int64_t N, int64_t K, int *tile) {
+    const MidTile t = mid_tile((LinearRoute)route, head_dim == 128, M, N);
+    tile[0] = t.rows, tile[1] = t.cols;
+    return linear_path((LinearRoute)route, amax != 0, M, N, K);
 }
 
 size_t dmpq_linear_backward_bytes(int64_t M, int64_t N, int64_t gate_rows) {

@@ -12,13 +12,12 @@
 // waves' sums meet in LDS and are added in wave order, 16 bytes of y a lane.
 #pragma once
 
-#include <type_traits>
-
 #include "device.hpp"
 #include "gemm_common.hpp"
 #include "gemm_dma.hpp"
 #include "internal.hpp"
 #include "linear.hpp"
+#include "linear_plan.hpp"
 #include "lora.hpp"
 
 namespace dmpq {
@@ -77,6 +76,7 @@ __device__ __forceinline__ void mid_amax_max(float *amax, float top, int64_t m0,
 // ---- bf16 and int8: operands staged through LDS -------------------------------------
 
 struct MidBF16 {
+    static constexpr LinearRoute ROUTE = kLinearBF16;
     typedef v16f acc_t;
     struct Arg {
         const uint16_t *x, *w;
@@ -91,6 +91,7 @@ struct MidBF16 {
 };
 
 struct MidI8 {
+    static constexpr LinearRoute ROUTE = kLinearInt8;
     typedef v16i acc_t;
     struct Arg {
         const int8_t *x, *w;
@@ -442,6 +443,7 @@ struct MidCodes {
 };
 
 struct MidFP4 {
+    static constexpr LinearRoute ROUTE = kLinearNVFP4;
     typedef v16f acc_t;
     typedef MidCodes Row;
     struct Arg {
@@ -618,7 +620,7 @@ __global__ __launch_bounds__(64 * lmid::WAVES, 2) void linear_codes_kernel(typen
 template <class Op, int MI, int NI, int OUT, int EPI, bool TAIL>
 static hipError_t launch_mid_one(hipStream_t s, const typename Op::Arg &op, int64_t M, int64_t N, int64_t K, void *y,
                                  const LinearEpi &L, float *amax) {
-    constexpr bool CODES = std::is_same<Op, MidFP4>::value;
+    constexpr bool CODES = Op::ROUTE == kLinearNVFP4;
     constexpr int BM = (CODES ? 32 : 64) * MI, BN = (CODES ? 32 : 64) * NI;
     const int64_t tm = (M + BM - 1) / BM, tn = (N + BN - 1) / BN;
     const dim3 grid((unsigned)(tm * tn));
@@ -642,25 +644,18 @@ static hipError_t launch_mid_one(hipStream_t s, const typename Op::Arg &op, int6
     return hipGetLastError();
 }
 
-// A CU holds one tile at a time, and a round of 256 of them takes about (K = 1920,
-// us, BF16 / INT8) 9 / 6 with 64 x 64, 14.5 / 10 with 64 x 128 and 25 / 18 with 128 x 128: the
-// smallest as long as it is one round, 128 x 128 where it takes at most 4/7 of the
-// rounds of 64 x 128 (1693 x 1920 x 1920: 28.9 / 19.7 and 25.9 / 18.4).  NVFP4: 64 x 64, and 32 x
-// 128 for heads of 128, which need a tile of their width.
 template <class Op, int OUT, int EPI, bool TAIL>
 static hipError_t launch_mid_tail(hipStream_t s, const typename Op::Arg &op, int64_t M, int64_t N, int64_t K, void *y,
                                   const LinearEpi &L, float *amax) {
     const bool wide = (EPI & kEpiHeads) != 0 && L.qk.D == 128;
-    if constexpr (std::is_same<Op, MidFP4>::value) {
+    const MidTile t = mid_tile(Op::ROUTE, wide, M, N);
+    if constexpr (Op::ROUTE == kLinearNVFP4) {
         if constexpr ((EPI & kEpiHeads) != 0)
-            if (wide) return launch_mid_one<Op, 1, 4, OUT, EPI, TAIL>(s, op, M, N, K, y, L, amax);
+            if (t.rows == 32) return launch_mid_one<Op, 1, 4, OUT, EPI, TAIL>(s, op, M, N, K, y, L, amax);
         return launch_mid_one<Op, 2, 2, OUT, EPI, TAIL>(s, op, M, N, K, y, L, amax);
     } else {
-        const int64_t m64 = (M + 63) / 64, n64 = (N + 63) / 64;
-        const int64_t wides = m64 * ((N + 127) / 128), larges = (M + 127) / 128 * ((N + 127) / 128);
-        if (!wide && (larges + 255) / 256 * 7 <= (wides + 255) / 256 * 4)
-            return launch_mid_one<Op, 2, 2, OUT, EPI, TAIL>(s, op, M, N, K, y, L, amax);
-        if (m64 * n64 > 256 || wide) return launch_mid_one<Op, 1, 2, OUT, EPI, TAIL>(s, op, M, N, K, y, L, amax);
+        if (t.rows == 128) return launch_mid_one<Op, 2, 2, OUT, EPI, TAIL>(s, op, M, N, K, y, L, amax);
+        if (t.cols == 128) return launch_mid_one<Op, 1, 2, OUT, EPI, TAIL>(s, op, M, N, K, y, L, amax);
         return launch_mid_one<Op, 1, 1, OUT, EPI, TAIL>(s, op, M, N, K, y, L, amax);
     }
 }
