@@ -354,30 +354,45 @@ static QkPlan qk_plan(const QkHeads &H, int64_t M, int heads_per_step, int64_t w
     return p;
 }
 
+// The forward pass of a plan in launches of at most kMaxGroups workgroups, four units
+// each, every one of which begins with the first unit of a row: launch i has the rows
+// from `row` on and `units` units are left.  False: there is no such launch.
+struct QkLaunch {
+    int64_t row, units;
+    unsigned groups;
+};
+static bool qk_launch(const QkPlan &p, int64_t i, QkLaunch &l) {
+    const int64_t most = kMaxGroups / p.parts * p.parts, first = i * most, groups = (p.units + 3) / 4;
+    if (first >= groups) return false;
+    l.row = first * 4 / p.parts, l.units = p.units - first * 4;
+    l.groups = (unsigned)(groups - first < most ? groups - first : most);
+    return true;
+}
+
+// Waves and steps of the forward pass (17776 rows of 4 + 4 steps: 2 / 3 / 4 / 8 steps a
+// wave 72 / 65 / 61 / 66 us).
+static QkPlan qk_forward_plan(const QkHeads &H, int64_t M, int lanes) { return qk_plan(H, M, 64 / lanes, 32768, 4); }
+
 template <int ES, int LAYOUT, int G>
 static hipError_t launch_qk_one(hipStream_t s, const QkTensors &T, const QkHeads &H, int64_t M, bool grad, float *part) {
-    // 17776 rows of 4 + 4 steps: 2 / 3 / 4 / 8 steps a wave 72 / 65 / 61 / 66 us; the
-    // gradients' waves go on to other rows, and take whole ones
-    const QkPlan p = grad ? qk_plan(H, M, 64 / G, 8192, 1 << 30) : qk_plan(H, M, 64 / G, 32768, 4);
     if (!grad) {
-        const int64_t groups = (p.units + 3) / 4;
-        // long batches take several launches, each of which begins with the first unit of a row
-        const int64_t most = kMaxGroups / p.parts * p.parts;
-        for (int64_t g = 0; g < groups; g += most) {
-            const int64_t n = groups - g < most ? groups - g : most;
+        const QkPlan p = qk_forward_plan(H, M, G);
+        QkLaunch l;
+        for (int64_t i = 0; qk_launch(p, i, l); i++) {
             QkTensors t = T;
             QkHeads h = H;
-            const int64_t rows = g * 4 / p.parts, es = ES;
-            t.q = static_cast<const uint8_t *>(T.q) + rows * T.ldq * es;
-            t.k = static_cast<const uint8_t *>(T.k) + rows * T.ldk * es;
-            t.q_out = static_cast<uint8_t *>(T.q_out) + rows * T.ldq_out * es;
-            t.k_out = static_cast<uint8_t *>(T.k_out) + rows * T.ldk_out * es;
-            h.table = H.table + rows * H.P * 2;
-            hipLaunchKernelGGL((qk_kernel<ES, LAYOUT, G>), dim3((unsigned)n), dim3(256), 0, s, t, h, M, p.sq, p.steps, p.per,
-                               p.units - g * 4, p.parts);
+            t.q = static_cast<const uint8_t *>(T.q) + l.row * T.ldq * ES;
+            t.k = static_cast<const uint8_t *>(T.k) + l.row * T.ldk * ES;
+            t.q_out = static_cast<uint8_t *>(T.q_out) + l.row * T.ldq_out * ES;
+            t.k_out = static_cast<uint8_t *>(T.k_out) + l.row * T.ldk_out * ES;
+            h.table = H.table + l.row * H.P * 2;
+            hipLaunchKernelGGL((qk_kernel<ES, LAYOUT, G>), dim3(l.groups), dim3(256), 0, s, t, h, M, p.sq, p.steps, p.per,
+                               l.units, p.parts);
         }
         return hipGetLastError();
     }
+    // the gradients' waves go on to other rows, and take whole ones
+    const QkPlan p = qk_plan(H, M, 64 / G, 8192, 1 << 30);
     const unsigned groups = stride_grid(p.units, 4, kQkGroups);
     hipLaunchKernelGGL((qk_grad_kernel<ES, LAYOUT, G>), dim3(groups), dim3(256), 0, s, T, H, M, p.sq, p.steps, p.per, p.units,
                        p.parts, part);
@@ -386,6 +401,20 @@ static hipError_t launch_qk_one(hipStream_t s, const QkTensors &T, const QkHeads
     hipLaunchKernelGGL(qk_grad_sums_kernel, dim3((4 * H.D + 7) / 8), dim3(256), 0, s, part, (int)groups, H.D, T.dwq, T.dbq,
                        T.dwk, T.dbk);
     return hipGetLastError();
+}
+
+// Launch i of a forward pass, for the tests of the split; not part of the ABI.  out:
+// parts of a row, first row, units left, workgroups.
+extern "C" int dmpq_test_qk_launch(int64_t M, int n_q, int n_k, int dim, int64_t i, int64_t *out) {
+    QkHeads H{};
+    H.nq = n_q, H.nk = n_k, H.D = dim;
+    int lanes = 1;
+    while (8 * lanes < dim) lanes *= 2;
+    const QkPlan p = qk_forward_plan(H, M, lanes);
+    QkLaunch l;
+    if (!qk_launch(p, i, l)) return 0;
+    out[0] = p.parts, out[1] = l.row, out[2] = l.units, out[3] = l.groups;
+    return 1;
 }
 
 template <int ES, int LAYOUT>
