@@ -187,10 +187,8 @@ __device__ __forceinline__ float other_half(float v) {
 }
 
 // max |value| of the rotated 16-block whose elements 0..7 (lo) or 8..15 the
-// lane holds as bf16; the other half is its neighbour's (HALVES: the lane's in the
-// wave's other half).  Stages 1, 2, 4 in the lane, stage 8 across the pair, then
-// * 1/4: the quantizer's order.
-template <bool HALVES = false>
+// lane holds as bf16; the other half is its neighbour's.  Stages 1, 2, 4 in the
+// lane, stage 8 across the pair, then * 1/4: the quantizer's order.
 __device__ __forceinline__ float block16_amax(const uint4 &v, bool lo) {
     float f[8];
     f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
@@ -209,7 +207,7 @@ __device__ __forceinline__ float block16_amax(const uint4 &v, bool lo) {
     for (int i = 0; i < 8; i++) {
         // the partner lane's value: DPP quad_perm [1, 0, 3, 2] swaps
         // lanes 2k and 2k+1 inside the VALU (no LDS round trip)
-        const float o = HALVES ? other_half(f[i]) : dpp_f32<0xB1>(f[i]);
+        const float o = dpp_f32<0xB1>(f[i]);
         const float w = lo ? f[i] + o : o - f[i];
         m = fmaxf(m, __builtin_fabsf(w * 0.25f));
     }

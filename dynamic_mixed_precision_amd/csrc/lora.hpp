@@ -212,7 +212,7 @@ __device__ __forceinline__ v4f mfma16(const v4i &a, const v4i &b, const v4f &c) 
 // the products, as in the expand kernel, so that the two agree for every scale.
 //
 // Of one 32-row slice, run by one wave on its own (the fixup of split tiles):
-// v = scale * (t b^T) for 32 rows x 32 NJ columns in the GEMMs' accumulator
+// v = scale * (t b^T) for 32 rows x 128 columns in the GEMMs' accumulator
 // layout: lane l holds row l % 32 (`row`; past M: unspecified) and, in
 // v[j][4g + e], column n0 + 32 j + 8 g + 4 (l / 32) + e.  Rows without adapter or
 // of rank 0 get -0, which adds nothing to any number.  b's rows are the MFMA's
@@ -227,21 +227,20 @@ __device__ __forceinline__ void lora_t_frag(const float *tr, v4i (&tf)[kParts]) 
     split8(v, tf);
 }
 
-template <int NJ>
 __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_t n0, int64_t N, int lane,
-                                           v16f (&v)[NJ]) {
+                                           v16f (&v)[4]) {
     const LoraBatch &B = L.batch;
     const int lm = lane & 31, lh = lane >> 5;
     const int mine = row < B.M ? row_adapter(B, (int)row) : -1;
     const float *tr = L.t + (row < B.M ? row : B.M - 1) * B.R + 8 * lh;
-    const uint16_t *bl[NJ];  // the lane's row of b, of adapter 0
+    const uint16_t *bl[4];  // the lane's row of b, of adapter 0
 #pragma unroll
-    for (int j = 0; j < NJ; j++) {
+    for (int j = 0; j < 4; j++) {
         const int64_t n = n0 + 32 * j + lm;
         bl[j] = L.b + (n < N ? n : N - 1) * B.R + 8 * lh;
     }
 #pragma unroll
-    for (int j = 0; j < NJ; j++)
+    for (int j = 0; j < 4; j++)
 #pragma unroll
         for (int e = 0; e < 16; e++) v[j][e] = -0.0f;
     uint64_t todo = __ballot(mine >= 0);
@@ -259,7 +258,7 @@ __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_
                 v4i tf[kParts];
                 lora_t_frag(tr + c, tf);
 #pragma unroll
-                for (int j = 0; j < NJ; j++) {
+                for (int j = 0; j < 4; j++) {
                     v4i bf = *reinterpret_cast<const v4i *>(bl[j] + off + c);
                     if (c + 16 > rank) bf = keep8(bf, rank - c - 8 * lh);
                     const v4i fin = finite8(bf);
@@ -268,12 +267,12 @@ __device__ __forceinline__ void lora_slice(const LoraEpi &L, int64_t row, int64_
                 }
             }
 #pragma unroll
-            for (int j = 0; j < NJ; j++)
+            for (int j = 0; j < 4; j++)
 #pragma unroll
                 for (int e = 0; e < 16; e++) v[j][e] *= sc;
         } else {
 #pragma unroll
-            for (int j = 0; j < NJ; j++) {
+            for (int j = 0; j < 4; j++) {
                 v16f d;
 #pragma unroll
                 for (int e = 0; e < 16; e++) d[e] = 0.0f;
