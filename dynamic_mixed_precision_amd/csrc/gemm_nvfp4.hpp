@@ -746,8 +746,7 @@ static hipError_t launch_fp4_paths(hipStream_t s, const uint8_t *ca, const uint8
     using namespace fp4gemm;
     static const hipError_t attr = [] {
         hipError_t e = allow_lds(gemm_fp4_f16_kernel<OUT, EPI>, epi_lds<EPI>(2 * STAGE));
-        if constexpr ((EPI & kEpiLinear) == 0)
-            if (e == hipSuccess) e = allow_lds(gemm_fp4_fast_kernel<OUT, EPI>, epi_lds<EPI>(2 * STAGE));
+        if (e == hipSuccess) e = allow_lds(gemm_fp4_fast_kernel<OUT, EPI>, epi_lds<EPI>(2 * STAGE));
         if (e == hipSuccess) e = allow_lds(gemm_fp4_dma_kernel<OUT, EPI>, epi_lds<EPI>(fp4dma::LDS_BYTES));
         if (e == hipSuccess) e = allow_lds(gemm_fp4_split_kernel, fp4dma::LDS_BYTES);
         if (e == hipSuccess) e = allow_lds(gemm_fp4_dma_tail_kernel<OUT, EPI>, epi_lds<EPI>(fp4dma::LDS_BYTES));
@@ -764,13 +763,10 @@ static hipError_t launch_fp4_paths(hipStream_t s, const uint8_t *ca, const uint8
     if (K % 128 == 0 && K >= 384)
         return launch_fp4_dma<OUT, EPI, true>(s, gemm_fp4_dma_tail_kernel<OUT, EPI>, gemm_fp4_split_tail_kernel, ca,
                                               sa, ga, cw, sw, gw, M, N, K, y, partial, spart, utm, utn, ep);
-    // (the whole linear takes the form for any K: its smaller tiles have most of these)
-    if constexpr ((EPI & kEpiLinear) == 0) {
-        if (K % (4 * 16) == 0) {
-            hipLaunchKernelGGL((gemm_fp4_fast_kernel<OUT, EPI>), grid, block, epi_lds<EPI>(2 * STAGE), s, ca, sa, ga, cw,
-                               sw, gw, M, N, K, y, utm, utn, partial, ep);
-            return hipGetLastError();
-        }
+    if (K % (4 * 16) == 0) {
+        hipLaunchKernelGGL((gemm_fp4_fast_kernel<OUT, EPI>), grid, block, epi_lds<EPI>(2 * STAGE), s, ca, sa, ga, cw,
+                           sw, gw, M, N, K, y, utm, utn, partial, ep);
+        return hipGetLastError();
     }
     hipLaunchKernelGGL((gemm_fp4_f16_kernel<OUT, EPI>), grid, block, epi_lds<EPI>(2 * STAGE), s, ca, sa, ga, cw, sw, gw, M,
                        N, K, y, utm, utn, partial, ep);

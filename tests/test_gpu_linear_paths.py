@@ -9,7 +9,7 @@ import linear_ref as lr
 from gpu_util import require_gpu, say
 from linear_paths import ROUTES, path
 from linear_ref import D64, U, Product
-from test_gpu_linear import BF, FORMS, _normal, _run, test_amax as amax, test_qkv as qkv
+from test_gpu_linear import BF, FORMS, _adapters as adapters_of, _normal, _run, test_amax as amax, test_qkv as qkv
 
 pytestmark = pytest.mark.gpu
 
@@ -147,3 +147,47 @@ def test_rows_do_not_depend_on_the_path(route, shape, whole, some):
     v, err = p.value()
     tol = (err + (v.abs() + err + _normal(1, N).cuda().abs()) * 2 * U)[:m]
     assert bool(((a[:m].to(D64) - b.to(D64)).abs() <= 2 * tol).all())
+
+
+# K with a remainder of 64 and of 16 values beside whole stages of 128, on tiles and in the middling
+# kernels; P 32 fills the head (from registers on tiles), 24 does not (through bands)
+@pytest.mark.parametrize("adapters", [0, 32])
+@pytest.mark.parametrize("P", [32, 24])
+@pytest.mark.parametrize("K", [192, 336])
+@pytest.mark.parametrize("M,heads,extra", [(2900, 20, 328), (900, 10, 640)])
+@pytest.mark.parametrize("route", ROUTES)
+def test_qkv_of_remainders(route, M, heads, extra, K, P, adapters):
+    require_gpu()
+    D, N = 64, 2 * heads * 64 + extra
+    assert path(route, M, N, K) == ("tiles" if M == 2900 else "64x64" if route == "nvfp4" else "64x128")
+    say(f"qkv {route} {M} {N} {K} {P} {adapters}")
+    p = Product(route, M, N, K, seed=K)
+    v, err = p.value()
+    kw = {}
+    if adapters:
+        kw["adapters"], term, et = adapters_of(p, adapters, 3, 2, 11)
+        v, err = v + term, err + et + (v + term).abs() * U
+    bias, angle = _normal(8, N).to(BF).cuda(), _normal(7, M, P) * 3
+    v = v + bias.to(D64)
+    err = err + v.abs() * U
+    table = torch.stack([angle.cos(), angle.sin()], -1).cuda()
+    w = {k: _normal(i, D).to(BF).cuda() for i, k in enumerate(("wq", "bq", "wk", "bk"))}
+    h = dm.qk_heads(heads, heads, D, norm=dm.NORM_LAYER, eps=1e-5, table=table, **w)
+    pre, y = (torch.full((M, N), float("nan"), device="cuda", dtype=BF) for _ in range(2))
+    p.gemm(dm)(*p.x, *p.w, y, dm.linear_epilogue(bias=bias, heads=h, pre=pre, **kw), dm.new_workspace(dm.OP_GEMM, "cuda", M, N), dm.OUT_BF16)
+    torch.cuda.synchronize()
+    lr.close(pre, v, lr.rounded(v, err, True), "pre")
+    for i, name in enumerate(("q", "k")):
+        cols = slice(i * heads * D, (i + 1) * heads * D)
+        x, e = (t[:, cols].reshape(M, heads, D) for t in (v, err))
+        o, eo = lr.heads(x, e, 2, 1e-5, w["w" + name], w["b" + name], table, 0)
+        lr.close(y[:, cols].reshape(M, heads, D), o, lr.rounded(o, eo, True), name)
+    lr.close(y[:, 2 * heads * D :], v[:, 2 * heads * D :], lr.rounded(v, err, True)[:, 2 * heads * D :], "v")
+
+
+@pytest.mark.parametrize("form", [{}, dict(gate=1, adapters=32)])
+@pytest.mark.parametrize("K", [192, 336])
+@pytest.mark.parametrize("route", ROUTES)
+def test_amax_of_remainders(route, K, form):
+    say(f"amax {route} {K} {form}")
+    amax(route, 2900, 2896, K, form)
