@@ -516,8 +516,8 @@ __global__ __launch_bounds__(256) void linear_grad_sums_kernel(LinearGrad G, int
     }
 }
 
-// Rows of a chunk: about 4096 waves, at least 8 rows (a chunk's sums are
-// written and read again as fp32), M / 2^20 for the longest batches.
+// Rows of a chunk: about 4096 waves, and 8 rows at least, as far as M has them (a
+// chunk's sums are written and read again as fp32).
 static int grad_rows(int64_t M, int64_t N) {
     const int64_t blocks = (N + lgrad::COLS - 1) / lgrad::COLS;
     const int64_t r = (M * blocks + 4095) / 4096;

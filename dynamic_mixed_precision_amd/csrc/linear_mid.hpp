@@ -1,15 +1,26 @@
 // linear_mid.hpp -- the whole linear where 256 x 256 tiles are too few to fill
 // the chip (prompts, batches of short requests, narrow projections).
 //
-// Such products are bound by the latency of their loads, not by their rate, so
-// nothing waits but for its own operands: a workgroup of 8 waves takes a tile of
-// 64 x 64 (or 32 x 128), and each wave computes the whole of it over its own part
-// of K, stages of 128 bytes of every row, straight from memory into fragments of
-// 32 x 32 MFMAs: no LDS and no barrier in the loop, two stages in flight a wave.
-// (With the operands staged through LDS for four waves, a stage took 790 cycles
-// of waiting for 128 of MFMA: 1920 x 1920 in bf16 14.2 us at 128 rows.)  A lane's
-// 16-byte pieces of a stage are its rows' own, and x and w pair the same k.  The
-// waves' sums meet in LDS and are added in wave order, 16 bytes of y a lane.
+// BF16 and INT8 (linear_staged_kernel): tiles of 64 x 64, 64 x 128 and 128 x 128.
+// Groups of 4 waves bring stages of 128 bytes of every row into LDS by DMA, three or
+// four stages ahead, with a barrier a stage; two groups share K between them (one in
+// the 128 x 128 tile).  A round of 256 tiles costs a part that does not depend on K
+// (the first stages' loads, the epilogue) and one a stage: us, BF16 and INT8 alike,
+// 64 x 64 5.5 + 0.2, 64 x 128 6 + 0.33, 128 x 128 10 + 0.52 a stage (256 tiles, K 1920 and
+// 3840: BF16 11.5 / 17.2, 15.6 / 25, 25.1 / 41; INT8 8.2 / 11.1, 11.3 / 15.9, 18.5 / 26.3).
+// The 128 x 128 tile's four waves are one a SIMD, so nothing hides their waits.
+//
+// NVFP4 (linear_codes_kernel): 8 waves take a tile of 64 x 64 (or 32 x 128), and each
+// computes the whole of it over its own part of K, stages of 128 values of every row,
+// straight from memory into fragments of 32 x 32 MFMAs: no LDS and no barrier in the
+// loop, two stages in flight a wave (one with 32 x 128).  Every wave dequantizes both
+// operands for its part of K.  A lane's 16-byte pieces of a stage are its rows' own,
+// and x and w pair the same k.
+//
+// The groups' or waves' sums meet in LDS and are added in their order, 16 bytes of y
+// a lane.  An adapter's term is added row by row from b in memory (lora_row), at a
+// cost that grows with its rank: 900 x 1920 x 1920 BF16 13.7 us, with rank 16 / 64 / 128
+// 24 / 46 / 75.
 #pragma once
 
 #include "device.hpp"

@@ -10,14 +10,19 @@ namespace dmpq {
 enum LinearRoute { kLinearBF16, kLinearInt8, kLinearNVFP4 };
 
 // Which kernels a whole linear takes.
-// kPathFew reads the weight once over the whole chip, 16 columns a workgroup: up to 16 rows, and more while the product is small (us, few / mid, bf16: 16 x 1920 x
-// 1920 6.5 / 9.1, 32 rows 8.2 / 9.1, 64 rows 11.9 / 9.3; 226 x 600 x 688 5.2 / 8.5).
+// kPathFew reads the weight once over the whole chip, 16 columns a workgroup: up to
+// 16 rows, and more while the product is small (us, few / mid: BF16 16 x 1920 x 1920
+// 6.3 / 9.0, 32 rows 8.3 / 9.0, 64 rows 11.8 / 9.6, 16 x 7680 x 1920 10.4 / 9.9, 32 rows 13.9 /
+// 10.1, 226 x 608 x 688 5.0 / 7.9; INT8 64 x 1920 x 1920 7.7 / 7.2; NVFP4 11.1 / 10.3).
 // kPathMid has tiles of 64 and 128, for products whose 256 x 256 tiles leave much
 // of the chip idle.  Those take about the same for any number of them up to 256,
-// and K long enough to be split shortens it (us, mid / tiles: bf16 900 x 1920 x 1920
-// 16 / 39, 900 x 5760 x 1920 43 / 46, 900 x 7680 x 1920 56 / 51, 900 x 1920 x 7680 46 / 52,
-// 1700 x 1920 x 7680 93 / 71; INT8 900 x 7680 x 1920 38 / 38, 1700 x 1920 x 7680 52 / 51;
-// NVFP4 450 x 7680 x 1920 40 / 42, 900 x 5760 x 1920 57 / 48, 900 x 1920 x 7680 71 / 53).
+// and K long enough to be split shortens it (us, mid / tiles: BF16 900 x 1920 x 1920
+// 16 / 34, 900 x 5760 x 1920 40 / 42, 900 x 7680 x 1920 46 / 55, 2900 x 1920 x 1920 39 / 41,
+// 900 x 1920 x 7680 41 / 51, 1700 x 1920 x 7680 66 / 71; INT8 900 x 7680 x 1920 33 / 33,
+// 3400 x 1920 x 1920 33 / 34, 1700 x 1920 x 7680 40 / 48; NVFP4 450 x 7680 x 1920 40 / 40,
+// 2000 x 1920 x 1920 37 / 39, 900 x 5760 x 1920 55 / 44, 450 x 1920 x 7680 35 / 37, 900 x 1920 x
+// 7680 66 / 49).  BF16 900 x 7680 x 1920 and 1700 x 1920 x 7680 are beyond the limits, though
+// the middling kernels' 128 x 128 tiles are 15 and 7% faster there.
 // The fused amax comes from tiles.
 enum LinearPath { kPathFew, kPathMid, kPathTiles };
 inline LinearPath linear_path(LinearRoute route, bool amax, int64_t M, int64_t N, int64_t K) {
@@ -30,11 +35,13 @@ inline LinearPath linear_path(LinearRoute route, bool amax, int64_t M, int64_t N
     return gemm_tiles(M, N) <= most[route][K >= 4096] ? kPathMid : kPathTiles;
 }
 
-// The tiles of a middling product (wide: with heads of 128).  A CU holds one tile at a time, and a round of 256 of them takes about (K = 1920,
-// us, BF16 / INT8) 9 / 6 with 64 x 64, 14.5 / 10 with 64 x 128 and 25 / 18 with 128 x 128: the
-// smallest as long as it is one round, 128 x 128 where it takes at most 4/7 of the
-// rounds of 64 x 128 (1693 x 1920 x 1920: 28.9 / 19.7 and 25.9 / 18.4).  NVFP4: 64 x 64, and 32 x
-// 128 for heads of 128, which need a tile of their width.
+// The tiles of a middling product (wide: with heads of 128).  A CU holds one tile at a
+// time, and a full round of 256 of them takes (K = 1920, us, BF16 / INT8) 11.5 / 8.2 with
+// 64 x 64, 15.6 / 11.3 with 64 x 128 and 25 / 18.5 with 128 x 128:
+// the smallest as long as it is one round, 128 x 128 where it takes at most 4/7 of the
+// rounds of 64 x 128 (1693 x 1920 x 1920 BF16 64 x 128 27.6, 128 x 128 24.5; INT8 19.5 and
+// 18.0; 1700 x 1920 x 7680 81 and 66, 48 and 40).  NVFP4: 64 x 64, and 32 x 128 for heads of
+// 128, which need a tile of their width.
 struct MidTile {
     int rows, cols;
 };

@@ -19,9 +19,9 @@ namespace dmpq {
 // ---- rotations -----------------------------------------------------------------
 
 // (cos, sin) of pos[m, axis(p)] * freq[p].  The angle is made in 64 bits, as
-// turns: its distance to the nearest quarter turn keeps all of fp32's bits
-// however far the position is.  32 pairs of a long video (106306 rows): 27 MB
-// written.
+// turns, so that its distance to the nearest quarter turn is off by |angle| 2^-51
+// at most: less than half a step of fp32 at 1 up to angles of 2^27, and 10^-6 at
+// 2^31.  Writes 8 bytes a pair (17776 rows of 32: 4.5 MB in 5.5 us).
 __global__ __launch_bounds__(256) void rope_table_kernel(const void *__restrict__ pos, int pos_f32, RopeAxes ax,
                                                          const double *__restrict__ freq, int64_t M, int P,
                                                          float2 *__restrict__ table) {

@@ -589,7 +589,7 @@ enum { DMPQ_ROPE_PAIRS = 0, DMPQ_ROPE_HALVES = 1 };
  * w and b [dim] (w_dtype F32 or BF16), of q and of k; NULL: 1 and 0.  dim is a
  * multiple of 8, at most 256; rope_pairs 0 .. dim/2 (0: no rotation; halves: a
  * multiple of 4).  fp32 throughout: a head whose squares overflow gives 0 (NaN
- * where it is infinite). */
+ * where it is infinite), and squares below fp32's range count as 0. */
 typedef struct dmpq_qk_heads {
     int32_t n_q, n_k, dim;
     int32_t norm, layout, w_dtype;
