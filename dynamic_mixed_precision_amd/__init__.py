@@ -809,9 +809,9 @@ def linear_epilogue(bias=None, act: int = ACT_NONE, gate=None, gate_start=None, 
     """y = residual + gate[request of the row] * act(x w^T + adapters + bias).
 
     bias [N] and gate [S, N]: fp32 or bf16; gate_start int32 [S + 1]: the rows'
-    requests (None: the gate's one row is for all); residual and pre [M, N] of
-    y's type, pre receiving the value before heads and act; heads: a QkHeads,
-    for a QKV linear; adapters: (t, b, rank, scale, seg_start, seg_adapter) as
+    requests (None: the gate's one row is for all; S = 0: no row has one);
+    residual and pre [M, N] of y's type, pre receiving the value before heads and
+    act; heads: a QkHeads, for a QKV linear; adapters: (t, b, rank, scale, seg_start, seg_adapter) as
     the *_lora GEMMs take them; amax: leave the NVFP4 amax of y in the workspace
     (EPI_NVFP4_AMAX).  The object can be kept for further calls of the same
     shapes: it holds the tensors, which must not move."""

@@ -638,8 +638,9 @@ dmpq_status dmpq_qgemm_nvfp4_linear(hipStream_t stream, const uint8_t *ca, const
  *   dbias = sum of du, before its rounding, over all rows  [N] fp32
  * dy, pre and du are F32 or BF16, all three; du may be dy or pre.  du, dgate and
  * dbias may be NULL (not computed), pre where act is NONE and dgate NULL, gate
- * where there is none.  Sums are fp32 in a fixed order (the same bits on every
- * call).  N at most 2^26.  ws for dgate and dbias:
+ * where there is none (gate_start with gate_rows 0: no row has a request).  Sums
+ * are fp32 in a fixed order (the same bits on every call).  N at most 2^26.  ws
+ * for dgate and dbias:
  * dmpq_linear_backward_bytes(M, N, gate_rows) bytes (0: out of range). */
 size_t dmpq_linear_backward_bytes(int64_t M, int64_t N, int64_t gate_rows);
 dmpq_status dmpq_linear_epilogue_backward(hipStream_t stream, const void *dy, const void *pre, int64_t M, int64_t N,
